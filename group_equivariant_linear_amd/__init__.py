@@ -20,8 +20,10 @@ LIB_PATH = os.path.join(_PKG, "libeqlinear.so")
 
 EQL_OK, EQL_ERR_INVALID, EQL_ERR_UNSUPPORTED, EQL_ERR_HIP, EQL_ERR_NOMEM = range(5)
 EQL_F32, EQL_BF16, EQL_F16 = 0, 1, 2
-EQL_KIND_CN, EQL_KIND_D8 = 0, 1
-EQL_ACT_NONE, EQL_ACT_GELU = 0, 1
+EQL_KIND_CN, EQL_KIND_D8, EQL_KIND_ROTARY, EQL_KIND_MIXER, EQL_KIND_NORM = range(5)
+EQL_ACT_NONE, EQL_ACT_GELU, EQL_ACT_SILU = range(3)
+EQL_ROTARY_HALF, EQL_ROTARY_INTERLEAVED = 0, 1
+EQL_ROTARY_PLAIN, EQL_ROTARY_LINEAR, EQL_ROTARY_RAISED_BASE, EQL_ROTARY_BANDED = range(4)
 
 # Every entry point of include/eqlinear.h.
 ABI_FUNCTIONS = (
@@ -32,6 +34,9 @@ ABI_FUNCTIONS = (
     "eqlinear_backward_weight_workspace", "eqlinear_backward_weight", "eqlinear_forward_bias_act",
     "eqlinear_d8_bias_act", "eqlinear_d8_to_fourier", "eqlinear_d8_to_regular", "eqlinear_dihedral_plan",
     "eqlinear_backward_weight_noalloc", "eqlinear_d8_regular_forward",
+    "eqlinear_rotary_plan", "eqlinear_rotary", "eqlinear_mixer_plan", "eqlinear_linear_attention_workspace",
+    "eqlinear_linear_attention", "eqlinear_linear_attention_backward", "eqlinear_linear_attention_step",
+    "eqlinear_norm_plan", "eqlinear_group_norm_workspace", "eqlinear_group_norm", "eqlinear_group_norm_backward",
 )
 
 # Size of the library-held scratch array of eqlinear_backward_weight_noalloc.
@@ -58,6 +63,12 @@ class eqlinear_info(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class eqlinear_heads(ctypes.Structure):
+    """A tensor [T][heads][d][N] with the last two axes contiguous; strides in elements."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -74,6 +85,7 @@ def load_library(path: str | None = None):
         lib = ctypes.CDLL(p)
         vp, i32, i64, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int
         plan_p = ctypes.POINTER(ctypes.c_void_p)
+        hp, f32, f64 = ctypes.POINTER(eqlinear_heads), ctypes.c_float, ctypes.c_double
         sig = {
             "eqlinear_status_string": ([st], ctypes.c_char_p),
             "eqlinear_plan": ([plan_p, i32, i32, i32, i32], st),
@@ -98,6 +110,20 @@ def load_library(path: str | None = None):
             "eqlinear_d8_to_fourier": ([vp, vp, vp, i64, vp], st),
             "eqlinear_d8_regular_forward": ([vp, vp, vp, vp, i32, vp, i64, vp], st),
             "eqlinear_d8_to_regular": ([vp, vp, vp, i64, vp], st),
+            "eqlinear_rotary_plan": ([plan_p] + [i32] * 6 + [f64, i32] + [f64] * 5 + [i32], st),
+            "eqlinear_rotary": ([vp, hp, hp, vp, i32, hp, hp, i64, vp], st),
+            "eqlinear_mixer_plan": ([plan_p] + [i32] * 6, st),
+            "eqlinear_linear_attention_workspace": ([vp, i64, i64, i32], ctypes.c_size_t),
+            "eqlinear_linear_attention": ([vp, hp, hp, hp, vp, f32, vp, i64, vp, vp, hp, i64, vp, ctypes.c_size_t, vp],
+                                          st),
+            "eqlinear_linear_attention_backward": ([vp, hp, hp, hp, hp, vp, f32, vp, i64, vp, vp, hp, hp, hp, vp, i64,
+                                                    vp, ctypes.c_size_t, vp], st),
+            "eqlinear_linear_attention_step": ([vp, hp, hp, hp, vp, f32, vp, hp, i64, vp], st),
+            "eqlinear_norm_plan": ([plan_p] + [i32] * 4 + [f64, i32], st),
+            "eqlinear_group_norm_workspace": ([vp, i64, i64, i32], ctypes.c_size_t),
+            "eqlinear_group_norm": ([vp, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, ctypes.c_size_t, vp], st),
+            "eqlinear_group_norm_backward": ([vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp,
+                                              ctypes.c_size_t, vp], st),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -136,6 +162,10 @@ class Plan:
     @property
     def dtype(self):
         return self.info["dtype"]
+
+    @property
+    def torch_dtype(self):
+        return _torch_dtype(self)
 
 
 def eqlinear_plan(N: int, C_in: int, C_out: int, dtype: int) -> Plan:
@@ -398,6 +428,239 @@ def eqlinear_backward_weight_noalloc(plan: Plan, x, dy, dw, T: int | None = None
         raise EqlError(st, f"eqlinear_backward_weight_noalloc (workspace {need} bytes > the "
                            f"{EQL_NOALLOC_SCRATCH_BYTES}-byte library scratch, or past the 2 GiB plane limit)")
     _check(st, "eqlinear_backward_weight_noalloc")
+
+
+# --- operators between the layers ---------------------------------------------------
+
+def eqlinear_rotary_plan(N: int, heads: int, kv_heads: int, d: int, rot: int, layout: int, dtype: int,
+                         base: float = 10000.0, scaling: int = EQL_ROTARY_PLAIN, factor: float = 1.0,
+                         context: float = 0.0, turns_slow: float = 1.0, turns_fast: float = 32.0,
+                         magnitude: float = 1.0) -> Plan:
+    """Plan of rotary positions over the first rot of each head's d channels."""
+    lib = load_library()
+    h = ctypes.c_void_p()
+    _check(lib.eqlinear_rotary_plan(ctypes.byref(h), N, heads, kv_heads, d, rot, int(layout), base, int(scaling),
+                                    factor, context, turns_slow, turns_fast, magnitude, int(dtype)),
+           "eqlinear_rotary_plan")
+    p = Plan(h.value, lib)
+    p.heads, p.kv_heads, p.d = heads, kv_heads, d
+    return p
+
+
+def eqlinear_mixer_plan(N: int, heads: int, kv_heads: int, d_k: int, d_v: int, dtype: int) -> Plan:
+    """Plan of linear attention: heads of d_k (queries, keys) and d_v (values) channels."""
+    lib = load_library()
+    h = ctypes.c_void_p()
+    _check(lib.eqlinear_mixer_plan(ctypes.byref(h), N, heads, kv_heads, d_k, d_v, int(dtype)), "eqlinear_mixer_plan")
+    p = Plan(h.value, lib)
+    p.heads, p.kv_heads, p.d_k, p.d_v = heads, kv_heads, d_k, d_v
+    return p
+
+
+def eqlinear_norm_plan(N: int, C: int, groups: int, act: int, dtype: int, eps: float = 1e-5) -> Plan:
+    """Plan of a group norm with an activation over C channels."""
+    lib = load_library()
+    h = ctypes.c_void_p()
+    _check(lib.eqlinear_norm_plan(ctypes.byref(h), N, C, groups, int(act), eps, int(dtype)), "eqlinear_norm_plan")
+    p = Plan(h.value, lib)
+    p.groups = groups
+    return p
+
+
+def _heads(t, plan: Plan, T: int, heads: int, d: int, name: str):
+    """A tensor [T, heads, d, N] (the last two axes contiguous) or an eqlinear_heads as it is."""
+    if isinstance(t, eqlinear_heads):
+        return t
+    N = plan.info["N"]
+    _gpu(t, name, plan.torch_dtype)
+    if tuple(t.shape) != (T, heads, d, N):
+        raise ValueError(f"{name}: expected shape {(T, heads, d, N)}, got {tuple(t.shape)}")
+    ts, hs, sd, sn = t.stride()
+    if (sn != 1 and N > 1) or (sd != N and d > 1):
+        raise ValueError(f"{name}: the channel and group axes must be contiguous")
+    return eqlinear_heads(t.data_ptr(), ts, hs)
+
+
+def _gpu(t, name: str, dtype):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must live on the GPU, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+
+
+def _dense(t, name: str, dtype, shape):
+    """Address of a contiguous GPU tensor of the given dtype and shape; None stays None, an address itself."""
+    if t is None or isinstance(t, int):
+        return t
+    _gpu(t, name, dtype)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _kind(plan: Plan, kind: int, where: str):
+    if plan.info["kind"] != kind:
+        raise EqlError(EQL_ERR_INVALID, where)
+
+
+def _sequences(offsets, batch):
+    """(address of the offsets or None, number of sequences)."""
+    import torch
+    if offsets is None:
+        return None, 1 if batch is None else int(batch)
+    if isinstance(offsets, int):
+        if batch is None:
+            raise ValueError("batch is required when offsets is a raw address")
+        return offsets, int(batch)
+    n = offsets.numel() - 1
+    if batch is not None and int(batch) != n:
+        raise ValueError(f"offsets: expected batch + 1 = {int(batch) + 1} values, got {n + 1}")
+    return _dense(offsets, "offsets", torch.int64, (n + 1,)), n
+
+
+def _workspace(workspace):
+    """(address or None, bytes) of a workspace tensor."""
+    if workspace is None:
+        return None, 0
+    if isinstance(workspace, int):
+        raise ValueError("workspace: pass a GPU tensor (its size is checked)")
+    return _raw_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _count(t, T, name):
+    if T is not None:
+        return int(T)
+    if isinstance(t, (int, eqlinear_heads)):
+        raise ValueError(f"T is required when {name} is an address")
+    return t.shape[0]
+
+
+def eqlinear_rotary(plan: Plan, q, k, positions, q_out, k_out, inverse: bool = False, T: int | None = None,
+                    stream=None):
+    """Turn q [T, heads, d, N] and k [T, kv_heads, d, N] (k and k_out may be None) by positions
+    (int32 [T]); q_out may be q and k_out k."""
+    import torch
+    _kind(plan, EQL_KIND_ROTARY, "eqlinear_rotary")
+    T = _count(q, T, "q")
+    H, K, d = plan.heads, plan.kv_heads, plan.d
+    _check(plan._lib.eqlinear_rotary(
+        plan.handle, _heads(q, plan, T, H, d, "q"), None if k is None else _heads(k, plan, T, K, d, "k"),
+        _dense(positions, "positions", torch.int32, (T,)), int(bool(inverse)), _heads(q_out, plan, T, H, d, "q_out"),
+        None if k_out is None else _heads(k_out, plan, T, K, d, "k_out"), T, _stream(stream)), "eqlinear_rotary")
+
+
+def eqlinear_linear_attention_workspace(plan: Plan, T: int, batch: int, backward: bool = False) -> int:
+    return int(plan._lib.eqlinear_linear_attention_workspace(plan.handle, int(T), int(batch), int(bool(backward))))
+
+
+def _state_shape(plan: Plan, batch: int):
+    N = plan.info["N"]
+    return (batch, plan.kv_heads, plan.d_k * N, plan.d_v * N)
+
+
+def eqlinear_linear_attention(plan: Plan, q, k, v, log_decay, o, scale: float, offsets=None, batch: int | None = None,
+                              state_in=None, state_out=None, workspace=None, T: int | None = None, stream=None):
+    """Causal linear attention with a decay for each kv head: o [T, heads, d_v, N] and the fp32 state
+    [batch, kv_heads, d_k N, d_v N] after the last token.  The sequences are offsets (int64 [batch + 1])
+    or batch equal runs (default: one)."""
+    import torch
+    _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention")
+    T = _count(q, T, "q")
+    H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    off, B = _sequences(offsets, batch)
+    ws, nb = _workspace(workspace)
+    shape = _state_shape(plan, B)
+    _check(plan._lib.eqlinear_linear_attention(
+        plan.handle, _heads(q, plan, T, H, dk, "q"), _heads(k, plan, T, K, dk, "k"), _heads(v, plan, T, K, dv, "v"),
+        _dense(log_decay, "log_decay", torch.float32, (K,)), scale, off, B,
+        _dense(state_in, "state_in", torch.float32, shape), _dense(state_out, "state_out", torch.float32, shape),
+        _heads(o, plan, T, H, dv, "o"), T, ws, nb, _stream(stream)), "eqlinear_linear_attention")
+
+
+def eqlinear_linear_attention_backward(plan: Plan, q, k, v, do, log_decay, dq, dk, dv, scale: float, offsets=None,
+                                       batch: int | None = None, state_in=None, dstate_out=None, dstate_in=None,
+                                       workspace=None, T: int | None = None, stream=None):
+    """Gradients dq, dk, dv (and dstate_in) of eqlinear_linear_attention."""
+    import torch
+    _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention_backward")
+    T = _count(q, T, "q")
+    H, K, ck, cv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    off, B = _sequences(offsets, batch)
+    ws, nb = _workspace(workspace)
+    shape = _state_shape(plan, B)
+    _check(plan._lib.eqlinear_linear_attention_backward(
+        plan.handle, _heads(q, plan, T, H, ck, "q"), _heads(k, plan, T, K, ck, "k"), _heads(v, plan, T, K, cv, "v"),
+        _heads(do, plan, T, H, cv, "do"), _dense(log_decay, "log_decay", torch.float32, (K,)), scale, off, B,
+        _dense(state_in, "state_in", torch.float32, shape), _dense(dstate_out, "dstate_out", torch.float32, shape),
+        _heads(dq, plan, T, H, ck, "dq"), _heads(dk, plan, T, K, ck, "dk"), _heads(dv, plan, T, K, cv, "dv"),
+        _dense(dstate_in, "dstate_in", torch.float32, shape), T, ws, nb, _stream(stream)),
+        "eqlinear_linear_attention_backward")
+
+
+def eqlinear_linear_attention_step(plan: Plan, q, k, v, log_decay, state, o, scale: float, batch: int | None = None,
+                                   stream=None):
+    """One token for each of batch sequences: state [batch, kv_heads, d_k N, d_v N] in place, o [batch, heads, d_v, N]."""
+    import torch
+    _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention_step")
+    B = _count(q, batch, "q")
+    H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    _check(plan._lib.eqlinear_linear_attention_step(
+        plan.handle, _heads(q, plan, B, H, dk, "q"), _heads(k, plan, B, K, dk, "k"), _heads(v, plan, B, K, dv, "v"),
+        _dense(log_decay, "log_decay", torch.float32, (K,)), scale,
+        _dense(state, "state", torch.float32, _state_shape(plan, B)), _heads(o, plan, B, H, dv, "o"), B,
+        _stream(stream)), "eqlinear_linear_attention_step")
+
+
+def eqlinear_group_norm_workspace(plan: Plan, T: int, batch: int, backward: bool = False) -> int:
+    return int(plan._lib.eqlinear_group_norm_workspace(plan.handle, int(T), int(batch), int(bool(backward))))
+
+
+def _tokens_of(t, plan: Plan, T: int, name: str):
+    """(address, token stride) of a tensor [T, C, N] with the last two axes contiguous."""
+    C, N = plan.info["C_in"], plan.info["N"]
+    _gpu(t, name, plan.torch_dtype)
+    if tuple(t.shape) != (T, C, N):
+        raise ValueError(f"{name}: expected shape {(T, C, N)}, got {tuple(t.shape)}")
+    ts, sc, sn = t.stride()
+    if (sn != 1 and N > 1) or (sc != N and C > 1):
+        raise ValueError(f"{name}: the channel and group axes must be contiguous")
+    return t.data_ptr(), ts
+
+
+def eqlinear_group_norm(plan: Plan, x, gamma, beta, y, stats=None, offsets=None, batch: int | None = None,
+                        workspace=None, stream=None):
+    """y = act(gamma (x - mean) / sqrt(var + eps) + beta), statistics over each sample's tokens, a group's
+    channels and their group elements; x, y [T, C, N].  The samples are offsets (int64 [batch + 1]) or batch
+    equal runs (default: one)."""
+    import torch
+    _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm")
+    T, C, dt = x.shape[0], plan.info["C_in"], plan.torch_dtype
+    off, B = _sequences(offsets, batch)
+    ws, nb = _workspace(workspace)
+    _check(plan._lib.eqlinear_group_norm(
+        plan.handle, *_tokens_of(x, plan, T, "x"), _dense(gamma, "gamma", dt, (C,)), _dense(beta, "beta", dt, (C,)),
+        off, B, *_tokens_of(y, plan, T, "y"), _dense(stats, "stats", torch.float32, (B, plan.groups, 2)), T, ws, nb,
+        _stream(stream)), "eqlinear_group_norm")
+
+
+def eqlinear_group_norm_backward(plan: Plan, dy, x, gamma, beta, stats, dx, dgamma, dbeta, offsets=None,
+                                 batch: int | None = None, workspace=None, stream=None):
+    """Gradients of eqlinear_group_norm: dx [T, C, N] in the plan dtype, dgamma and dbeta fp32 [C] (or None)."""
+    import torch
+    _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm_backward")
+    T, C, dt = x.shape[0], plan.info["C_in"], plan.torch_dtype
+    off, B = _sequences(offsets, batch)
+    ws, nb = _workspace(workspace)
+    _check(plan._lib.eqlinear_group_norm_backward(
+        plan.handle, *_tokens_of(dy, plan, T, "dy"), *_tokens_of(x, plan, T, "x"), _dense(gamma, "gamma", dt, (C,)),
+        _dense(beta, "beta", dt, (C,)), _dense(stats, "stats", torch.float32, (B, plan.groups, 2)), off, B,
+        *_tokens_of(dx, plan, T, "dx"), _dense(dgamma, "dgamma", torch.float32, (C,)),
+        _dense(dbeta, "dbeta", torch.float32, (C,)), T, ws, nb, _stream(stream)), "eqlinear_group_norm_backward")
 
 
 def built() -> bool:

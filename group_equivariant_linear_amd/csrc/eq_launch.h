@@ -97,4 +97,71 @@ hipError_t launch_dn_to_fourier(int n, int io, const void* x_reg, void* x_four, 
 hipError_t launch_dn_to_regular(int n, int io, const void* y_four, void* y_reg, int m, int64_t T,
                                 hipStream_t stream);
 
+// --- operators between the layers ---------------------------------------------------
+
+// Tensor [T][heads][D], the last axis contiguous; strides in elements.
+struct Heads {
+    const void* p;
+    int64_t ts, hs;
+};
+
+constexpr int kMaxRotaryPairs = 128;
+
+// Turns per position of every channel pair, and the factor on the turned pairs.
+struct RotaryFreq {
+    double turns[kMaxRotaryPairs];
+    float magnitude;
+};
+
+// rotary.hip: q and k in one launch (k_heads = 0: q alone)
+struct RotaryArgs {
+    Heads q, k, q_out, k_out;
+    const int32_t* positions;
+    int64_t T;
+    int q_heads, k_heads;
+    int N, d, rot, layout, inverse;
+};
+hipError_t launch_rotary(int io, const RotaryArgs& a, const RotaryFreq& f, hipStream_t stream);
+
+// group_norm.hip: C channels x N elements per token in `groups` groups; offsets
+// null: samples of T / batch tokens
+struct NormArgs {
+    const void* x;
+    int64_t ldx;
+    const void *gamma, *beta;
+    const int64_t* offsets;
+    int64_t batch, T;
+    int C, N, groups, act;
+    float eps;
+    float* stats;
+    void* y;  // forward
+    int64_t ldy;
+    const void* dy;  // backward
+    int64_t lddy;
+    void* dx;
+    int64_t lddx;
+    float *dgamma, *dbeta;
+};
+size_t group_norm_workspace(int io, int C, int N, int groups, int64_t T, int64_t batch, bool backward);
+hipError_t launch_group_norm(int io, const NormArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_group_norm_backward(int io, const NormArgs& a, void* ws, hipStream_t stream);
+
+// linear_attention.hip.  D_k, D_v: numbers per head.
+struct MixArgs {
+    Heads q, k, v, o;
+    Heads d_o, dq, dk, dv;  // backward
+    const float* log_decay;
+    float scale;
+    const int64_t* offsets;
+    int64_t batch, T;
+    int heads, kv_heads, D_k, D_v;
+    const float *state_in, *d_state_out;
+    float *state_out, *d_state_in;
+};
+size_t linear_attention_workspace(int io, int heads, int kv_heads, int D_k, int D_v, int64_t T, int64_t batch,
+                                  bool backward);
+hipError_t launch_linear_attention(int io, const MixArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_linear_attention_backward(int io, const MixArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_linear_attention_step(int io, const MixArgs& a, hipStream_t stream);
+
 }  // namespace eql

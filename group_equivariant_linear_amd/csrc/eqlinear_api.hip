@@ -3,34 +3,23 @@
 // before any HIP call so the error paths can be exercised without a GPU.
 #include <new>
 
-#include "../../include/eqlinear.h"
-#include "eq_launch.h"
+#include "eq_plan.h"
 
-struct eqlinear_plan_s {
-    int kind;
-    int dtype;
-    int N;
-    int C_in, C_out;
-};
+using eql::dtype_ok;
+using eql::elem_size;
+using eql::hip_status;
+using eql::kMaxWidth;
+using eql::overlaps;
 
 namespace {
-
-
-bool dtype_ok(int dt) { return dt == EQL_F32 || dt == EQL_BF16 || dt == EQL_F16; }
 
 // The plan dtype is the launchers' element-type code (eql::kIo*).
 static_assert(EQL_F32 == eql::kIoF32 && EQL_BF16 == eql::kIoBF16 && EQL_F16 == eql::kIoF16, "type codes");
 
-size_t elem_size(const eqlinear_plan_s* p) { return p->dtype == EQL_F32 ? 4 : 2; }
-
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
-eqlinear_status hip_status(hipError_t e) { return e == hipSuccess ? EQL_OK : EQL_ERR_HIP; }
+// The kinds that are linear layers: what the comparator takes.
+bool is_layer(const eqlinear_plan_s* p) { return p->kind == EQL_KIND_CN || p->kind == EQL_KIND_D8; }
 
 int64_t in_width(const eqlinear_plan_s* p) {
     return p->kind == EQL_KIND_CN ? (int64_t)p->N * p->C_in : p->C_in;
@@ -38,9 +27,6 @@ int64_t in_width(const eqlinear_plan_s* p) {
 int64_t out_width(const eqlinear_plan_s* p) {
     return p->kind == EQL_KIND_CN ? (int64_t)p->N * p->C_out : p->C_out;
 }
-
-// Widths are capped so every per-row offset fits an int in the kernels.
-constexpr int64_t kMaxWidth = 1 << 20;
 
 // Irreps of the dihedral group of the regular n-gon: 1-D ones (A1, A2, and B1,
 // B2 for even n) and 2-D ones E_k.
@@ -105,6 +91,11 @@ eqlinear_status eqlinear_plan_info(eqlinear_plan_t p, eqlinear_info* out) {
     in.N = p->N;
     in.C_in = p->C_in;
     in.C_out = p->C_out;
+    if (!is_layer(p)) {  // operators: no weight spectrum, no products
+        in.params = p->kind == EQL_KIND_NORM ? 2 * (int64_t)p->C_in : 0;
+        *out = in;
+        return EQL_OK;
+    }
     const int64_t ci = p->C_in, co = p->C_out;
     if (p->kind == EQL_KIND_CN) {
         const int N = p->N;
@@ -368,7 +359,7 @@ eqlinear_status eqlinear_d8_forward(eqlinear_plan_t p, const void* x, const void
 
 eqlinear_status eqlinear_expand_dense(eqlinear_plan_t p, const void* w, void* w_dense,
                                       void* stream) {
-    if (!p || !w || !w_dense) return EQL_ERR_INVALID;
+    if (!p || !is_layer(p) || !w || !w_dense) return EQL_ERR_INVALID;
     if (!aligned16(w) || !aligned16(w_dense)) return EQL_ERR_INVALID;
     const size_t es = elem_size(p);
     const size_t wb = eqlinear_w_hat_elems(p) * es;
@@ -386,7 +377,7 @@ eqlinear_status eqlinear_expand_dense(eqlinear_plan_t p, const void* w, void* w_
 
 eqlinear_status eqlinear_dense_forward(eqlinear_plan_t p, const void* x, const void* w_dense,
                                        void* y, int64_t T, void* stream) {
-    if (!p) return EQL_ERR_INVALID;
+    if (!p || !is_layer(p)) return EQL_ERR_INVALID;
     if (T < 0) return EQL_ERR_INVALID;
     if (T == 0) return EQL_OK;
     if (!x || !w_dense || !y) return EQL_ERR_INVALID;

@@ -63,7 +63,13 @@ typedef enum {
 
 typedef enum { EQL_F32 = 0, EQL_BF16 = 1, EQL_F16 = 2 } eqlinear_dtype;
 
-typedef enum { EQL_KIND_CN = 0, EQL_KIND_D8 = 1 } eqlinear_kind;
+typedef enum {
+    EQL_KIND_CN = 0,
+    EQL_KIND_D8 = 1,
+    EQL_KIND_ROTARY = 2, /* eqlinear_rotary_plan */
+    EQL_KIND_MIXER = 3,  /* eqlinear_mixer_plan */
+    EQL_KIND_NORM = 4    /* eqlinear_norm_plan */
+} eqlinear_kind;
 
 typedef struct eqlinear_plan_s* eqlinear_plan_t;
 
@@ -74,7 +80,8 @@ typedef struct {
     int32_t kind;               /* eqlinear_kind */
     int32_t dtype;              /* eqlinear_dtype */
     int32_t N;                  /* group order (8 for D8) */
-    int32_t C_in, C_out;        /* C_N: channels per group element; D8: full widths */
+    int32_t C_in, C_out;        /* C_N: channels per group element; D8: full widths;
+                                   rotary, mixer: channels of all query heads; norm: C */
     int32_t bins;               /* C_N: floor(N/2)+1 kept frequencies; D8: 5 irrep blocks */
     int32_t planes;             /* C_N: real frequency planes (= N) */
     int32_t has_nyquist;        /* C_N: 1 when N is even */
@@ -195,8 +202,10 @@ eqlinear_status eqlinear_forward_tiled(eqlinear_plan_t plan, const void* x, cons
 /* Activations that eqlinear_forward_bias_act can apply. */
 typedef enum {
     EQL_ACT_NONE = 0, /* y = layer(x) + bias                                   */
-    EQL_ACT_GELU = 1  /* y = GELU(layer(x) + bias), GELU(v) = v * Phi(v) =
+    EQL_ACT_GELU = 1, /* y = GELU(layer(x) + bias), GELU(v) = v * Phi(v) =
                          v/2 * (1 + erf(v / sqrt 2)), the exact (erf) form     */
+    EQL_ACT_SILU = 2  /* v / (1 + exp(-v)); norm plans only (the layers' fused
+                         epilogues take the two above)                         */
 } eqlinear_act;
 
 /* C_N forward with the layer's neighbours fused into the store: a per-channel
@@ -378,6 +387,188 @@ eqlinear_status eqlinear_expand_dense(eqlinear_plan_t plan, const void* w, void*
  * input and output widths of the plan. */
 eqlinear_status eqlinear_dense_forward(eqlinear_plan_t plan, const void* x,
                                        const void* w_dense, void* y, int64_t T, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators between the layers: token mixing on regular-representation
+ * features.  A feature is a record of N group elements per channel, as the
+ * C_N layers read and write it; a head is a run of d whole channels, d N
+ * numbers.  Each operator commutes with a cyclic shift of the group axis, so a
+ * block of them and of C_N layers is equivariant: rotary turns a channel pair
+ * by one angle for all its group elements, attention scores sum over the group
+ * axis, and norm statistics run over it.
+ *
+ * Conventions beyond those above
+ *  - Per-token tensors come as an eqlinear_heads (or, for the norm, a pointer
+ *    and a token stride), so that q, k and v may be slices of one projection's
+ *    output and gradients may be written into slices of one buffer.  They need
+ *    element alignment only; whole 16-byte rows (address and strides) run
+ *    faster.  Strides are in elements, >= 0; a stride of 0 repeats an input.
+ *    Outputs must not repeat elements and must not overlap inputs or each
+ *    other, except where a call allows its input as output.  Tensors whose
+ *    address ranges interleave must have the same token stride.
+ *  - offsets: device, batch + 1 int64 values, the first token of each sequence
+ *    and the end of the last (offsets[0] = 0, offsets[batch] = T, not
+ *    decreasing; equal neighbours are an empty sequence); 8-byte aligned.
+ *    NULL: batch sequences of T / batch tokens each (T a multiple of batch).
+ *    The kernels clamp offsets to [0, T], so wrong ones give wrong results,
+ *    never accesses outside the tensors.
+ *  - fp32 arithmetic, statistics and states for every plan dtype; where a
+ *    kernel rounds an intermediate value it is said at the call.
+ * ------------------------------------------------------------------------- */
+
+/* A tensor [T][heads][d][N] with the last two axes contiguous. */
+typedef struct {
+    void* ptr;            /* device address of token 0, head 0; inputs are only read */
+    int64_t token_stride; /* elements from one token to the next */
+    int64_t head_stride;  /* elements from one head to the next */
+} eqlinear_heads;
+
+/* Which channels of a head form a pair under rotary positions: channel j with
+ * j + rot/2 (HALF), or 2j with 2j + 1 (INTERLEAVED), j < rot/2. */
+typedef enum { EQL_ROTARY_HALF = 0, EQL_ROTARY_INTERLEAVED = 1 } eqlinear_rotary_layout;
+
+/* How pair j's angle per position, f_j = base^(-2j/rot), is scaled for contexts
+ * longer than the trained one:
+ *   PLAIN        f_j
+ *   LINEAR       f_j / factor
+ *   RAISED_BASE  base -> base factor^(rot/(rot-2)): the slowest pair is
+ *                stretched by factor, the fastest not at all (rot = 2: f_0)
+ *   BANDED       f_j (w + (1 - w)/factor), w = clamp((t_j - turns_slow) /
+ *                (turns_fast - turns_slow), 0, 1), t_j = context f_j / 2 pi the
+ *                turns that pair j makes within the trained context */
+typedef enum {
+    EQL_ROTARY_PLAIN = 0,
+    EQL_ROTARY_LINEAR = 1,
+    EQL_ROTARY_RAISED_BASE = 2,
+    EQL_ROTARY_BANDED = 3
+} eqlinear_rotary_scaling;
+
+/* Plan of rotary positions for heads of d channels, of which the first rot (even,
+ * 2 <= rot <= d, rot <= 256) turn and the rest pass through.  heads query heads
+ * and kv_heads key heads; heads d N and kv_heads d N at most 2^20.  base > 0;
+ * factor > 0 (not PLAIN); context > 0 and turns_fast > turns_slow >= 0
+ * (BANDED); magnitude multiplies the turned pairs (1: a pure rotation), > 0.
+ * Host metadata only.  rot > 256: EQL_ERR_UNSUPPORTED. */
+eqlinear_status eqlinear_rotary_plan(eqlinear_plan_t* out, int N, int heads, int kv_heads, int d, int rot,
+                                     eqlinear_rotary_layout layout, double base, eqlinear_rotary_scaling scaling,
+                                     double factor, double context, double turns_slow, double turns_fast,
+                                     double magnitude, eqlinear_dtype dt);
+
+/* Rotary positions.  For token t at position p, every head, pair (a, b) with
+ * angle w = p f, and every group element:
+ *   a' = m (a cos w - b sin w),  b' = m (b cos w + a sin w)      (m = magnitude)
+ * inverse != 0 turns by -w: the gradient of the forward (the transpose), and
+ * for m = 1 its inverse.
+ *   q, q_out  [T][heads][d][N], k, k_out [T][kv_heads][d][N]; q_out may be q
+ *             and k_out k (the same address and strides); k and k_out may both
+ *             be NULL
+ *   positions int32 [T], device, any value; 4-byte aligned
+ * The angle is reduced to a fraction of a turn in fp64, so its error does not
+ * grow with the position; cos, sin and the rotation are fp32, rounded once. */
+eqlinear_status eqlinear_rotary(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
+                                const int32_t* positions, int inverse, const eqlinear_heads* q_out,
+                                const eqlinear_heads* k_out, int64_t T, void* stream);
+
+/* Plan of linear attention: heads query heads that share kv_heads key and value
+ * heads (heads a multiple of kv_heads; query head h reads kv head
+ * h / (heads / kv_heads)), d_k channels per query and key head and d_v per value
+ * head.  D_k = d_k N and D_v = d_v N are the numbers per head, at most 128
+ * (EQL_ERR_UNSUPPORTED beyond).  Host metadata only. */
+eqlinear_status eqlinear_mixer_plan(eqlinear_plan_t* out, int N, int heads, int kv_heads, int d_k, int d_v,
+                                    eqlinear_dtype dt);
+
+/* Bytes of workspace of eqlinear_linear_attention, or with backward != 0 of
+ * either call (0: none needed); 0 for other plans and negative sizes. */
+size_t eqlinear_linear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t batch, int backward);
+
+/* Causal linear attention with a decay for each kv head, for prompts and training.
+ * Per sequence and kv head, with g = exp(log_decay) and the state S
+ * (D_k x D_v, rows indexed by the key's numbers):
+ *   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * i.e. o_t = scale sum over s <= t of g^(t-s) (q_t . k_s) v_s + scale g^(t+1) S_0^T q_t.
+ *   q [T][heads][d_k][N], k [T][kv_heads][d_k][N], v [T][kv_heads][d_v][N],
+ *   o [T][heads][d_v][N]
+ *   log_decay fp32 [kv_heads], device: the natural logarithm of each decay, <= 0
+ *             (-infinity: no memory); scale: finite, not 0
+ *   state_in  fp32 [batch][kv_heads][D_k][D_v] before the first token, or NULL
+ *             (zeros); state_out the same after the last, or NULL; the two must
+ *             not overlap (several workgroups read a state that one writes).  An
+ *             empty sequence passes its state through.  16-byte aligned
+ *   workspace at least eqlinear_linear_attention_workspace bytes, 256-byte aligned
+ * 16-bit plans round the decayed scores to the plan dtype before their product
+ * with v; the state keeps fp32 between tokens and enters the matrix cores as two
+ * terms of the plan dtype.  Asynchronous on stream, no allocation; deterministic. */
+eqlinear_status eqlinear_linear_attention(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
+                                          const eqlinear_heads* v, const float* log_decay, float scale,
+                                          const int64_t* offsets, int64_t batch, const float* state_in,
+                                          float* state_out, const eqlinear_heads* o, int64_t T, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Its gradients for upstream gradients d_o (of o) and d_state_out (of the state
+ * after the last token; NULL: zeros):
+ *   dq_t = scale S_t d_o_t,   R_t = g R_{t+1} + scale sum over the heads that share
+ *   the state of q_t d_o_t^T  (R_T = g^-1 d_state_out),
+ *   dk_t = R_t v_t,  dv_t = R_t^T k_t,  d_state_in = g R_0
+ * (dk and dv sum over the query heads of their kv head).  state_in as given to
+ * the forward; d_state_in may be NULL and must not overlap d_state_out.  The decays are constants:
+ * no gradient.  Same rounding rule, for the scores of each product. */
+eqlinear_status eqlinear_linear_attention_backward(eqlinear_plan_t plan, const eqlinear_heads* q,
+                                                   const eqlinear_heads* k, const eqlinear_heads* v,
+                                                   const eqlinear_heads* d_o, const float* log_decay, float scale,
+                                                   const int64_t* offsets, int64_t batch, const float* state_in,
+                                                   const float* d_state_out, const eqlinear_heads* dq,
+                                                   const eqlinear_heads* dk, const eqlinear_heads* dv,
+                                                   float* d_state_in, int64_t T, void* workspace,
+                                                   size_t workspace_bytes, void* stream);
+
+/* One token for each of batch sequences (serving): S <- g S + k v^T and
+ * o = scale S^T q, all fp32, the state updated in place and o rounded once.
+ *   q, k, v, o as above with T = batch (token b belongs to sequence b);
+ *   state fp32 [batch][kv_heads][D_k][D_v]. */
+eqlinear_status eqlinear_linear_attention_step(eqlinear_plan_t plan, const eqlinear_heads* q,
+                                               const eqlinear_heads* k, const eqlinear_heads* v,
+                                               const float* log_decay, float scale, float* state,
+                                               const eqlinear_heads* o, int64_t batch, void* stream);
+
+/* Plan of a group norm with an activation over C channels in groups of C / groups
+ * (C a multiple of groups, C N at most 2^20); act is an eqlinear_act; eps >= 0.
+ * Host metadata only. */
+eqlinear_status eqlinear_norm_plan(eqlinear_plan_t* out, int N, int C, int groups, eqlinear_act act, double eps,
+                                   eqlinear_dtype dt);
+
+/* Bytes of workspace of eqlinear_group_norm, or with backward != 0 of either
+ * call (0: none needed); 0 for other plans and negative sizes. */
+size_t eqlinear_group_norm_workspace(eqlinear_plan_t plan, int64_t T, int64_t batch, int backward);
+
+/* Group norm, channels last: for every sample b and group j, over the sample's
+ * tokens, the group's channels and their N group elements,
+ *   xh = (x - mean) / sqrt(var + eps)   (var: mean of squared differences)
+ *   y[t][c][n] = act(gamma[c] xh[t][c][n] + beta[c])
+ * A sample is a run of tokens: batch == T makes every token its own (a norm per
+ * token, with groups = heads a norm per head).
+ *   x, y  [T][C][N] with x_stride, y_stride elements from token to token; y may
+ *         be x (with the same stride)
+ *   gamma, beta  plan dtype [C], element-aligned, or NULL (1 and 0)
+ *   stats fp32 [batch][groups][2] out: mean and 1/sqrt(var + eps) for the
+ *         backward, or NULL; an empty sample has (0, 0); 8-byte aligned
+ * Statistics are fp32 and do not cancel when the mean is large against the
+ * spread.  Asynchronous on stream, no allocation; deterministic. */
+eqlinear_status eqlinear_group_norm(eqlinear_plan_t plan, const void* x, int64_t x_stride, const void* gamma,
+                                    const void* beta, const int64_t* offsets, int64_t batch, void* y,
+                                    int64_t y_stride, float* stats, int64_t T, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Its gradients from dy, x and the forward's stats, with dz = dy act'(gamma xh + beta):
+ *   dgamma[c] = sum dz xh,  dbeta[c] = sum dz          (all tokens, N elements; fp32)
+ *   dx = (gamma dz - m1 - xh m2) / sqrt(var + eps), m1 and m2 the means of
+ *        gamma dz and gamma dz xh over the sample and group
+ * dgamma and dbeta may be NULL; they are overwritten (zeros for T = 0).  dx may be
+ * dy (with the same stride).  16-byte aligned dgamma, dbeta. */
+eqlinear_status eqlinear_group_norm_backward(eqlinear_plan_t plan, const void* dy, int64_t dy_stride, const void* x,
+                                             int64_t x_stride, const void* gamma, const void* beta,
+                                             const float* stats, const int64_t* offsets, int64_t batch, void* dx,
+                                             int64_t dx_stride, float* dgamma, float* dbeta, int64_t T,
+                                             void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
