@@ -769,41 +769,99 @@ hipError_t launch_linear_attention_backward(int io, const MixArgs& a, void* ws, 
 
 namespace {
 
-// One workgroup per (sequence, kv head): the state in memory, each element read and
-// written once, for all query heads that share it.
-template <typename IO>
-__global__ __launch_bounds__(256) void step_kernel(MixArgs a) {
-    __shared__ float vk[kMaxD], vv[kMaxD], vq[kMaxD];
-    const int64_t b = blockIdx.x / a.kv_heads;
-    const int kv = (int)(blockIdx.x % a.kv_heads), r = a.heads / a.kv_heads, tid = (int)threadIdx.x;
-    const float g = expf(a.log_decay[kv]);
-    float* S = a.state_out + (int64_t)blockIdx.x * a.D_k * a.D_v;
-    for (int e = tid; e < a.D_k; e += 256) vk[e] = (float)((const IO*)a.k.p)[b * a.k.ts + kv * a.k.hs + e];
-    for (int e = tid; e < a.D_v; e += 256) vv[e] = (float)((const IO*)a.v.p)[b * a.v.ts + kv * a.v.hs + e];
-    __syncthreads();
-    for (int e = tid; e < a.D_k * a.D_v; e += 256) S[e] = fmaf(vk[e / a.D_v], vv[e % a.D_v], g * S[e]);
-    for (int hh = 0; hh < r; ++hh) {
-        const int h = kv * r + hh;
-        __syncthreads();
-        for (int e = tid; e < a.D_k; e += 256) vq[e] = (float)((const IO*)a.q.p)[b * a.q.ts + h * a.q.hs + e];
-        __syncthreads();
-        for (int c = tid; c < a.D_v; c += 256) {
-            float o = 0.0f;
-            for (int i = 0; i < a.D_k; ++i) o = fmaf(vq[i], S[i * a.D_v + c], o);
-            ((IO*)const_cast<void*>(a.o.p))[b * a.o.ts + h * a.o.hs + c] = (IO)(o * a.scale);
+// One token.  A workgroup takes one (sequence, kv head): each thread reads, updates
+// and writes back four columns (one, where D_v is odd against that) of rows row,
+// row + rows, ... of the state, and adds them into the outputs of HB query heads that
+// share it; further heads, HB at a time, read the state again.  The state, read and
+// written once, is all the traffic that counts; its loads go out U at a time.
+template <typename IO, bool VEC, int HB>
+__global__ __launch_bounds__(256) void step_kernel(MixArgs a, int cols) {
+    constexpr int U = 4, W = VEC ? 4 : 1;  // columns of a thread
+    __shared__ float vk[kMaxD], vq[HB][kMaxD], red[HB][256 * W];
+    const int64_t b = blockIdx.x / (uint32_t)a.kv_heads;
+    const int kv = (int)(blockIdx.x % (uint32_t)a.kv_heads), r = a.heads / a.kv_heads, tid = (int)threadIdx.x;
+    const int rows = 256 / cols, row = tid / cols, c = (tid - row * cols) * W;
+    const bool on = row < rows;
+    using R = std::conditional_t<VEC, f32x4, float>;
+    float* S = a.state_out + (int64_t)blockIdx.x * a.D_k * a.D_v + c;
+    const float g = power(a.log_decay[kv] * kLog2e, 1);
+    R v{};
+    if (on) {
+        const IO* p = (const IO*)a.v.p + b * a.v.ts + kv * a.v.hs + c;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (float)p[i];
+        } else {
+            v = (float)p[0];
         }
     }
+    if (tid < a.D_k) vk[tid] = (float)((const IO*)a.k.p)[b * a.k.ts + kv * a.k.hs + tid];
+    for (int h0 = 0; h0 < r; h0 += HB) {
+        const int nh = r - h0 < HB ? r - h0 : HB;
+        const IO* q = (const IO*)a.q.p + b * a.q.ts + (int64_t)(kv * r + h0) * a.q.hs;
+        for (int e = tid; e < nh * kMaxD; e += 256) {
+            const int h = e / kMaxD, i = e % kMaxD;
+            if (i < a.D_k) vq[h][i] = a.scale * (float)q[h * a.q.hs + i];
+        }
+        __syncthreads();
+        R o[HB];
+#pragma unroll
+        for (int h = 0; h < HB; ++h) o[h] = R{};
+        if (on)
+            for (int i0 = row; i0 < a.D_k; i0 += U * rows) {
+                R s[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u * rows < a.D_k) s[u] = *reinterpret_cast<const R*>(S + (i0 + u * rows) * a.D_v);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * rows;
+                    if (i < a.D_k) {
+                        if (h0 == 0) {
+                            s[u] = s[u] * g + v * vk[i];
+                            *reinterpret_cast<R*>(S + i * a.D_v) = s[u];
+                        }
+#pragma unroll
+                        for (int h = 0; h < HB; ++h)
+                            if (h < nh) o[h] += s[u] * vq[h][i];
+                    }
+                }
+            }
+#pragma unroll
+        for (int h = 0; h < HB; ++h) *reinterpret_cast<R*>(red[h] + tid * W) = o[h];
+        __syncthreads();
+        IO* out = (IO*)const_cast<void*>(a.o.p) + b * a.o.ts + (int64_t)(kv * r + h0) * a.o.hs;
+        for (int e = tid; e < nh * a.D_v; e += 256) {
+            const int h = e / a.D_v, i = e - h * a.D_v;
+            float w = red[h][i];
+            for (int k = 1; k < rows; ++k) w += red[h][k * a.D_v + i];
+            out[h * a.o.hs + i] = (IO)w;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename IO>
+hipError_t step(const MixArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)(a.batch * a.kv_heads));
+    const int r = a.heads / a.kv_heads;
+    if (a.D_v % 4 == 0) {
+        const int cols = a.D_v / 4;
+        if (r == 1) hipLaunchKernelGGL((step_kernel<IO, true, 1>), grid, dim3(256), 0, stream, a, cols);
+        else if (r == 2) hipLaunchKernelGGL((step_kernel<IO, true, 2>), grid, dim3(256), 0, stream, a, cols);
+        else hipLaunchKernelGGL((step_kernel<IO, true, 4>), grid, dim3(256), 0, stream, a, cols);
+    } else {
+        hipLaunchKernelGGL((step_kernel<IO, false, 2>), grid, dim3(256), 0, stream, a, a.D_v);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_linear_attention_step(int io, const MixArgs& a, hipStream_t stream) {
     if (a.batch * a.kv_heads > 0x7fffffff) return hipErrorNotSupported;
-    const dim3 grid((uint32_t)(a.batch * a.kv_heads));
-    if (io == kIoF32) hipLaunchKernelGGL(step_kernel<float>, grid, dim3(256), 0, stream, a);
-    else if (io == kIoBF16) hipLaunchKernelGGL(step_kernel<__bf16>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(step_kernel<_Float16>, grid, dim3(256), 0, stream, a);
-    return hipGetLastError();
+    return io == kIoF32 ? step<float>(a, stream)
+                        : (io == kIoBF16 ? step<__bf16>(a, stream) : step<_Float16>(a, stream));
 }
 
 }  // namespace eql
