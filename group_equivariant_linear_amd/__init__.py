@@ -12,6 +12,7 @@ Tensor arguments may be torch tensors on a ROCm device, or plain integers
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -149,6 +150,7 @@ class Plan:
         self.handle = ctypes.c_void_p(handle)
         self._lib = lib
         self.info = eqlinear_plan_info(self)
+        self.kind, self.N, self.C = self.info["kind"], self.info["N"], self.info["C_in"]
 
     def __del__(self):
         # may run during interpreter shutdown, when module globals (ctypes among
@@ -163,7 +165,7 @@ class Plan:
     def dtype(self):
         return self.info["dtype"]
 
-    @property
+    @functools.cached_property
     def torch_dtype(self):
         return _torch_dtype(self)
 
@@ -467,13 +469,28 @@ def eqlinear_norm_plan(N: int, C: int, groups: int, act: int, dtype: int, eps: f
     return p
 
 
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """The torch module: imported by the first call that has tensors."""
+    import torch
+    return torch
+
+
+def _raw_stream(stream):
+    """hipStream_t of a torch stream or an address; None: the current stream of the current device."""
+    if stream is None:
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _heads(t, plan: Plan, T: int, heads: int, d: int, name: str):
     """A tensor [T, heads, d, N] (the last two axes contiguous) or an eqlinear_heads as it is."""
-    if isinstance(t, eqlinear_heads):
+    if type(t) is eqlinear_heads:
         return t
-    N = plan.info["N"]
+    N = plan.N
     _gpu(t, name, plan.torch_dtype)
-    if tuple(t.shape) != (T, heads, d, N):
+    if t.shape != (T, heads, d, N):
         raise ValueError(f"{name}: expected shape {(T, heads, d, N)}, got {tuple(t.shape)}")
     ts, hs, sd, sn = t.stride()
     if (sn != 1 and N > 1) or (sd != N and d > 1):
@@ -482,21 +499,22 @@ def _heads(t, plan: Plan, T: int, heads: int, d: int, name: str):
 
 
 def _gpu(t, name: str, dtype):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensor must live on the GPU, got {t.device}")
-    if t.dtype != dtype:
+    try:
+        fits = t.is_cuda and t.dtype is dtype
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+    if not fits:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensor must live on the GPU, got {t.device}")
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
 
 
 def _dense(t, name: str, dtype, shape):
     """Address of a contiguous GPU tensor of the given dtype and shape; None stays None, an address itself."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
     _gpu(t, name, dtype)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
@@ -504,13 +522,12 @@ def _dense(t, name: str, dtype, shape):
 
 
 def _kind(plan: Plan, kind: int, where: str):
-    if plan.info["kind"] != kind:
+    if plan.kind != kind:
         raise EqlError(EQL_ERR_INVALID, where)
 
 
 def _sequences(offsets, batch):
     """(address of the offsets or None, number of sequences)."""
-    import torch
     if offsets is None:
         return None, 1 if batch is None else int(batch)
     if isinstance(offsets, int):
@@ -520,7 +537,7 @@ def _sequences(offsets, batch):
     n = offsets.numel() - 1
     if batch is not None and int(batch) != n:
         raise ValueError(f"offsets: expected batch + 1 = {int(batch) + 1} values, got {n + 1}")
-    return _dense(offsets, "offsets", torch.int64, (n + 1,)), n
+    return _dense(offsets, "offsets", _torch().int64, (n + 1,)), n
 
 
 def _workspace(workspace):
@@ -544,14 +561,14 @@ def eqlinear_rotary(plan: Plan, q, k, positions, q_out, k_out, inverse: bool = F
                     stream=None):
     """Turn q [T, heads, d, N] and k [T, kv_heads, d, N] (k and k_out may be None) by positions
     (int32 [T]); q_out may be q and k_out k."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_ROTARY, "eqlinear_rotary")
     T = _count(q, T, "q")
     H, K, d = plan.heads, plan.kv_heads, plan.d
     _check(plan._lib.eqlinear_rotary(
         plan.handle, _heads(q, plan, T, H, d, "q"), None if k is None else _heads(k, plan, T, K, d, "k"),
         _dense(positions, "positions", torch.int32, (T,)), int(bool(inverse)), _heads(q_out, plan, T, H, d, "q_out"),
-        None if k_out is None else _heads(k_out, plan, T, K, d, "k_out"), T, _stream(stream)), "eqlinear_rotary")
+        None if k_out is None else _heads(k_out, plan, T, K, d, "k_out"), T, _raw_stream(stream)), "eqlinear_rotary")
 
 
 def eqlinear_linear_attention_workspace(plan: Plan, T: int, batch: int, backward: bool = False) -> int:
@@ -559,8 +576,7 @@ def eqlinear_linear_attention_workspace(plan: Plan, T: int, batch: int, backward
 
 
 def _state_shape(plan: Plan, batch: int):
-    N = plan.info["N"]
-    return (batch, plan.kv_heads, plan.d_k * N, plan.d_v * N)
+    return (batch, plan.kv_heads, plan.d_k * plan.N, plan.d_v * plan.N)
 
 
 def eqlinear_linear_attention(plan: Plan, q, k, v, log_decay, o, scale: float, offsets=None, batch: int | None = None,
@@ -568,7 +584,7 @@ def eqlinear_linear_attention(plan: Plan, q, k, v, log_decay, o, scale: float, o
     """Causal linear attention with a decay for each kv head: o [T, heads, d_v, N] and the fp32 state
     [batch, kv_heads, d_k N, d_v N] after the last token.  The sequences are offsets (int64 [batch + 1])
     or batch equal runs (default: one)."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention")
     T = _count(q, T, "q")
     H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
@@ -579,14 +595,14 @@ def eqlinear_linear_attention(plan: Plan, q, k, v, log_decay, o, scale: float, o
         plan.handle, _heads(q, plan, T, H, dk, "q"), _heads(k, plan, T, K, dk, "k"), _heads(v, plan, T, K, dv, "v"),
         _dense(log_decay, "log_decay", torch.float32, (K,)), scale, off, B,
         _dense(state_in, "state_in", torch.float32, shape), _dense(state_out, "state_out", torch.float32, shape),
-        _heads(o, plan, T, H, dv, "o"), T, ws, nb, _stream(stream)), "eqlinear_linear_attention")
+        _heads(o, plan, T, H, dv, "o"), T, ws, nb, _raw_stream(stream)), "eqlinear_linear_attention")
 
 
 def eqlinear_linear_attention_backward(plan: Plan, q, k, v, do, log_decay, dq, dk, dv, scale: float, offsets=None,
                                        batch: int | None = None, state_in=None, dstate_out=None, dstate_in=None,
                                        workspace=None, T: int | None = None, stream=None):
     """Gradients dq, dk, dv (and dstate_in) of eqlinear_linear_attention."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention_backward")
     T = _count(q, T, "q")
     H, K, ck, cv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
@@ -598,14 +614,14 @@ def eqlinear_linear_attention_backward(plan: Plan, q, k, v, do, log_decay, dq, d
         _heads(do, plan, T, H, cv, "do"), _dense(log_decay, "log_decay", torch.float32, (K,)), scale, off, B,
         _dense(state_in, "state_in", torch.float32, shape), _dense(dstate_out, "dstate_out", torch.float32, shape),
         _heads(dq, plan, T, H, ck, "dq"), _heads(dk, plan, T, K, ck, "dk"), _heads(dv, plan, T, K, cv, "dv"),
-        _dense(dstate_in, "dstate_in", torch.float32, shape), T, ws, nb, _stream(stream)),
+        _dense(dstate_in, "dstate_in", torch.float32, shape), T, ws, nb, _raw_stream(stream)),
         "eqlinear_linear_attention_backward")
 
 
 def eqlinear_linear_attention_step(plan: Plan, q, k, v, log_decay, state, o, scale: float, batch: int | None = None,
                                    stream=None):
     """One token for each of batch sequences: state [batch, kv_heads, d_k N, d_v N] in place, o [batch, heads, d_v, N]."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_MIXER, "eqlinear_linear_attention_step")
     B = _count(q, batch, "q")
     H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
@@ -613,7 +629,7 @@ def eqlinear_linear_attention_step(plan: Plan, q, k, v, log_decay, state, o, sca
         plan.handle, _heads(q, plan, B, H, dk, "q"), _heads(k, plan, B, K, dk, "k"), _heads(v, plan, B, K, dv, "v"),
         _dense(log_decay, "log_decay", torch.float32, (K,)), scale,
         _dense(state, "state", torch.float32, _state_shape(plan, B)), _heads(o, plan, B, H, dv, "o"), B,
-        _stream(stream)), "eqlinear_linear_attention_step")
+        _raw_stream(stream)), "eqlinear_linear_attention_step")
 
 
 def eqlinear_group_norm_workspace(plan: Plan, T: int, batch: int, backward: bool = False) -> int:
@@ -622,9 +638,9 @@ def eqlinear_group_norm_workspace(plan: Plan, T: int, batch: int, backward: bool
 
 def _tokens_of(t, plan: Plan, T: int, name: str):
     """(address, token stride) of a tensor [T, C, N] with the last two axes contiguous."""
-    C, N = plan.info["C_in"], plan.info["N"]
+    C, N = plan.C, plan.N
     _gpu(t, name, plan.torch_dtype)
-    if tuple(t.shape) != (T, C, N):
+    if t.shape != (T, C, N):
         raise ValueError(f"{name}: expected shape {(T, C, N)}, got {tuple(t.shape)}")
     ts, sc, sn = t.stride()
     if (sn != 1 and N > 1) or (sc != N and C > 1):
@@ -637,30 +653,30 @@ def eqlinear_group_norm(plan: Plan, x, gamma, beta, y, stats=None, offsets=None,
     """y = act(gamma (x - mean) / sqrt(var + eps) + beta), statistics over each sample's tokens, a group's
     channels and their group elements; x, y [T, C, N].  The samples are offsets (int64 [batch + 1]) or batch
     equal runs (default: one)."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm")
-    T, C, dt = x.shape[0], plan.info["C_in"], plan.torch_dtype
+    T, C, dt = x.shape[0], plan.C, plan.torch_dtype
     off, B = _sequences(offsets, batch)
     ws, nb = _workspace(workspace)
     _check(plan._lib.eqlinear_group_norm(
         plan.handle, *_tokens_of(x, plan, T, "x"), _dense(gamma, "gamma", dt, (C,)), _dense(beta, "beta", dt, (C,)),
         off, B, *_tokens_of(y, plan, T, "y"), _dense(stats, "stats", torch.float32, (B, plan.groups, 2)), T, ws, nb,
-        _stream(stream)), "eqlinear_group_norm")
+        _raw_stream(stream)), "eqlinear_group_norm")
 
 
 def eqlinear_group_norm_backward(plan: Plan, dy, x, gamma, beta, stats, dx, dgamma, dbeta, offsets=None,
                                  batch: int | None = None, workspace=None, stream=None):
     """Gradients of eqlinear_group_norm: dx [T, C, N] in the plan dtype, dgamma and dbeta fp32 [C] (or None)."""
-    import torch
+    torch = _torch()
     _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm_backward")
-    T, C, dt = x.shape[0], plan.info["C_in"], plan.torch_dtype
+    T, C, dt = x.shape[0], plan.C, plan.torch_dtype
     off, B = _sequences(offsets, batch)
     ws, nb = _workspace(workspace)
     _check(plan._lib.eqlinear_group_norm_backward(
         plan.handle, *_tokens_of(dy, plan, T, "dy"), *_tokens_of(x, plan, T, "x"), _dense(gamma, "gamma", dt, (C,)),
         _dense(beta, "beta", dt, (C,)), _dense(stats, "stats", torch.float32, (B, plan.groups, 2)), off, B,
         *_tokens_of(dx, plan, T, "dx"), _dense(dgamma, "dgamma", torch.float32, (C,)),
-        _dense(dbeta, "dbeta", torch.float32, (C,)), T, ws, nb, _stream(stream)), "eqlinear_group_norm_backward")
+        _dense(dbeta, "dbeta", torch.float32, (C,)), T, ws, nb, _raw_stream(stream)), "eqlinear_group_norm_backward")
 
 
 def built() -> bool:
