@@ -88,12 +88,13 @@ struct Piece {
     }
 };
 
-// gamma and beta of the numbers e .. e + V - 1 of a token's row.
-template <typename IO, int V>
-__device__ __forceinline__ void affine(const NormArgs& a, int e, float (&gm)[V], float (&be)[V]) {
+// gamma and beta of the numbers e .. e + V - 1 of a token's row: CP of them, V or, where
+// N is a multiple of V and a piece lies within a channel, one.
+template <typename IO, int CP>
+__device__ __forceinline__ void affine(const NormArgs& a, int e, float (&gm)[CP], float (&be)[CP]) {
     int c = e / a.N, n = e - c * a.N;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < CP; ++i) {
         gm[i] = a.gamma ? (float)((const IO*)a.gamma)[c] : 1.0f;
         be[i] = a.beta ? (float)((const IO*)a.beta)[c] : 0.0f;
         if (++n == a.N) n = 0, ++c;
@@ -123,21 +124,21 @@ __device__ __forceinline__ void slope_all(int act, const float (&z)[V], float (&
 }
 
 // y = act(gamma (x - mean) rstd + beta) of one piece
-template <typename IO, int V>
+template <typename IO, int V, int CP>
 __device__ __forceinline__ void put_y(const NormArgs& a, IO* to, const Piece<IO, V>& x, float mean, float rstd,
-                                      const float (&gm)[V], const float (&be)[V]) {
+                                      const float (&gm)[CP], const float (&be)[CP]) {
     float v[V];
     x.get(v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = fmaf((v[i] - mean) * rstd, gm[i], be[i]);
+    for (int i = 0; i < V; ++i) v[i] = fmaf((v[i] - mean) * rstd, gm[i % CP], be[i % CP]);
     act_all(a.act, v);
     Piece<IO, V>::store(to, v);
 }
 
 // xh and dz = dy act'(gamma xh + beta) of one piece
-template <typename IO, int V>
+template <typename IO, int V, int CP>
 __device__ __forceinline__ void get_dz(const NormArgs& a, const Piece<IO, V>& x, const Piece<IO, V>& dy, float mean,
-                                       float rstd, const float (&gm)[V], const float (&be)[V], float (&xh)[V],
+                                       float rstd, const float (&gm)[CP], const float (&be)[CP], float (&xh)[V],
                                        float (&dz)[V]) {
     float z[V];
     x.get(xh);
@@ -145,17 +146,17 @@ __device__ __forceinline__ void get_dz(const NormArgs& a, const Piece<IO, V>& x,
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         xh[i] = (xh[i] - mean) * rstd;
-        z[i] = fmaf(xh[i], gm[i], be[i]);
+        z[i] = fmaf(xh[i], gm[i % CP], be[i % CP]);
     }
     slope_all(a.act, z, dz);
 }
 
-template <typename IO, int V>
-__device__ __forceinline__ void put_dx(IO* to, const float (&xh)[V], const float (&dz)[V], const float (&gm)[V],
+template <typename IO, int V, int CP>
+__device__ __forceinline__ void put_dx(IO* to, const float (&xh)[V], const float (&dz)[V], const float (&gm)[CP],
                                        float m1, float m2, float rstd) {
     float v[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (fmaf(dz[i], gm[i], -m1) - xh[i] * m2) * rstd;
+    for (int i = 0; i < V; ++i) v[i] = (fmaf(dz[i], gm[i % CP], -m1) - xh[i] * m2) * rstd;
     Piece<IO, V>::store(to, v);
 }
 
@@ -183,7 +184,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Slabs are numbered token by token, group by group; a wave takes 64 / lps of them at
 // once, a lane K pieces of its slab.  Waves step by whole tokens, so a lane keeps its
 // group.  The next token's pieces load while the current one's are worked on.
-template <typename IO, int V, int K>
+template <typename IO, int V, int CP, int K>
 __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
@@ -191,12 +192,12 @@ __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
     const int64_t slab = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / s.lps) + lane / s.lps;
     int64_t t = slab / a.groups;
     const int g = (int)(slab - t * a.groups), e0 = g * s.W;
-    float gm[K][V], be[K][V];
+    float gm[K][CP], be[K][CP];
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         in[k] = sub + k * s.lps < s.cols;
-        affine<IO, V>(a, e0 + (in[k] ? (sub + k * s.lps) * V : 0), gm[k], be[k]);
+        affine<IO>(a, e0 + (in[k] ? (sub + k * s.lps) * V : 0), gm[k], be[k]);
     }
     const float inv = 1.0f / (float)s.W;
     const IO* x = (const IO*)a.x + e0 + sub * V;
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
         if (t < a.T) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (in[k]) put_y<IO, V>(a, y + t * a.ldy + k * s.lps * V, now[k], mean, rstd, gm[k], be[k]);
+                if (in[k]) put_y<IO>(a, y + t * a.ldy + k * s.lps * V, now[k], mean, rstd, gm[k], be[k]);
             if (a.stats && sub == 0) *reinterpret_cast<float2*>(a.stats + 2 * (t * a.groups + g)) = float2{mean, rstd};
         }
 #pragma unroll
@@ -241,24 +242,24 @@ __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
 
 // The same slabs; the lane's sums of dz xh and dz over its tokens go, through LDS, to
 // part[workgroup] as sums per channel.
-template <typename IO, int V, int K>
+template <typename IO, int V, int CP, int K>
 __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
-    __shared__ float acc[256 * K * V];  // [slab of the workgroup][its numbers, lps K V]
+    __shared__ float acc[256 * K * CP];  // [slab of the workgroup][its sums, lps K CP]
     const int lane = (int)threadIdx.x & 63, sub = lane & (s.lps - 1), spw = 64 / s.lps;
     const int here = (int)(threadIdx.x >> 6) * spw + lane / s.lps;
     const int64_t base = (int64_t)blockIdx.x * 4 * spw, slab = base + here;
     int64_t t = slab / a.groups;
     const int g = (int)(slab - t * a.groups), e0 = g * s.W;
-    float gm[K][V], be[K][V], dg[K][V], db[K][V];
+    float gm[K][CP], be[K][CP], dg[K][CP], db[K][CP];
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         in[k] = sub + k * s.lps < s.cols;
-        affine<IO, V>(a, e0 + (in[k] ? (sub + k * s.lps) * V : 0), gm[k], be[k]);
+        affine<IO>(a, e0 + (in[k] ? (sub + k * s.lps) * V : 0), gm[k], be[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dg[k][i] = db[k][i] = 0.0f;
+        for (int i = 0; i < CP; ++i) dg[k][i] = db[k][i] = 0.0f;
     }
     const float inv = 1.0f / (float)s.W;
     const IO* x = (const IO*)a.x + e0 + sub * V;
@@ -285,40 +286,41 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
         float xh[K][V], dz[K][V], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            get_dz<IO, V>(a, xc[k], dc[k], st.x, st.y, gm[k], be[k], xh[k], dz[k]);
+            get_dz<IO>(a, xc[k], dc[k], st.x, st.y, gm[k], be[k], xh[k], dz[k]);
+            // (a piece past the slab or the last token has dy = 0 and adds nothing)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float d = in[k] && t < a.T ? dz[k][i] : 0.0f;
-                dg[k][i] = in[k] && t < a.T ? fmaf(d, xh[k][i], dg[k][i]) : dg[k][i];
-                db[k][i] += d;
-                s1 = fmaf(d, gm[k][i], s1);
-                s2 = in[k] && t < a.T ? fmaf(d * gm[k][i], xh[k][i], s2) : s2;
+                dg[k][i % CP] = fmaf(dz[k][i], xh[k][i], dg[k][i % CP]);
+                db[k][i % CP] += dz[k][i];
+                const float g = dz[k][i] * gm[k][i % CP];
+                s1 += g;
+                s2 = fmaf(g, xh[k][i], s2);
             }
         }
         const float m1 = lane_sum(s1, s.lps) * inv, m2 = lane_sum(s2, s.lps) * inv;
         if (t < a.T) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (in[k]) put_dx<IO, V>(dx + t * a.lddx + k * s.lps * V, xh[k], dz[k], gm[k], m1, m2, st.y);
+                if (in[k]) put_dx<IO>(dx + t * a.lddx + k * s.lps * V, xh[k], dz[k], gm[k], m1, m2, st.y);
         }
         t += s.step;
     }
     if (!s.part) return;
-    const int width = s.lps * K * V, g0 = (int)(base % a.groups), slabs = 4 * spw;
+    const int width = s.lps * K * CP, per = a.N * CP / V, g0 = (int)(base % a.groups), slabs = 4 * spw;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                acc[here * width + (sub + k * s.lps) * V + i] = q == 0 ? dg[k][i] : db[k][i];
+            for (int i = 0; i < CP; ++i)
+                acc[here * width + (sub + k * s.lps) * CP + i] = q == 0 ? dg[k][i] : db[k][i];
         __syncthreads();
         for (int c = (int)threadIdx.x; c < a.C; c += 256) {
-            const int gc = c / s.cpg, at = (c - gc * s.cpg) * a.N;
+            const int gc = c / s.cpg, at = (c - gc * s.cpg) * per;
             float v = 0.0f;
             for (int j = (gc - g0 + a.groups) % a.groups; j < slabs; j += a.groups)
-                for (int n = 0; n < a.N; ++n) v += acc[j * width + at + n];
+                for (int n = 0; n < per; ++n) v += acc[j * width + at + n];
             s.part[((int64_t)blockIdx.x * 2 + q) * a.C + c] = v;
         }
     }
@@ -329,7 +331,7 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
 // tokens row, row + rows, ... of its piece, K of them in registers; tokens past those
 // (in packed batches, where one sample can be much longer than the mean) are read again
 // in each pass.
-template <typename IO, int V, int K, int NT>
+template <typename IO, int V, int CP, int K, int NT>
 __global__ __launch_bounds__(NT) void slab_forward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
@@ -338,8 +340,8 @@ __global__ __launch_bounds__(NT) void slab_forward_kernel(Norm s) {
     const int row = tid / s.cols, col = tid - row * s.cols;
     const bool on = row < s.rows;
     const int e = g * s.W + (on ? col : 0) * V;
-    float gm[V], be[V];
-    affine<IO, V>(a, e, gm, be);
+    float gm[CP], be[CP];
+    affine<IO>(a, e, gm, be);
     for (int64_t b = blockIdx.x / (uint32_t)a.groups; b < a.batch; b += s.step) {
         int64_t t0, t1;
         sample_range(a, b, t0, t1);
@@ -386,17 +388,17 @@ __global__ __launch_bounds__(NT) void slab_forward_kernel(Norm s) {
         for (int k = 0; k < K; ++k) {
             const int64_t t = row + (int64_t)k * s.rows;
             p[k].keep_packed();
-            if (on && t < n) put_y<IO, V>(a, y + t * a.ldy, p[k], mean, rstd, gm, be);
+            if (on && t < n) put_y<IO>(a, y + t * a.ldy, p[k], mean, rstd, gm, be);
         }
         for (int64_t t = over; t < n; t += s.rows)
-            put_y<IO, V>(a, y + t * a.ldy, P::load(x + t * a.ldx), mean, rstd, gm, be);
+            put_y<IO>(a, y + t * a.ldy, P::load(x + t * a.ldx), mean, rstd, gm, be);
         if (a.stats && tid == 0)
             *reinterpret_cast<float2*>(a.stats + 2 * (b * a.groups + g)) = float2{mean, rstd};
     }
 }
 
-// Sums over the rows of a workgroup of each piece's numbers, then over each channel's
-// N numbers, to out[channel].  acc: NT V floats.
+// Sums over the rows of a workgroup of each piece's V sums, then over each channel's N
+// of them, to out[channel].  acc: NT V floats.
 template <int V, int NT>
 __device__ __forceinline__ void channel_sums(const float (&v)[V], float* acc, int rows, int cols, int n_channels, int N,
                                              float* out) {
@@ -419,21 +421,21 @@ __device__ __forceinline__ void channel_sums(const float (&v)[V], float* acc, in
     }
 }
 
-template <typename IO, int V, int K, int NT>
-__global__ __launch_bounds__(NT) void slab_backward_kernel(Norm s) {
+template <typename IO, int V, int CP, int K, int NT>
+__global__ __launch_bounds__(NT, K == 6 && CP == 1 ? 4 : 2) void slab_backward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
     __shared__ float red[NT / 64];
-    __shared__ float acc[NT * V];
+    __shared__ float acc[NT * CP];
     const int g = (int)(blockIdx.x % (uint32_t)a.groups), tid = (int)threadIdx.x;
     const int64_t part = blockIdx.x / (uint32_t)a.groups;
     const int row = tid / s.cols, col = tid - row * s.cols;
     const bool on = row < s.rows;
     const int e = g * s.W + (on ? col : 0) * V;
-    float gm[V], be[V], dg[V], db[V];
-    affine<IO, V>(a, e, gm, be);
+    float gm[CP], be[CP], dg[CP], db[CP];
+    affine<IO>(a, e, gm, be);
 #pragma unroll
-    for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
+    for (int i = 0; i < CP; ++i) dg[i] = db[i] = 0.0f;
     for (int64_t b = part; b < a.batch; b += s.step) {
         int64_t t0, t1;
         sample_range(a, b, t0, t1);
@@ -442,32 +444,52 @@ __global__ __launch_bounds__(NT) void slab_backward_kernel(Norm s) {
         const IO* dy = (const IO*)a.dy + t0 * a.lddy + e;
         IO* dx = (IO*)a.dx + t0 * a.lddx + e;
         const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * (b * a.groups + g));
-        P px[K], pd[K];
-        float xh[V], dz[V], sg[V], sb[V];
+        P px[K];
+        float d[K][V];  // dy, then dz: the slope is the costly part, and taken once
+        float xh[V], dz[V], sg[CP], sb[CP];
+        {
+            P pd[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int64_t t = row + (int64_t)k * s.rows;
-            px[k] = on && t < n ? P::load(x + t * a.ldx) : P::zero();
-            pd[k] = on && t < n ? P::load(dy + t * a.lddy) : P::zero();
+            for (int k = 0; k < K; ++k) {
+                const int64_t t = row + (int64_t)k * s.rows;
+                px[k] = on && t < n ? P::load(x + t * a.ldx) : P::zero();
+                pd[k] = on && t < n ? P::load(dy + t * a.lddy) : P::zero();
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) pd[k].get(d[k]);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) sg[i] = sb[i] = 0.0f;
+        for (int i = 0; i < CP; ++i) sg[i] = sb[i] = 0.0f;
         auto add = [&](const P& xp, const P& dp) {
-            get_dz<IO, V>(a, xp, dp, st.x, st.y, gm, be, xh, dz);
+            get_dz<IO>(a, xp, dp, st.x, st.y, gm, be, xh, dz);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                sg[i] = fmaf(dz[i], xh[i], sg[i]);
-                sb[i] += dz[i];
+                sg[i % CP] = fmaf(dz[i], xh[i], sg[i % CP]);
+                sb[i % CP] += dz[i];
             }
         };
         const int64_t over = on ? row + (int64_t)K * s.rows : n;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && row + (int64_t)k * s.rows < n) add(px[k], pd[k]);
+        for (int k = 0; k < K; ++k) {  // (pieces past the sample have dy = 0 and add nothing)
+            __builtin_amdgcn_sched_barrier(0);  // piece by piece: mixed, they take twice the registers
+            float z[V];
+            px[k].get(xh);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                xh[i] = (xh[i] - st.x) * st.y;
+                z[i] = fmaf(xh[i], gm[i % CP], be[i % CP]);
+            }
+            slope_all(a.act, z, d[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sg[i % CP] = fmaf(d[k][i], xh[i], sg[i % CP]);
+                sb[i % CP] += d[k][i];
+            }
+        }
         for (int64_t t = over; t < n; t += s.rows) add(P::load(x + t * a.ldx), P::load(dy + t * a.lddy));
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < CP; ++i) {
             s1 = fmaf(sb[i], gm[i], s1);
             s2 = fmaf(sg[i], gm[i], s2);
             dg[i] += sg[i];
@@ -479,21 +501,23 @@ __global__ __launch_bounds__(NT) void slab_backward_kernel(Norm s) {
         for (int k = 0; k < K; ++k) {
             const int64_t t = row + (int64_t)k * s.rows;
             px[k].keep_packed();
-            pd[k].keep_packed();
+            __builtin_amdgcn_sched_barrier(0);
             if (on && t < n) {
-                get_dz<IO, V>(a, px[k], pd[k], st.x, st.y, gm, be, xh, dz);
-                put_dx<IO, V>(dx + t * a.lddx, xh, dz, gm, m1, m2, st.y);
+                px[k].get(xh);
+#pragma unroll
+                for (int i = 0; i < V; ++i) xh[i] = (xh[i] - st.x) * st.y;
+                put_dx<IO>(dx + t * a.lddx, xh, d[k], gm, m1, m2, st.y);
             }
         }
         for (int64_t t = over; t < n; t += s.rows) {
-            get_dz<IO, V>(a, P::load(x + t * a.ldx), P::load(dy + t * a.lddy), st.x, st.y, gm, be, xh, dz);
-            put_dx<IO, V>(dx + t * a.lddx, xh, dz, gm, m1, m2, st.y);
+            get_dz<IO>(a, P::load(x + t * a.ldx), P::load(dy + t * a.lddy), st.x, st.y, gm, be, xh, dz);
+            put_dx<IO>(dx + t * a.lddx, xh, dz, gm, m1, m2, st.y);
         }
     }
     if (!s.part) return;
     float* to = s.part + part * 2 * a.C + g * s.cpg;
-    channel_sums<V, NT>(dg, acc, s.rows, s.cols, s.cpg, a.N, to);
-    channel_sums<V, NT>(db, acc, s.rows, s.cols, s.cpg, a.N, to + a.C);
+    channel_sums<CP, NT>(dg, acc, s.rows, s.cols, s.cpg, a.N * CP / V, to);
+    channel_sums<CP, NT>(db, acc, s.rows, s.cols, s.cpg, a.N * CP / V, to + a.C);
 }
 
 // --- split path -----------------------------------------------------------------------
@@ -663,7 +687,7 @@ __global__ __launch_bounds__(256) void apply_forward_kernel(Norm s) {
     const RowTile<IO, V> rt(s);
     if (!rt.on) return;
     float gm[V], be[V];
-    affine<IO, V>(a, rt.e, gm, be);
+    affine<IO>(a, rt.e, gm, be);
     const float2 st = *reinterpret_cast<const float2*>(s.joined + 2 * (k.b * a.groups + rt.g));
     const IO* x = (const IO*)a.x + rt.e;
     IO* y = (IO*)a.y + rt.e;
@@ -674,7 +698,7 @@ __global__ __launch_bounds__(256) void apply_forward_kernel(Norm s) {
             p[u] = t + u * rt.rows < k.t1 ? P::load(x + (t + u * rt.rows) * a.ldx) : P::zero();
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u * rt.rows < k.t1) put_y<IO, V>(a, y + (t + u * rt.rows) * a.ldy, p[u], st.x, st.y, gm, be);
+            if (t + u * rt.rows < k.t1) put_y<IO>(a, y + (t + u * rt.rows) * a.ldy, p[u], st.x, st.y, gm, be);
     }
 }
 
@@ -692,7 +716,7 @@ __global__ __launch_bounds__(256) void sums_kernel(Norm s) {
     const RowTile<IO, V> rt(s);
     const int tid = (int)threadIdx.x;
     float gm[V], be[V], dg[V], db[V], xh[V], dz[V];
-    affine<IO, V>(a, rt.e, gm, be);
+    affine<IO>(a, rt.e, gm, be);
 #pragma unroll
     for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
     if (!k.idle && rt.on) {
@@ -710,7 +734,7 @@ __global__ __launch_bounds__(256) void sums_kernel(Norm s) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t + u * rt.rows < k.t1) {
-                    get_dz<IO, V>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
+                    get_dz<IO>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         dg[i] = fmaf(dz[i], xh[i], dg[i]);
@@ -778,7 +802,7 @@ __global__ __launch_bounds__(256) void apply_backward_kernel(Norm s) {
     const RowTile<IO, V> rt(s);
     if (!rt.on) return;
     float gm[V], be[V], xh[V], dz[V];
-    affine<IO, V>(a, rt.e, gm, be);
+    affine<IO>(a, rt.e, gm, be);
     const int64_t slab = k.b * a.groups + rt.g;
     const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * slab);
     const float2 m = *reinterpret_cast<const float2*>(s.joined + 2 * slab);
@@ -796,8 +820,8 @@ __global__ __launch_bounds__(256) void apply_backward_kernel(Norm s) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (t + u * rt.rows < k.t1) {
-                get_dz<IO, V>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
-                put_dx<IO, V>(dx + (t + u * rt.rows) * a.lddx, xh, dz, gm, m.x, m.y, st.y);
+                get_dz<IO>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
+                put_dx<IO>(dx + (t + u * rt.rows) * a.lddx, xh, dz, gm, m.x, m.y, st.y);
             }
     }
 }
@@ -849,9 +873,9 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // The smallest workgroup of the slab path whose registers hold a sample of `mean`
 // tokens, K pieces a thread; false: none.
-// (The backward holds x and dy: half the pieces at the largest.)
+// (The backward holds x and dz: half the pieces at the largest.)
 bool slab_shape(Choice& c, int64_t mean, bool backward) {
-    const int shapes[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {16, 256}, {backward ? 8 : 16, 512}};
+    const int shapes[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {6, 512}, {backward ? 8 : 16, 512}};
     for (const auto& k : shapes)
         if (c.cols <= k[1] && mean <= (int64_t)k[0] * (k[1] / c.cols)) {
             c.K = k[0];
@@ -880,7 +904,7 @@ Choice choose(int V, int C, int N, int groups, int64_t T, int64_t batch, bool ra
         c.wgs = round_up(want < cap ? want : cap, unit);
         c.step = c.wgs * per / groups;
         c.part = backward ? (size_t)c.wgs * 2 * C * 4 : 0;
-    } else if (slab_shape(c, mean, backward) && (c.NT <= 256 || batch * groups >= 128)) {
+    } else if (slab_shape(c, mean, backward) && (c.K <= 8 || batch * groups >= 128)) {
         c.path = kSlab;
         c.rows = c.NT / c.cols;
         const int64_t cap = (backward ? 2048 : 8192) / groups;
@@ -926,7 +950,7 @@ Norm norm_of(const NormArgs& a, const Choice& c, void* ws, bool backward) {
     return s;
 }
 
-template <typename IO, int V>
+template <typename IO, int V, int CP>
 hipError_t forward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     const Choice c = choose(V, a.C, a.N, a.groups, a.T, a.batch, a.offsets != nullptr, false);
     const Norm s = norm_of(a, c, ws, false);
@@ -934,17 +958,17 @@ hipError_t forward_v(const NormArgs& a, void* ws, hipStream_t stream) {
         if (c.wgs > 0x7fffffff) return hipErrorNotSupported;
         const dim3 grid((uint32_t)c.wgs);
         switch (c.K) {
-            case 1: hipLaunchKernelGGL((token_forward_kernel<IO, V, 1>), grid, dim3(256), 0, stream, s); break;
-            case 2: hipLaunchKernelGGL((token_forward_kernel<IO, V, 2>), grid, dim3(256), 0, stream, s); break;
-            default: hipLaunchKernelGGL((token_forward_kernel<IO, V, 4>), grid, dim3(256), 0, stream, s);
+            case 1: hipLaunchKernelGGL((token_forward_kernel<IO, V, CP, 1>), grid, dim3(256), 0, stream, s); break;
+            case 2: hipLaunchKernelGGL((token_forward_kernel<IO, V, CP, 2>), grid, dim3(256), 0, stream, s); break;
+            default: hipLaunchKernelGGL((token_forward_kernel<IO, V, CP, 4>), grid, dim3(256), 0, stream, s);
         }
     } else if (c.path == kSlab) {
         if (c.wgs > 0x7fffffff) return hipErrorNotSupported;
         const dim3 grid((uint32_t)c.wgs);
 #define EQL_SLAB(k, nt)                                                                                       \
     if (c.K == k && c.NT == nt)                                                                                \
-        hipLaunchKernelGGL((slab_forward_kernel<IO, V, k, nt>), grid, dim3(nt), 0, stream, s);
-        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256) EQL_SLAB(16, 256) EQL_SLAB(16, 512)
+        hipLaunchKernelGGL((slab_forward_kernel<IO, V, CP, k, nt>), grid, dim3(nt), 0, stream, s);
+        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256) EQL_SLAB(6, 512) EQL_SLAB(16, 512)
 #undef EQL_SLAB
     } else {
         const int64_t tiles = ((int64_t)c.cols * a.groups + 255) / 256;
@@ -959,7 +983,7 @@ hipError_t forward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename IO, int V>
+template <typename IO, int V, int CP>
 hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     const Choice c = choose(V, a.C, a.N, a.groups, a.T, a.batch, a.offsets != nullptr, true);
     Norm s = norm_of(a, c, ws, true);
@@ -972,9 +996,9 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
         if (c.wgs > 0x7fffffff) return hipErrorNotSupported;
         const dim3 grid((uint32_t)c.wgs);
         switch (c.K) {
-            case 1: hipLaunchKernelGGL((token_backward_kernel<IO, V, 1>), grid, dim3(256), 0, stream, s); break;
-            case 2: hipLaunchKernelGGL((token_backward_kernel<IO, V, 2>), grid, dim3(256), 0, stream, s); break;
-            default: hipLaunchKernelGGL((token_backward_kernel<IO, V, 4>), grid, dim3(256), 0, stream, s);
+            case 1: hipLaunchKernelGGL((token_backward_kernel<IO, V, CP, 1>), grid, dim3(256), 0, stream, s); break;
+            case 2: hipLaunchKernelGGL((token_backward_kernel<IO, V, CP, 2>), grid, dim3(256), 0, stream, s); break;
+            default: hipLaunchKernelGGL((token_backward_kernel<IO, V, CP, 4>), grid, dim3(256), 0, stream, s);
         }
         parts = c.wgs;
     } else if (c.path == kSlab) {
@@ -983,8 +1007,8 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
         const dim3 grid((uint32_t)c.wgs);
 #define EQL_SLAB(k, nt)                                                                                       \
     if (c.K == k && c.NT == nt)                                                                                \
-        hipLaunchKernelGGL((slab_backward_kernel<IO, V, k, nt>), grid, dim3(nt), 0, stream, s);
-        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256) EQL_SLAB(16, 256) EQL_SLAB(8, 512)
+        hipLaunchKernelGGL((slab_backward_kernel<IO, V, CP, k, nt>), grid, dim3(nt), 0, stream, s);
+        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256) EQL_SLAB(6, 512) EQL_SLAB(8, 512)
 #undef EQL_SLAB
         parts = c.step;
     } else {
@@ -1004,18 +1028,20 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
 
 template <typename IO>
 hipError_t forward(int io, const NormArgs& a, void* ws, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(IO);
     const int W = a.C / a.groups * a.N;
     if (wide_ok(io, a.x, a.ldx, W) && wide_ok(io, a.y, a.ldy, W))
-        return forward_v<IO, 16 / sizeof(IO)>(a, ws, stream);
-    return forward_v<IO, 1>(a, ws, stream);
+        return a.N % V == 0 ? forward_v<IO, V, 1>(a, ws, stream) : forward_v<IO, V, V>(a, ws, stream);
+    return forward_v<IO, 1, 1>(a, ws, stream);
 }
 
 template <typename IO>
 hipError_t backward(int io, const NormArgs& a, void* ws, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(IO);
     const int W = a.C / a.groups * a.N;
     if (wide_ok(io, a.x, a.ldx, W) && wide_ok(io, a.dy, a.lddy, W) && wide_ok(io, a.dx, a.lddx, W))
-        return backward_v<IO, 16 / sizeof(IO)>(a, ws, stream);
-    return backward_v<IO, 1>(a, ws, stream);
+        return a.N % V == 0 ? backward_v<IO, V, 1>(a, ws, stream) : backward_v<IO, V, V>(a, ws, stream);
+    return backward_v<IO, 1, 1>(a, ws, stream);
 }
 
 }  // namespace

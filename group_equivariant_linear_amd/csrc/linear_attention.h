@@ -37,8 +37,10 @@ struct Job {
     // segments: runs of seg_len tokens (whole chunks) of a sequence, each a
     // workgroup's; part holds the state before each segment (0: one per sequence)
     int64_t seg_len, slots;
+    int64_t mean;      // T / batch
+    uint32_t per_seq;  // segments of each sequence (no offsets)
     float* part;
-    int out_vec;  // output rows in whole pieces of four
+    int out_vec;  // rows of out in whole pieces of four
 };
 
 // The products of one launch: workgroups first[k] .. first[k + 1] - 1 take jobs[k].
@@ -49,15 +51,17 @@ struct Jobs {
     int count;
 };
 
-__device__ __forceinline__ void sequence(const int64_t* offsets, int64_t batch, int64_t T, int64_t b, int64_t& t0,
-                                         int64_t& t1) {
-    if (offsets) {
-        t0 = offsets[b], t1 = offsets[b + 1];
-        t0 = t0 < 0 ? 0 : (t0 > T ? T : t0);
-        t1 = t1 < t0 ? t0 : (t1 > T ? T : t1);
+__device__ __forceinline__ int64_t offset_of(const Job& j, int64_t b) {
+    const int64_t o = j.offsets[b];
+    return o < 0 ? 0 : (o > j.T ? j.T : o);
+}
+
+__device__ __forceinline__ void sequence(const Job& j, int64_t b, int64_t& t0, int64_t& t1) {
+    if (j.offsets) {
+        t0 = offset_of(j, b), t1 = offset_of(j, b + 1);
+        t1 = t1 < t0 ? t0 : t1;
     } else {
-        const int64_t n = T / batch;
-        t0 = b * n, t1 = t0 + n;
+        t0 = b * j.mean, t1 = t0 + j.mean;
     }
 }
 
@@ -70,39 +74,30 @@ struct Segment {
     bool idle;
 };
 
-__device__ __forceinline__ Segment segment_of(const Job& j, int64_t slot) {
+__device__ __forceinline__ Segment segment_of(const Job& j, uint32_t slot) {
     Segment s;
-    int64_t first_slot;
-    if (j.seg_len == 0) {
-        s.b = slot;
-        first_slot = slot;
-    } else if (!j.offsets) {
-        const int64_t n = j.T / j.batch, per = (n + j.seg_len - 1) / j.seg_len;
-        s.b = slot / per;
-        first_slot = s.b * per;
-    } else {
-        int64_t lo = 0, hi = j.batch - 1;  // last b whose first slot is at most `slot`
+    uint32_t first_slot = slot;
+    s.b = slot;
+    if (j.seg_len && !j.offsets) {
+        s.b = slot / j.per_seq;
+        first_slot = (uint32_t)s.b * j.per_seq;
+    } else if (j.seg_len) {
+        uint32_t lo = 0, hi = (uint32_t)j.batch - 1;  // last b whose first slot is at most `slot`
         while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) / 2;
-            int64_t o = j.offsets[mid];
-            o = o < 0 ? 0 : (o > j.T ? j.T : o);
-            if (o / j.seg_len + mid <= slot) lo = mid;
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (offset_of(j, mid) / j.seg_len + mid <= slot) lo = mid;
             else hi = mid - 1;
         }
         s.b = lo;
-        int64_t o = j.offsets[lo];
-        o = o < 0 ? 0 : (o > j.T ? j.T : o);
-        first_slot = o / j.seg_len + lo;
+        first_slot = (uint32_t)(offset_of(j, lo) / j.seg_len) + lo;
     }
     int64_t q0, q1;
-    sequence(j.offsets, j.batch, j.T, s.b, q0, q1);
-    if (j.seg_len == 0) {
-        s.t0 = q0, s.t1 = q1;
-        s.first = s.last = true;
-        s.idle = false;
-        return s;
-    }
-    s.t0 = q0 + (slot - first_slot) * j.seg_len;
+    sequence(j, s.b, q0, q1);
+    s.t0 = q0, s.t1 = q1;
+    s.first = s.last = true;
+    s.idle = false;
+    if (j.seg_len == 0) return s;
+    s.t0 = q0 + (int64_t)(slot - first_slot) * j.seg_len;
     s.t1 = s.t0 + j.seg_len < q1 ? s.t0 + j.seg_len : q1;
     s.first = slot == first_slot;
     s.last = s.t1 == q1;
@@ -118,7 +113,7 @@ __device__ __forceinline__ float power(float l2, int n) {
 // --- matrix-core operands of the three types ----------------------------------------
 // A fragment holds, in each lane, KF numbers along the contraction: KS over the four
 // lane groups kg = lane / 16, at row (column) lane % 16 of the operand; group kg has
-// positions KF kg .. KF kg + KF - 1.
+// positions KF kg .. KF kg + KF - 1: in a row-major tile one 16-byte piece.
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -128,23 +123,20 @@ template <typename IO>
 struct Op {  // __bf16, _Float16
     using F = typename Half<IO>::x8;
     static constexpr int KS = 32, KF = 8, ES = 2;
+    static constexpr bool BF = std::is_same_v<IO, __bf16>;
     // terms in which an fp32 number enters a product without loss of its fp32 accuracy
-    static constexpr int TERMS = std::is_same_v<IO, __bf16> ? 3 : 2;
+    static constexpr int TERMS = BF ? 3 : 2;
     static __device__ __forceinline__ void mma(f32x4& acc, const F& a, const F& b) {
-        if constexpr (std::is_same_v<IO, __bf16>) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+        if constexpr (BF) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
         else acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
     }
-    static __device__ __forceinline__ F row(const char* p) { return *reinterpret_cast<const F*>(p); }
-    // Columns of a row-major tile: contraction along its rows row0 + 8 kg + 0..7.  A
-    // transposed read takes 4 rows x 4 runs of 4 columns from each group of 16 lanes
-    // (lane 4r + u points at row r, run u) and hands lane 4u + v column v of run u.
-    // Run u starts at column col0 + step u.
-    static __device__ __forceinline__ F column(const char* tile, int pitch, int row0, int col0, int step) {
-        const int lane = (int)threadIdx.x & 63, kg = lane >> 4, i = lane & 15;
-        const char* p = tile + (row0 + 8 * kg + (i >> 2)) * pitch + (col0 + step * (i & 3)) * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * pitch));
-        return __builtin_bit_cast(F, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    // Two transposed reads: 4 rows x 4 runs of 4 columns from each group of 16 lanes (lane
+    // 4r + u points at row r, run u) to lane 4u + v: column v of run u.  lo: rows 8 kg +
+    // 0..3 of the contraction, hi: 8 kg + 4..7.
+    static __device__ __forceinline__ F column(const char* lo, const char* hi) {
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lo));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(hi));
+        return __builtin_bit_cast(F, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     static __device__ __forceinline__ float get(const F& f, int e) { return (float)f[e]; }
     // infinities and NaN as 0
@@ -153,7 +145,8 @@ struct Op {  // __bf16, _Float16
         for (int e = 0; e < KF; ++e) f[e] = fabsf((float)f[e]) < __builtin_inff() ? f[e] : (IO)0.0f;
         return f;
     }
-    // v (8 numbers) as TERMS fragments, each the rounding of what the ones before left
+    // v (8 numbers) as N fragments, each what the ones before left, cut off (not rounded:
+    // the next term holds the rest exactly; three bf16 or two fp16 terms hold 22 bits or more)
     template <int N>
     static __device__ __forceinline__ void split(const float (&v)[8], F (&out)[N]) {
         float r[8];
@@ -164,18 +157,29 @@ struct Op {  // __bf16, _Float16
             u32x4 u;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                u[q] = Half<IO>::pack2(r[2 * q], r[2 * q + 1]);
-                if (t + 1 < N) {
-                    r[2 * q] -= Half<IO>::lo(u[q]);
-                    r[2 * q + 1] -= Half<IO>::hi(u[q]);
+                float& x = r[2 * q];
+                float& y = r[2 * q + 1];
+                if constexpr (BF) {
+                    u[q] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+                    if (t + 1 < N) {
+                        x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+                        y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+                    }
+                } else {
+                    u[q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(x, y));
+                    if (t + 1 < N) {
+                        x -= Half<IO>::lo(u[q]);
+                        y -= Half<IO>::hi(u[q]);
+                    }
                 }
             }
             out[t] = __builtin_bit_cast(F, u);
         }
     }
-    // whether a piece of memory holds an infinity or a NaN
-    static __device__ __forceinline__ bool odd(const u32x4& v) {
-        constexpr unsigned short top = std::is_same_v<IO, __bf16> ? 0x7f80 : 0x7c00;
+    // whether a fragment holds an infinity or a NaN
+    static __device__ __forceinline__ bool odd(const F& f) {
+        const u32x4 v = __builtin_bit_cast(u32x4, f);
+        constexpr unsigned short top = BF ? 0x7f80 : 0x7c00;
         u16x2 m = {0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[q] & 0x7fff7fffu));
@@ -187,19 +191,10 @@ template <>
 struct Op<float> {
     using F = f32x4;
     static constexpr int KS = 16, KF = 4, ES = 4, TERMS = 1;
+    static constexpr bool BF = false;
     static __device__ __forceinline__ void mma(f32x4& acc, const F& a, const F& b) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
-    }
-    static __device__ __forceinline__ F row(const char* p) { return *reinterpret_cast<const F*>(p); }
-    // column lane % 16 of the 16 that the runs name
-    static __device__ __forceinline__ F column(const char* tile, int pitch, int row0, int col0, int step) {
-        const int lane = (int)threadIdx.x & 63, kg = lane >> 4, i = lane & 15;
-        const char* p = tile + (row0 + 4 * kg) * pitch + (col0 + step * (i >> 2) + (i & 3)) * 4;
-        F f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(p + e * pitch);
-        return f;
     }
     static __device__ __forceinline__ float get(const F& f, int e) { return f[e]; }
     static __device__ __forceinline__ F finite(F f) {
@@ -211,11 +206,9 @@ struct Op<float> {
     static __device__ __forceinline__ void split(const float (&v)[4], F (&out)[N]) {
         out[0] = F{v[0], v[1], v[2], v[3]};
     }
-    static __device__ __forceinline__ bool odd(const u32x4& v) {
-        bool b = false;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) b |= (v[q] & 0x7f800000u) == 0x7f800000u;
-        return b;
+    static __device__ __forceinline__ bool odd(const F& f) {
+        return !(fabsf(f[0]) < __builtin_inff() && fabsf(f[1]) < __builtin_inff() && fabsf(f[2]) < __builtin_inff() &&
+                 fabsf(f[3]) < __builtin_inff());
     }
 };
 
@@ -240,113 +233,187 @@ __device__ __forceinline__ u32x4 load_piece(const IO* row, int col, int D) {
 
 // The kernel's shape: D_a padded to 32 KB, D_c to 16 NW, NW waves; wave w owns
 // columns 16 w .. 16 w + 15 of the state and of the output.
-template <typename IO_, int KB_, int NW_>
+template <typename IO_, int KB_, int NW_, bool OUT_>
 struct Cfg {
     using IO = IO_;
     using O = Op<IO_>;
+    static constexpr bool OUT = OUT_;
     static constexpr int ES = O::ES, KB = KB_, NW = NW_, NT = 64 * NW_;
-    static constexpr int DA = 32 * KB_, DC = 16 * NW_, NB = DA / 16, NM = DA / O::KS, NS = kChunk / O::KS;
-    // row pitches: an odd number of 16-byte pieces, so that 16 rows spread over the banks
-    static constexpr int PA = DA * ES + 16, PC = DC * ES + 16, PP = kChunk * ES + 16;
-    static constexpr int E = 16 / ES, PPA = DA / E, PPC = DC / E;  // numbers of a piece; pieces of a row
-    static constexpr int NPA = (kChunk * PPA + NT - 1) / NT, NPC = (kChunk * PPC + NT - 1) / NT;
-    static constexpr int OFF_B = kChunk * PA, OFF_C = 2 * kChunk * PA, OFF_P = OFF_C + kChunk * PC;
-    static constexpr int OFF_FLAG = OFF_P + kChunk * PP, LDS = OFF_FLAG + 16;
+    static constexpr int DA = 32 * KB_, NB = DA / 16, NM = DA / O::KS, NS = kChunk / O::KS;
+    static constexpr int E = 16 / ES;                                // numbers of a piece
+    static constexpr int PA = DA / E, PC = 16 / E, PP = kChunk / E;  // pieces of a row of a and b, c, P
+    // a and b of the next chunk load into a second tile while this one is worked on
+    // (wide fp32 tiles leave no room for it)
+    static constexpr bool TWO = !OUT_ || ES == 2 || KB_ <= 2;
+    static constexpr int TILE = kChunk * PA * 16, CTILE = kChunk * PC * 16;
+    static constexpr int OFF_B = OUT_ ? (TWO ? 2 : 1) * TILE : 0;
+    static constexpr int OFF_C = OFF_B + (TWO ? 2 : 1) * TILE;
+    static constexpr int OFF_P = OFF_C + NW * CTILE, LDS = OFF_P + (OUT_ ? kChunk * PP * 16 : 0);
+    static constexpr int NPA = (PA + NW - 1) / NW;  // loads of a wave per a or b tile, 64 pieces each
+};
+
+// Row-major tiles of P pieces a row: piece p of row r lies at piece p ^ fold(r).  A read
+// of fragments along the rows takes the same piece of 16 rows; one along the columns four
+// neighbouring pieces of rows r .. r + 3 (16-bit types) or r, r + 4, r + 8, r + 12 (fp32).
+// fold() spreads both over the 256 bytes of the LDS banks: the rows of a column read to
+// different 64-byte windows (bits 2 and up; rows of 64 and 192 bytes are there already),
+// the others to the four pieces of a window.
+template <int ES, int P>
+__device__ __forceinline__ constexpr int fold(int r) {
+    const int near = ES == 2 ? r : r >> 2, far = ES == 2 ? (r >> 2) & 3 : r & 3;
+    if (P % 16 == 0) return (near & 3) << 2 | far;
+    if (P % 8 == 0) return (ES == 2 ? (r >> 1) & 1 : near & 1) << 2 | far;
+    return far;
+}
+template <int ES, int P>
+__device__ __forceinline__ int place(int r, int p) {
+    return (r * P + (p ^ fold<ES, P>(r))) * 16;
+}
+
+// Fragments along the rows of such a tile: rows 16 q + lane % 16, contraction step m
+// (pieces 4 m + lane group).  fold() is the same in all blocks q; its high bits permute
+// the steps within a run of four.
+template <int ES, int P>
+struct RowReader {
+    static constexpr int N = P / 4 < 4 ? P / 4 : (P % 16 == 0 ? 4 : 2);
+    const char* base[N];
+    __device__ __forceinline__ explicit RowReader(const char* tile) {
+        const int lane = (int)threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) base[i] = tile + place<ES, P>(lane & 15, 4 * i + (lane >> 4)) - 64 * i;
+    }
+    // of the tile `at` bytes on
+    template <typename F>
+    __device__ __forceinline__ F get(int q, int m, int at) const {
+        return *reinterpret_cast<const F*>(base[m % N] + at + q * (16 * P * 16) + m * 64);
+    }
+};
+
+// Fragments along its columns: block a of 16 columns (in the order of state_row),
+// contraction over rows KS m + ...
+template <class C>
+struct ColumnReader {
+    static constexpr int P = C::PA, ES = C::ES;
+    const char* base[2][C::KB];  // 16-bit types: rows + 0 and + 4, columns from 32 k
+    const char* tile;
+    __device__ __forceinline__ explicit ColumnReader(const char* t) : tile(t) {
+        if constexpr (ES == 2) {
+            const int lane = (int)threadIdx.x & 63, r = 8 * (lane >> 4) + ((lane & 15) >> 2), u = lane & 3;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < C::KB; ++k) base[h][k] = t + place<ES, P>(r + 4 * h, 4 * k + u);
+        }
+    }
+    // of the tile `at` bytes on
+    __device__ __forceinline__ typename C::O::F get(int a, int m, int at) const {
+        if constexpr (ES == 2) {
+            const int off = at + (a & 1) * 8 + m * (32 * P * 16);
+            return C::O::column(base[0][a >> 1] + off, base[1][a >> 1] + off);
+        } else {
+            const int lane = (int)threadIdx.x & 63, kg = lane >> 4, ln = lane & 15;
+            typename C::O::F f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = *reinterpret_cast<const float*>(tile + at + place<ES, P>(16 * m + 4 * kg + e, 4 * a + (ln >> 2)) +
+                                                       (ln & 3) * 4);
+            return f;
+        }
+    }
 };
 
 // Row of the state that lane group kg holds as element i of block a: such that the
 // blocks of one contraction step are, in order, that step's positions of the group.
+// (16-bit: run u of block a starts at column 32 (a / 2) + 4 (a % 2) + 8 u of the b tile.)
 template <class C>
 __device__ __forceinline__ int state_row(int a, int kg, int i) {
     if constexpr (C::ES == 2) return 32 * (a >> 1) + 8 * kg + 4 * (a & 1) + i;
     else return 16 * a + 4 * kg + i;
 }
-// first column and step of the runs that give those rows as columns of the b tile
-template <class C>
-__device__ __forceinline__ int state_col0(int a) {
-    return C::ES == 2 ? 32 * (a >> 1) + 4 * (a & 1) : 16 * a;
-}
-constexpr int state_step(int es) { return es == 2 ? 8 : 4; }
 
 __device__ __forceinline__ float uniform(float v) {
     return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
 
-// The b (c) tile's pieces of this thread: piece tid + k NT is 16 bytes of row
-// (tid + k NT) / PPR.  VEC: rows are whole aligned pieces, read through a buffer
-// resource over the chunk's rows, offsets past which read zeros.
-template <typename IO, int PPR, int NT, int NP, bool VEC>
+// Loads of 64 rows into a tile of P pieces a row (folded or in order), NP per wave, 64
+// pieces each: columns from `col` on, the tile's slots in order.  VEC: rows are whole aligned pieces; they go
+// straight to LDS through a buffer resource over the chunk's rows, which reads zeros past
+// its last row and (by an offset past any resource) past column D.
+template <typename IO, int P, int NP, bool FOLD, bool VEC>
 struct Loader {
     static constexpr int ES = (int)sizeof(IO), E = 16 / ES;
     uint32_t off[VEC ? NP : 1];
-    __device__ __forceinline__ Loader(const Heads& x, int D) {
+    static __device__ __forceinline__ void where(int i, int& row, int& piece) {
+        const int slot = 64 * i + ((int)threadIdx.x & 63);
+        row = slot / P;
+        piece = FOLD ? slot % P ^ fold<ES, P>(row) : slot % P;
+    }
+    // first: the wave's first load; step: from one of its loads to the next
+    __device__ __forceinline__ Loader(const Heads& x, int D, int col, int first, int step) {
         if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int p = (int)threadIdx.x + k * NT, row = p / PPR, col = p % PPR * E;
-                off[k] = row < kChunk && col < D ? (uint32_t)row * (uint32_t)x.ts * ES + (uint32_t)col * ES : kOOB;
+                int row, piece;
+                where(first + k * step, row, piece);
+                off[k] = col + piece * E < D ? (uint32_t)row * (uint32_t)x.ts * ES + (uint32_t)(col + piece * E) * ES
+                                             : kOOB;
             }
         }
     }
-    // rows t .. t + n - 1 of head h
-    __device__ __forceinline__ void load(const Heads& x, int64_t t, int64_t h, int n, int D, u32x4 (&r)[NP]) const {
+    // rows t .. t + n - 1 of head h to the tile at `to`
+    __device__ __forceinline__ void run(const Heads& x, int64_t t, int64_t h, int n, int D, int col, int first, int step,
+                                        char* to) const {
         const IO* base = (const IO*)x.p + t * x.ts + h * x.hs;
         if constexpr (VEC) {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)(((n - 1) * x.ts + D) * ES));
-            if (n == kChunk) {
 #pragma unroll
-                for (int k = 0; k < NP; ++k) r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, off[k], 0, 0);
-            } else {  // (strides below a row's width: later rows may lie inside the resource)
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    const int row = ((int)threadIdx.x + k * NT) / PPR;
-                    r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < n ? off[k] : kOOB, 0, 0);
-                }
+            for (int k = 0; k < NP; ++k) {
+                const int i = first + k * step;
+                const uint32_t o = off[k];  // (an array element given straight to the builtin loses the host stub)
+                if (i < P)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        rs, (__attribute__((address_space(3))) void*)(to + i * 1024), 16, o, 0, 0, 0);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int p = (int)threadIdx.x + k * NT, row = p / PPR;
-                r[k] = u32x4{0u, 0u, 0u, 0u};
-                if (row < n) r[k] = load_piece<IO>(base + row * x.ts, p % PPR * E, D);
+                const int i = first + k * step;
+                if (i >= P) continue;
+                int row, piece;
+                where(i, row, piece);
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (row < n) v = load_piece<IO>(base + row * x.ts, col + piece * E, D);
+                *reinterpret_cast<u32x4*>(to + i * 1024 + ((int)threadIdx.x & 63) * 16) = v;
             }
-        }
-    }
-    static __device__ __forceinline__ void stage(char* to, int pitch, const u32x4 (&r)[NP]) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int p = (int)threadIdx.x + k * NT;
-            if (kChunk * PPR % NT == 0 || p < kChunk * PPR)
-                *reinterpret_cast<u32x4*>(to + (p / PPR) * pitch + (p % PPR) * 16) = r[k];
         }
     }
 };
 
-// Waves per SIMD that the registers are held to: as many as the LDS allows, except
-// where that would spill.
+// Waves per SIMD that the registers are held to.
 template <class C>
-constexpr int kWaves = C::NW == 8 ? 2 : (C::ES == 2 ? (C::KB <= 2 ? 3 : 2) : (C::KB <= 2 ? 2 : 1));
+constexpr int kWaves = C::ES == 4 ? (C::NW == 8 || C::KB == 1 ? 2 : 1) : (C::NW == 8 ? 2 : (C::KB <= 2 ? 3 : 2));
 
 // Chunks of 64 tokens, in time order or (reversed) from the end.  Per chunk, and per
 // head of b and c that shares the state:
 //   1. scores P[t][s] = scale g^|t-s| (a_t . b_s) of the causal half, to LDS in the
 //      plan dtype, split over the waves by 16 x 16 blocks;
 //   2. wave w, for its 16 columns of out^T: the old state (two terms) times a, decayed
-//      per token in fp32, plus c^T P^T;
+//      per token in fp32;
 //   3. the state's 16 columns: S = g^n S + b^T (decayed c), the decayed c in as many
-//      terms as keep the state's fp32 accuracy.
+//      terms as keep the state's fp32 accuracy;
+//   4. out^T += c^T P^T, and the rows of out go to memory.
 // The state never leaves its wave's registers: the accumulator of step 3 is, in its
-// lanes, the operand of step 2.  OUT: the whole; else step 3 alone, and the state
-// goes to part[slot].
-template <class C, bool OUT, bool VEC>
+// lanes, the operand of step 2.  Two barriers a chunk: the tiles of a and b are there;
+// P is there (and the tiles are free).  A wave loads its own columns of c.
+// OUT: the whole; else step 3 alone, and the state goes to part[slot].
+template <class C, bool VEC>
 __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     using IO = typename C::IO;
     using O = typename C::O;
     using F = typename O::F;
-    constexpr int NS = C::NS, KF = O::KF;
+    constexpr bool OUT = C::OUT, TWO = C::TWO;
+    constexpr int NS = C::NS, KF = O::KF, ES = C::ES;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
-    char *const ta = lds, *const tb = lds + C::OFF_B, *const tc = lds + C::OFF_C, *const tp = lds + C::OFF_P;
-    volatile int* const flag = reinterpret_cast<volatile int*>(lds + C::OFF_FLAG);
 
     // consecutive workgroups (heads of one sequence, which may share b and c) on one XCD
     const uint32_t wg = xcd_remap(blockIdx.x, gridDim.x);
@@ -357,8 +424,8 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kg = lane >> 4, ln = lane & 15;
     const int Hkv = j.Ha < j.Hb ? j.Ha : j.Hb, heads = OUT ? j.Ha : Hkv;
-    const int64_t slot = id / (uint32_t)heads;
-    const int hx = (int)(id % (uint32_t)heads);
+    const uint32_t slot = id / (uint32_t)heads;
+    const int hx = (int)(id - slot * (uint32_t)heads);
     const int r = j.Ha > j.Hb ? j.Ha / j.Hb : 1;   // heads of a per state
     const int rb = j.Hb > j.Ha ? j.Hb / j.Ha : 1;  // heads of b and c per state
     const int kv = OUT ? hx / r : hx;
@@ -370,16 +437,40 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 
     const float l2 = uniform(j.log_decay[kv] * kLog2e);
     const int n_tok = (int)(seg.t1 - seg.t0), n_chunks = (n_tok + kChunk - 1) / kChunk;
+    const int total = n_chunks * rb;
     const bool own = 16 * wave < j.Dc;  // waves past D_c only load and score
     const int dc = 16 * wave + ln;
     const int64_t state_at = (seg.b * Hkv + kv) * (int64_t)j.Da * j.Dc;
+    const int sgn = rev ? -1 : 1;
+
+    char *const tile_a = lds, *const tile_b = lds + C::OFF_B;
+    char *const tc = lds + C::OFF_C + wave * C::CTILE, *const tp = lds + C::OFF_P;
+    const Loader<IO, C::PA, C::NPA, true, VEC> la(j.a, j.Da, 0, wave, C::NW), lb(j.b, j.Da, 0, wave, C::NW);
+    const Loader<IO, C::PC, C::PC, false, VEC> lc(j.c, j.Dc, 16 * wave, 0, 1);
+    auto rows_of = [&](int64_t t) { return (int)(seg.t1 - t < kChunk ? seg.t1 - t : kChunk); };
+    auto load_a = [&](int64_t t, int buf) {
+        if constexpr (OUT) la.run(j.a, t, hx, rows_of(t), j.Da, 0, wave, C::NW, tile_a + buf * C::TILE);
+    };
+    auto load_b = [&](int64_t t, int hh, int buf) {
+        lb.run(j.b, t, kv * rb + hh, rows_of(t), j.Da, 0, wave, C::NW, tile_b + buf * C::TILE);
+    };
+    auto load_c = [&](int64_t t, int hh) {
+        if (own) lc.run(j.c, t, kv * rb + hh, rows_of(t), j.Dc, 16 * wave, 0, 1, tc);
+    };
+
+    int64_t t = seg.t0 + (rev ? (int64_t)(n_chunks - 1) * kChunk : 0);
+    if (total > 0) {
+        load_a(t, 0);
+        load_b(t, 0, 0);
+        load_c(t, 0);
+    }
 
     f32x4 S[C::NB];
 #pragma unroll
     for (int a = 0; a < C::NB; ++a) S[a] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (OUT && own) {
         if (j.seg_len) {
-            const float* p = j.part + ((slot * Hkv + kv) * C::NW + wave) * (int64_t)(C::NB * 256) + lane * 4;
+            const float* p = j.part + (((int64_t)slot * Hkv + kv) * C::NW + wave) * (int64_t)(C::NB * 256) + lane * 4;
 #pragma unroll
             for (int a = 0; a < C::NB; ++a) S[a] = *reinterpret_cast<const f32x4*>(p + a * 256);
         } else if (j.S0) {
@@ -396,255 +487,311 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 
     // Decays, the same in every whole chunk: of the scores (within a diagonal block, one
     // block apart; g^16 per further block), of the old state at a token (g^16 per block
-    // of tokens), of a token's weight in the new state (step m, lane group, element e).
-    const int sgn = rev ? -1 : 1;
+    // of tokens), of a token's weight in the new state (step m and lane group; element e).
     float near0[4], near1[4], wb[NS], we[KF];
     const float g16 = uniform(power(l2, 16)), g64 = uniform(power(l2, kChunk));
+    float old = 0.0f;
+    if constexpr (OUT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = sgn * (ln - (4 * kg + i));  // t - s (s - t reversed) on the diagonal
-        near0[i] = d >= 0 ? j.scale * power(l2, d) : 0.0f;
-        near1[i] = j.scale * power(l2, 16 + d);
+        for (int i = 0; i < 4; ++i) {
+            const int d = sgn * (ln - (4 * kg + i));  // t - s (s - t reversed) on the diagonal
+            near0[i] = d >= 0 ? j.scale * power(l2, d) : 0.0f;
+            near1[i] = j.scale * power(l2, 16 + d);
+        }
+        old = j.scale * power(l2, rev ? 16 - ln : 1 + ln);
+        // blocks of P above (reversed: below) the diagonal that step 4 reads with their neighbours
+        for (int i = tid; i < kChunk * C::PP; i += C::NT) reinterpret_cast<u32x4*>(tp)[i] = u32x4{0u, 0u, 0u, 0u};
     }
-    const float old = j.scale * power(l2, rev ? 16 - ln : 1 + ln);
 #pragma unroll
     for (int m = 0; m < NS; ++m)
         wb[m] = power(l2, rev ? O::KS * m + KF * kg : kChunk - O::KS * m - KF * (kg + 1));
+    {
+        const float g1 = power(l2, 1);
+        float up[KF];
+        up[0] = 1.0f;
 #pragma unroll
-    for (int e = 0; e < KF; ++e) we[e] = uniform(power(l2, rev ? e : KF - 1 - e));
-    if (OUT) {
-        for (int i = tid; i < kChunk * C::PP / 16; i += C::NT) reinterpret_cast<u32x4*>(tp)[i] = u32x4{0u, 0u, 0u, 0u};
+        for (int e = 1; e < KF; ++e) up[e] = up[e - 1] * g1;
+#pragma unroll
+        for (int e = 0; e < KF; ++e) we[e] = uniform(rev ? up[e] : up[KF - 1 - e]);
     }
-    if (tid < 2) flag[tid] = 0;
-    __syncthreads();
 
-    u32x4 ra[OUT ? C::NPA : 1], rbv[C::NPA], rc[C::NPC];
-    const Loader<IO, C::PPA, C::NT, C::NPA, VEC> la(j.a, j.Da), lb(j.b, j.Da);
-    const Loader<IO, C::PPC, C::NT, C::NPC, VEC> lc(j.c, j.Dc);
-    const int total = n_chunks * rb;
-    auto load = [&](int64_t t, int hh) {  // chunk from t, head hh of those that share the state
-        const int n = (int)(seg.t1 - t < kChunk ? seg.t1 - t : kChunk);
-        if constexpr (OUT) {
-            if (hh == 0) la.load(j.a, t, hx, n, j.Da, ra);
-        }
-        lb.load(j.b, t, kv * rb + hh, n, j.Da, rbv);
-        lc.load(j.c, t, kv * rb + hh, n, j.Dc, rc);
-    };
+    const RowReader<ES, C::PA> rows(lds);
+    const RowReader<ES, C::PP> rp(lds);
+    const ColumnReader<C> cb(lds);
+    // 16 x 64 tokens of c: its columns of a wave alone, rows of 16 numbers
+    const char* const c_lo = ES == 2 ? tc + (8 * kg + (ln >> 2)) * 32 + (ln & 3) * 8 : tc + kg * 256 + ln * 4;
+
+    // the rows of out: element offsets of this lane's four columns at token 16 q + ln
+    const uint32_t out_row = (uint32_t)j.out.ts * ES, out_at = (uint32_t)ln * out_row + (uint32_t)(16 * wave + 4 * kg) * ES;
 
     f32x4 acc[4];
-    int64_t t = seg.t0 + (rev ? (int64_t)(n_chunks - 1) * kChunk : 0);
     int hh = 0, left = n_chunks;  // chunks from this one on
-    if (total > 0) load(t, 0);
+    int ba = 0, bb = 0;           // tiles in use
+    bool stored = false;          // four stores went out after this wave's last loads
     for (int it = 0; it < total; ++it) {
-        const int n = (int)(seg.t1 - t < kChunk ? seg.t1 - t : kChunk), nq = (n + 15) / 16;
-        if constexpr (OUT) {
-            if (hh == 0) la.stage(ta, C::PA, ra);
-        }
-        lb.stage(tb, C::PA, rbv);
-        lc.stage(tc, C::PC, rc);
-        if constexpr (OUT) {
-            bool odd = false;
-#pragma unroll
-            for (int k = 0; k < C::NPC; ++k) odd |= O::odd(rc[k]);
-            if (odd) flag[it & 1] = 1;
-        }
+        const int n = rows_of(t), nq = (n + 15) / 16;
+        const bool last_head = hh + 1 == rb, more = it + 1 < total;
+        const int64_t tn = last_head ? t + sgn * kChunk : t;  // of the next iteration
+        const int hn = last_head ? 0 : hh + 1;
+        // the tiles' loads are older than the last rows' stores, which need not be waited for
+        if (stored) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        stored = false;
         __syncthreads();
-        if (it + 1 < total) {
-            if (hh + 1 < rb) load(t, hh + 1);
-            else load(t + sgn * kChunk, 0);
-        }
-
-        if constexpr (OUT) {
-            // 1. block idx of the lower triangle, row by row; reversed its transpose, and
-            // keys in whole 32-token steps
-            const int nk = rev ? (n + 31) / 32 * 2 : nq;
-            for (int idx = wave; idx < 10; idx += C::NW) {
-                const int hi = idx >= 6 ? 3 : (idx >= 3 ? 2 : (idx >= 1 ? 1 : 0));
-                const int lo = idx - hi * (hi + 1) / 2;
-                const int qb = rev ? lo : hi, kb = rev ? hi : lo;
-                if (qb >= nq || kb >= nk) continue;
-                f32x4 s = {0.f, 0.f, 0.f, 0.f};
-                const char* pb = tb + (16 * kb + ln) * C::PA + KF * kg * C::ES;
-                const char* pa = ta + (16 * qb + ln) * C::PA + KF * kg * C::ES;
-#pragma unroll
-                for (int m = 0; m < C::NM; ++m)
-                    O::mma(s, O::row(pb + O::KS * m * C::ES), O::row(pa + O::KS * m * C::ES));
-                float p[4];
-                if (hi == lo) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = sgn * (ln - (4 * kg + i)) >= 0 ? s[i] * near0[i] : 0.0f;
-                } else {
-                    const float f = hi - lo == 1 ? 1.0f : (hi - lo == 2 ? g16 : g16 * g16);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = s[i] * (near1[i] * f);
-                }
-                char* to = tp + (16 * qb + ln) * C::PP + (16 * kb + 4 * kg) * C::ES;
-                if constexpr (C::ES == 2)
-                    *reinterpret_cast<u32x2*>(to) = u32x2{Half<IO>::pack2(p[0], p[1]), Half<IO>::pack2(p[2], p[3])};
-                else
-                    *reinterpret_cast<f32x4*>(to) = f32x4{p[0], p[1], p[2], p[3]};
+        if constexpr (TWO) {
+            if (more) {
+                if (last_head) load_a(tn, ba ^ 1);
+                load_b(tn, hn, bb ^ 1);
             }
-            __syncthreads();
         }
+        const int oa = ba * C::TILE, ob = C::OFF_B + bb * C::TILE;
 
-        if (own) {
-            // the chunk's columns of c: contraction over its tokens
-            F ct[NS];
+        // reversed, the initial state belongs to the last token itself: no decay before it
+        const int e0 = (rev && initial_seg && left == n_chunks) ? 0 : 1;
+        const bool keep = !OUT || left > 1 || (j.S1 && final_seg && hx % r == 0);  // the state is needed on
+
+        // The chunk's arithmetic, without branches between its products: a whole chunk; part
+        // of one; at most 16 tokens.
+        auto chunk = [&](auto full_c, auto nq_c) {
+            constexpr bool FULL = decltype(full_c)::value;
+            constexpr int NQ = decltype(nq_c)::value, NM_T = (16 * NQ + O::KS - 1) / O::KS;  // blocks, steps of tokens
+            // (the rare paths compute their indexes where they are: hoisted out of the loop they
+            // would take the registers that the whole chunks need)
+            int lnp = ln, kgp = kg;
+            if constexpr (!FULL) asm volatile("" : "+v"(lnp), "+v"(kgp));
+            // the chunk's columns of c, contraction over its tokens
+            F ct[NM_T];
+            if (own) {
 #pragma unroll
-            for (int m = 0; m < NS; ++m) ct[m] = O::column(tc, C::PC, O::KS * m, 16 * wave, 4);
-            // reversed, the initial state belongs to the last token itself: no decay before it
-            const int e0 = (rev && initial_seg && left == n_chunks) ? 0 : 1;
-            if constexpr (OUT) {
-                // 2.
-                if (hh == 0) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    float norm = 1.0f, inv_norm = 1.0f;  // fp16: the state scaled into its range, by a power of two
-                    if constexpr (std::is_same_v<IO, _Float16>) {
-                        float mx = 0.0f;
-#pragma unroll
-                        for (int a = 0; a < C::NB; ++a)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[a][i]));
-#pragma unroll
-                        for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-                        int ex = 0;
-                        if (mx > 0.0f && mx < __builtin_inff()) (void)frexpf(mx, &ex);
-                        ex = ex < -100 ? -100 : ex;
-                        norm = ldexpf(1.0f, ex);
-                        inv_norm = ldexpf(1.0f, -ex);
-                    }
-#pragma unroll
-                    for (int m = 0; m < C::NM; ++m) {
-                        constexpr int ST = C::ES == 2 ? 2 : 1;
-                        F st[ST];
-                        float v[KF];
-#pragma unroll
-                        for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * inv_norm;
-                        O::split(v, st);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q < nq) {
-                                const F at = O::row(ta + (16 * q + ln) * C::PA + (O::KS * m + KF * kg) * C::ES);
-#pragma unroll
-                                for (int x = 0; x < ST; ++x) O::mma(acc[q], st[x], at);
-                            }
-                    }
-                    if (n == kChunk && e0 == 1) {
-                        float f = old * norm;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            acc[rev ? 3 - q : q] *= f;
-                            f *= g16;
-                        }
+                for (int m = 0; m < NM_T; ++m) {
+                    if constexpr (ES == 2) {
+                        ct[m] = O::column(c_lo + m * 1024, c_lo + m * 1024 + 128);
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int tq = 16 * q + ln, d = (rev ? n - 1 - tq : tq) + e0;
-                            acc[q] *= norm * j.scale * power(l2, d > 0 ? d : 0);
-                        }
+                        for (int e = 0; e < 4; ++e) ct[m][e] = *reinterpret_cast<const float*>(c_lo + m * 1024 + e * 64);
                     }
                 }
-                // An infinity or NaN among the chunk's values: 0 times it must not reach the
-                // outputs that do not see it, so the product takes 0 in its place (the other
-                // outputs keep their bits) and those that do see it add it one by one.
-                const int odd = __builtin_amdgcn_readfirstlane(flag[it & 1]);
-                F cf[NS];
+            }
+            if constexpr (OUT) {
+                // 1. blocks of the lower triangle, row by row; reversed its transpose, with the keys
+                // of a part of a chunk in whole steps of 32
+                constexpr int BLOCKS = NQ == 1 ? 3 : 10;
 #pragma unroll
-                for (int m = 0; m < NS; ++m) cf[m] = ct[m];
-                if (odd) {
+                for (int k = 0; k < (BLOCKS + C::NW - 1) / C::NW; ++k) {
+                    const int idx = wave + k * C::NW;
+                    if (idx >= BLOCKS) continue;
+                    const int hi = idx >= 6 ? 3 : (idx >= 3 ? 2 : (idx >= 1 ? 1 : 0));
+                    const int lo = idx - hi * (hi + 1) / 2;
+                    const int qb = rev ? lo : hi, kb = rev ? hi : lo;
+                    if (!FULL && qb >= nq) continue;
+                    f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int m = 0; m < NS; ++m) cf[m] = O::finite(ct[m]);
-                }
+                    for (int m = 0; m < C::NM; ++m)
+                        O::mma(s, rows.template get<F>(kb, m, ob), rows.template get<F>(qb, m, oa));
+                    const bool diag = hi == lo;
+                    const float f = hi - lo <= 1 ? 1.0f : (hi - lo == 2 ? g16 : g16 * g16);
+                    float p[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int m = 0; m < NS; ++m) {
-                        const bool sees = rev ? O::KS * (m + 1) > 16 * q && O::KS * m < n : O::KS * m < 16 * (q + 1);
-                        if (q < nq && sees)
-                            O::mma(acc[q], cf[m], O::row(tp + (16 * q + ln) * C::PP + (O::KS * m + KF * kg) * C::ES));
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = diag ? near0[i] : near1[i] * f;
+                        p[i] = diag && w == 0.0f ? 0.0f : s[i] * w;  // (a NaN among the masked scores: 0)
                     }
-                if (odd) {
+                    const int row = 16 * qb + ln;
+                    if constexpr (ES == 2)
+                        *reinterpret_cast<u32x2*>(tp + place<ES, C::PP>(row, 2 * kb + (kg >> 1)) + (kg & 1) * 8) =
+                            u32x2{Half<IO>::pack2(p[0], p[1]), Half<IO>::pack2(p[2], p[3])};
+                    else
+                        *reinterpret_cast<f32x4*>(tp + place<ES, C::PP>(row, 4 * kb + kg)) = f32x4{p[0], p[1], p[2], p[3]};
+                }
+            }
+            // the columns of c are in registers: the next chunk's may take their place, unless
+            // step 4 has to come back to them
+            bool odd = false;
+            if (own) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        for (int s = 0; s < n; ++s) {
-                            const int tq = 16 * q + ln;
-                            if (rev ? s < tq : s > tq) continue;
-                            const float p = (float)*reinterpret_cast<const IO*>(tp + tq * C::PP + s * C::ES);
+                for (int m = 0; m < NM_T; ++m) odd |= O::odd(ct[m]);
+                odd = OUT && __any(odd);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (more && !odd) load_c(tn, hn);
+            }
+            // the steps stay apart: mixed, they would not fit the registers
+            __builtin_amdgcn_sched_barrier(0);
+            if (own) {
+                if constexpr (OUT) {
+                    // 2.
+                    if (hh == 0) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float v = (float)*reinterpret_cast<const IO*>(
-                                    tc + s * C::PC + (16 * wave + 4 * kg + i) * C::ES);
-                                if (!(fabsf(v) < __builtin_inff())) acc[q][i] = fmaf(p, v, acc[q][i]);
+                        for (int q = 0; q < NQ; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        float norm = 1.0f, inv_norm = 1.0f;  // fp16: a state out of its range scaled by a power of two
+                        if constexpr (std::is_same_v<IO, _Float16>) {
+                            float mx = 0.0f;
+#pragma unroll
+                            for (int a = 0; a < C::NB; ++a)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[a][i]));
+                            if (__any(mx > 32768.0f) || (!__any(mx > 0.03125f) && __any(mx > 0.0f))) {
+#pragma unroll
+                                for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+                                int ex = 0;
+                                if (mx < __builtin_inff()) (void)frexpf(mx, &ex);
+                                ex = ex < -100 ? -100 : ex;
+                                norm = uniform(ldexpf(1.0f, ex));
+                                inv_norm = uniform(ldexpf(1.0f, -ex));
                             }
                         }
-                }
-                if (hh == rb - 1) {
-                    const int c0 = 16 * wave + 4 * kg;
-                    IO* out = (IO*)const_cast<void*>(j.out.p) + t * j.out.ts + hx * j.out.hs;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int tq = 16 * q + ln;
-                        if (tq >= n) continue;
-                        IO* p = out + tq * j.out.ts + c0;
-                        if (j.out_vec && c0 + 3 < j.Dc) {
-                            if constexpr (C::ES == 2)
-                                *reinterpret_cast<u32x2*>(p) = u32x2{Half<IO>::pack2(acc[q][0], acc[q][1]),
-                                                                     Half<IO>::pack2(acc[q][2], acc[q][3])};
-                            else
-                                *reinterpret_cast<f32x4*>(p) = acc[q];
+                        for (int m = 0; m < C::NM; ++m) {
+                            constexpr int ST = ES == 2 ? 2 : 1;
+                            F st[ST], at[NQ];
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) at[q] = rows.template get<F>(q, m, oa);
+                            float v[KF];
+#pragma unroll
+                            for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * inv_norm;
+                            O::split(v, st);
+#pragma unroll
+                            for (int x = 0; x < ST; ++x)
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q) O::mma(acc[q], st[x], at[q]);
+                            if (m % 2) __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if constexpr (FULL) {
+                            float d[4];
+                            d[0] = norm * (e0 ? old : j.scale * power(l2, 15 - ln));
+                            d[1] = d[0] * g16, d[2] = d[1] * g16, d[3] = d[2] * g16;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) acc[q] *= rev ? d[3 - q] : d[q];
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (c0 + i < j.Dc) p[i] = (IO)acc[q][i];
+                            for (int q = 0; q < NQ; ++q) {
+                                const int tq = 16 * q + lnp, d = (rev ? n - 1 - tq : tq) + e0;
+                                acc[q] *= norm * j.scale * power(l2, d > 0 ? d : 0);
+                            }
                         }
                     }
                 }
-            }
-            // 3.
-            if (!OUT || left > 1 || (j.S1 && final_seg && hx % r == 0)) {
-                if (hh == 0) {
-                    const float carry = n == kChunk && e0 == 1 ? g64 : power(l2, n - 1 + e0);
+                // 3.
+                __builtin_amdgcn_sched_barrier(0);
+                if (keep) {
+                    if (hh == 0) {
+                        const float carry = FULL ? (e0 ? g64 : power(l2, kChunk - 1)) : power(l2, n - 1 + e0);
 #pragma unroll
-                    for (int a = 0; a < C::NB; ++a) S[a] *= carry;
-                }
+                        for (int a = 0; a < C::NB; ++a) S[a] *= carry;
+                    }
 #pragma unroll
-                for (int m = 0; m < NS; ++m) {
-                    if (O::KS * m >= n) continue;
-                    float v[KF];
-                    if (rev || n == kChunk) {
-#pragma unroll
-                        for (int e = 0; e < KF; ++e) v[e] = O::get(ct[m], e) * (wb[m] * we[e]);
-                    } else {
+                    for (int m = 0; m < NM_T; ++m) {
+                        float v[KF];
 #pragma unroll
                         for (int e = 0; e < KF; ++e) {
-                            const int d = n - 1 - (O::KS * m + KF * kg + e);
-                            v[e] = O::get(ct[m], e) * power(l2, d > 0 ? d : 0);
+                            if constexpr (FULL) {
+                                v[e] = O::get(ct[m], e) * we[e] * wb[m];
+                            } else {
+                                const int s = O::KS * m + KF * kgp + e, d = rev ? s : n - 1 - s;
+                                v[e] = O::get(ct[m], e) * power(l2, d > 0 ? d : 0);
+                            }
                         }
-                    }
-                    F cw[O::TERMS];
-                    O::split(v, cw);
+                        F cw[O::TERMS];
+                        O::split(v, cw);
 #pragma unroll
-                    for (int a = 0; a < C::NB; ++a) {
-                        const F bt = O::column(tb, C::PA, O::KS * m, state_col0<C>(a), state_step(C::ES));
+                        for (int a = 0; a < C::NB; ++a) {
+                            const F bt = cb.get(a, m, ob);
 #pragma unroll
-                        for (int x = 0; x < O::TERMS; ++x) O::mma(S[a], bt, cw[x]);
+                            for (int x = 0; x < O::TERMS; ++x) O::mma(S[a], bt, cw[x]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
+            __syncthreads();  // P is there; the tiles of a and b are free
+            if constexpr (!TWO) {
+                if (more) {
+                    if (last_head) load_a(tn, 0);
+                    load_b(tn, hn, 0);
+                }
+            }
+            if constexpr (OUT) {
+                if (own) {
+                    // 4.  An infinity or NaN among the chunk's values: 0 times it must not reach the
+                    // outputs that do not see it, so the product takes 0 in its place (the other
+                    // outputs keep their bits) and those that do see it add it one by one.
+                    if (odd) {
+#pragma unroll
+                        for (int m = 0; m < NM_T; ++m) ct[m] = O::finite(ct[m]);
+                    }
+                    // (P is 0 in the blocks that are not written)
+#pragma unroll
+                    for (int m = 0; m < NM_T; ++m)
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) O::mma(acc[q], ct[m], rp.template get<F>(q, m, C::OFF_P));
+                    if (odd) {
+                        int lno = ln, kgo = kg;
+                        asm volatile("" : "+v"(lno), "+v"(kgo));
+                        for (int s = 0; s < n; ++s)
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                const int tq = 16 * q + lno;
+                                if (rev ? s < tq : s > tq) continue;
+                                const float p =
+                                    (float)*reinterpret_cast<const IO*>(tp + place<ES, C::PP>(tq, s / C::E) + s % C::E * ES);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float v = (float)*reinterpret_cast<const IO*>(tc + (s * 16 + 4 * kgo + i) * ES);
+                                    if (!(fabsf(v) < __builtin_inff())) acc[q][i] = fmaf(p, v, acc[q][i]);
+                                }
+                            }
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        if (more) load_c(tn, hn);
+                    }
+                    if (last_head) {
+                        IO* out = (IO*)const_cast<void*>(j.out.p) + t * j.out.ts + hx * j.out.hs;
+                        if (j.out_vec) {
+                            asm volatile("" ::: "memory");  // the loads above stay older than these
+                            __builtin_amdgcn_sched_barrier(0);
+                            const __amdgpu_buffer_rsrc_t ro = make_rsrc(out, (uint32_t)(((n - 1) * j.out.ts + j.Dc) * ES));
+                            const bool in = 16 * wave + 4 * kg < j.Dc;
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                const uint32_t at = in && (FULL || 16 * q + lnp < n) ? out_at + 16 * q * out_row : kOOB;
+                                if constexpr (ES == 2)
+                                    __builtin_amdgcn_raw_buffer_store_b64(
+                                        u32x2{Half<IO>::pack2(acc[q][0], acc[q][1]), Half<IO>::pack2(acc[q][2], acc[q][3])},
+                                        ro, at, 0, 0);
+                                else
+                                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[q]), ro, at, 0, 0);
+                            }
+                            stored = NQ == 4;
+                        } else {
+                            int lno = ln, kgo = kg;
+                            asm volatile("" : "+v"(lno), "+v"(kgo));
+                            const int c0 = 16 * wave + 4 * kgo;
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                if (16 * q + lno >= n) continue;
+                                IO* p = out + (16 * q + lno) * j.out.ts + c0;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (c0 + i < j.Dc) p[i] = (IO)acc[q][i];
+                            }
+                        }
+                    }
+                }
+            }
+        };
+        if (n == kChunk) chunk(std::true_type{}, std::integral_constant<int, 4>{});
+        else if (n > 16) chunk(std::false_type{}, std::integral_constant<int, 4>{});
+        else chunk(std::false_type{}, std::integral_constant<int, 1>{});
+        if constexpr (TWO) {
+            bb ^= 1;
+            if (last_head) ba ^= 1;
         }
-        __syncthreads();
-        if (tid == 0) flag[it & 1] = 0;  // the next writer comes after the next barrier
-        if (++hh == rb) {
-            hh = 0;
-            t += sgn * kChunk;
-            --left;
-        }
+        t = tn;
+        hh = hn;
+        if (last_head) --left;
     }
 
     if (!own) return;
     if (!OUT) {
-        float* p = j.part + ((slot * Hkv + kv) * C::NW + wave) * (int64_t)(C::NB * 256) + lane * 4;
+        float* p = j.part + (((int64_t)slot * Hkv + kv) * C::NW + wave) * (int64_t)(C::NB * 256) + lane * 4;
 #pragma unroll
         for (int a = 0; a < C::NB; ++a) *reinterpret_cast<f32x4*>(p + a * 256) = S[a];
     } else if (j.S1 && final_seg && hx % r == 0) {
@@ -674,7 +821,7 @@ __global__ __launch_bounds__(256) void join_kernel(Jobs jobs) {
     const int dc = 16 * wave + (lane & 15);
     if (16 * wave >= j.Dc) return;
     int64_t t0, t1;
-    sequence(j.offsets, j.batch, j.T, b, t0, t1);
+    sequence(j, b, t0, t1);
     const int64_t segs = t1 > t0 ? (t1 - t0 + j.seg_len - 1) / j.seg_len : 1;
     const int64_t slot0 = j.offsets ? t0 / j.seg_len + b : b * segs;
     const float l2 = j.log_decay[kv] * kLog2e;
@@ -719,7 +866,8 @@ inline int waves_for(int Dc) { return Dc <= 64 ? 4 : 8; }
 
 template <typename IO, int KB, int NW, bool VEC>
 hipError_t run_cfg(Jobs& jobs, hipStream_t stream) {
-    using C = Cfg<IO, KB, NW>;
+    using C = Cfg<IO, KB, NW, true>;
+    using CS = Cfg<IO, KB, NW, false>;
     auto grid = [&](bool out) {  // workgroups of each job
         int64_t n = 0;
         for (int k = 0; k <= kMaxJobs; ++k) {
@@ -735,7 +883,7 @@ hipError_t run_cfg(Jobs& jobs, hipStream_t stream) {
     if (jobs.j[0].seg_len) {
         const int64_t n = grid(false);
         if (n == 0) return hipErrorNotSupported;
-        hipLaunchKernelGGL((chunk_kernel<C, false, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
+        hipLaunchKernelGGL((chunk_kernel<CS, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
         const Job& j = jobs.j[0];
         const int64_t threads = j.batch * (j.Ha < j.Hb ? j.Ha : j.Hb) * (C::NW * C::NB * 64);
         if ((threads + 255) / 256 > 0x7fffffff) return hipErrorNotSupported;
@@ -744,14 +892,14 @@ hipError_t run_cfg(Jobs& jobs, hipStream_t stream) {
     }
     const int64_t n = grid(true);
     if (n == 0) return hipErrorNotSupported;
-    hipLaunchKernelGGL((chunk_kernel<C, true, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
+    hipLaunchKernelGGL((chunk_kernel<C, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
     return hipGetLastError();
 }
 
-// whole pieces, and offsets within a chunk that fit a buffer resource
-inline bool vec_ok(const Heads& h, int D, size_t es) {
-    return (uintptr_t)h.p % 16 == 0 && h.ts * es % 16 == 0 && h.hs * es % 16 == 0 && D * es % 16 == 0 &&
-           h.ts * es < ((int64_t)1 << 24);
+// whole pieces, rows that do not overlap, offsets within a chunk that fit a buffer resource
+inline bool vec_ok(const Heads& h, int D, size_t es, size_t piece) {
+    return (uintptr_t)h.p % piece == 0 && h.ts * es % piece == 0 && h.hs * es % piece == 0 && D * es % piece == 0 &&
+           h.ts >= D && h.ts * es < ((int64_t)1 << 24);
 }
 
 // Jobs of one shape (D_a and D_c alike).
@@ -761,9 +909,8 @@ hipError_t run(Jobs& jobs, hipStream_t stream) {
     bool vec = true;
     for (int k = 0; k < jobs.count; ++k) {
         Job& j = jobs.j[k];
-        vec = vec && vec_ok(j.a, j.Da, es) && vec_ok(j.b, j.Da, es) && vec_ok(j.c, j.Dc, es);
-        const size_t p = 4 * es;
-        j.out_vec = (uintptr_t)j.out.p % p == 0 && j.out.ts * es % p == 0 && j.out.hs * es % p == 0;
+        vec = vec && vec_ok(j.a, j.Da, es, 16) && vec_ok(j.b, j.Da, es, 16) && vec_ok(j.c, j.Dc, es, 16);
+        j.out_vec = vec_ok(j.out, j.Dc, es, 4 * es);
     }
     const int kb = padded_a(jobs.j[0].Da), nw = waves_for(jobs.j[0].Dc);
 #define EQL_MIX(KB, NW)                                                     \

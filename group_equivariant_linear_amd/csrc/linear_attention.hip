@@ -53,6 +53,8 @@ Job job(const Heads& x, const Heads& y, const Heads& z, const Heads& out, int Ha
     j.T = a.T;
     j.seg_len = s.seg_len;
     j.slots = s.slots;
+    j.mean = a.batch ? a.T / a.batch : 0;
+    j.per_seq = s.seg_len ? (uint32_t)((j.mean + s.seg_len - 1) / s.seg_len) : 1;
     return j;
 }
 
