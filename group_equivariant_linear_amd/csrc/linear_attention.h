@@ -277,15 +277,18 @@ template <int ES, int P>
 struct RowReader {
     static constexpr int N = P / 4 < 4 ? P / 4 : (P % 16 == 0 ? 4 : 2);
     const char* base[N];
+    __device__ __forceinline__ void move(int by) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) base[i] += by;
+    }
     __device__ __forceinline__ explicit RowReader(const char* tile) {
         const int lane = (int)threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < N; ++i) base[i] = tile + place<ES, P>(lane & 15, 4 * i + (lane >> 4)) - 64 * i;
     }
-    // of the tile `at` bytes on
     template <typename F>
-    __device__ __forceinline__ F get(int q, int m, int at) const {
-        return *reinterpret_cast<const F*>(base[m % N] + at + q * (16 * P * 16) + m * 64);
+    __device__ __forceinline__ F get(int q, int m) const {
+        return *reinterpret_cast<const F*>(base[m % N] + q * (16 * P * 16) + m * 64);
     }
 };
 
@@ -296,6 +299,13 @@ struct ColumnReader {
     static constexpr int P = C::PA, ES = C::ES;
     const char* base[2][C::KB];  // 16-bit types: rows + 0 and + 4, columns from 32 k
     const char* tile;
+    __device__ __forceinline__ void move(int by) {
+        tile += by;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < C::KB; ++k) base[h][k] += by;
+    }
     __device__ __forceinline__ explicit ColumnReader(const char* t) : tile(t) {
         if constexpr (ES == 2) {
             const int lane = (int)threadIdx.x & 63, r = 8 * (lane >> 4) + ((lane & 15) >> 2), u = lane & 3;
@@ -305,17 +315,16 @@ struct ColumnReader {
                 for (int k = 0; k < C::KB; ++k) base[h][k] = t + place<ES, P>(r + 4 * h, 4 * k + u);
         }
     }
-    // of the tile `at` bytes on
-    __device__ __forceinline__ typename C::O::F get(int a, int m, int at) const {
+    __device__ __forceinline__ typename C::O::F get(int a, int m) const {
         if constexpr (ES == 2) {
-            const int off = at + (a & 1) * 8 + m * (32 * P * 16);
+            const int off = (a & 1) * 8 + m * (32 * P * 16);
             return C::O::column(base[0][a >> 1] + off, base[1][a >> 1] + off);
         } else {
             const int lane = (int)threadIdx.x & 63, kg = lane >> 4, ln = lane & 15;
             typename C::O::F f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                f[e] = *reinterpret_cast<const float*>(tile + at + place<ES, P>(16 * m + 4 * kg + e, 4 * a + (ln >> 2)) +
+                f[e] = *reinterpret_cast<const float*>(tile + place<ES, P>(16 * m + 4 * kg + e, 4 * a + (ln >> 2)) +
                                                        (ln & 3) * 4);
             return f;
         }
@@ -333,6 +342,33 @@ __device__ __forceinline__ int state_row(int a, int kg, int i) {
 
 __device__ __forceinline__ float uniform(float v) {
     return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
+// A barrier that waits for this wave's LDS accesses only.  (__syncthreads() and every LDS
+// read after a builtin's load to LDS would also wait for the loads in flight, which are
+// the next chunk's: hence this and the loads in assembly, which have no register results.)
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 64 pieces of 16 bytes, one from each lane's offset in the resource, to LDS from `to` on.
+__device__ __forceinline__ void load_to_lds(const u32x4& rsrc, uint32_t offset, const char* to) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(offset), "s"(rsrc), "s"(at)
+                 : "memory");  // (m0 is nobody else's here)
+}
+
+// A raw buffer resource as four words; base and size are the same in all lanes.
+__device__ __forceinline__ u32x4 resource(const void* base, uint32_t bytes) {
+    const uintptr_t p = (uintptr_t)base;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32) & 0xffffu),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
 }
 
 // Loads of 64 rows into a tile of P pieces a row (folded or in order), NP per wave, 64
@@ -365,14 +401,11 @@ struct Loader {
                                         char* to) const {
         const IO* base = (const IO*)x.p + t * x.ts + h * x.hs;
         if constexpr (VEC) {
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)(((n - 1) * x.ts + D) * ES));
+            const u32x4 rs = resource(base, (uint32_t)(((n - 1) * x.ts + D) * ES));
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 const int i = first + k * step;
-                const uint32_t o = off[k];  // (an array element given straight to the builtin loses the host stub)
-                if (i < P)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        rs, (__attribute__((address_space(3))) void*)(to + i * 1024), 16, o, 0, 0, 0);
+                if (i < P) load_to_lds(rs, off[k], to + i * 1024);
             }
         } else {
 #pragma unroll
@@ -390,8 +423,11 @@ struct Loader {
 };
 
 // Waves per SIMD that the registers are held to.
+constexpr int waves_per_simd(int es, int kb, int nw) {
+    return es == 4 ? (nw == 8 || kb == 1 ? 2 : 1) : (nw == 8 ? 2 : (kb <= 2 ? 3 : 2));
+}
 template <class C>
-constexpr int kWaves = C::ES == 4 ? (C::NW == 8 || C::KB == 1 ? 2 : 1) : (C::NW == 8 ? 2 : (C::KB <= 2 ? 3 : 2));
+constexpr int kWaves = waves_per_simd(C::ES, C::KB, C::NW);
 
 // Chunks of 64 tokens, in time order or (reversed) from the end.  Per chunk, and per
 // head of b and c that shares the state:
@@ -478,17 +514,23 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
             for (int a = 0; a < C::NB; ++a)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {  // (rows and columns past the state: any number, then 0)
                     const int da = state_row<C>(a, kg, i);
-                    if (da < j.Da && dc < j.Dc) S[a][i] = s0 * j.S0[state_at + (int64_t)da * j.sa + (int64_t)dc * j.sc];
+                    const int ra = da < j.Da ? da : j.Da - 1, rc = dc < j.Dc ? dc : j.Dc - 1;
+                    S[a][i] = j.S0[state_at + ra * j.sa + rc * j.sc];
                 }
+#pragma unroll
+            for (int a = 0; a < C::NB; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    S[a][i] = state_row<C>(a, kg, i) < j.Da && dc < j.Dc ? s0 * S[a][i] : 0.0f;
         }
     }
 
     // Decays, the same in every whole chunk: of the scores (within a diagonal block, one
     // block apart; g^16 per further block), of the old state at a token (g^16 per block
     // of tokens), of a token's weight in the new state (step m and lane group; element e).
-    float near0[4], near1[4], wb[NS], we[KF];
+    float near0[4], near1 = 0.0f, wb[NS], we[KF], ge[4];
     const float g16 = uniform(power(l2, 16)), g64 = uniform(power(l2, kChunk));
     float old = 0.0f;
     if constexpr (OUT) {
@@ -496,8 +538,8 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         for (int i = 0; i < 4; ++i) {
             const int d = sgn * (ln - (4 * kg + i));  // t - s (s - t reversed) on the diagonal
             near0[i] = d >= 0 ? j.scale * power(l2, d) : 0.0f;
-            near1[i] = j.scale * power(l2, 16 + d);
         }
+        near1 = j.scale * power(l2, rev ? 16 - ln + 4 * kg : 13 + ln - 4 * kg);  // and ge[i]: g^(16 + d)
         old = j.scale * power(l2, rev ? 16 - ln : 1 + ln);
         // blocks of P above (reversed: below) the diagonal that step 4 reads with their neighbours
         for (int i = tid; i < kChunk * C::PP; i += C::NT) reinterpret_cast<u32x4*>(tp)[i] = u32x4{0u, 0u, 0u, 0u};
@@ -513,11 +555,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         for (int e = 1; e < KF; ++e) up[e] = up[e - 1] * g1;
 #pragma unroll
         for (int e = 0; e < KF; ++e) we[e] = uniform(rev ? up[e] : up[KF - 1 - e]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ge[i] = uniform(rev ? up[i] : up[3 - i]);
     }
 
-    const RowReader<ES, C::PA> rows(lds);
-    const RowReader<ES, C::PP> rp(lds);
-    const ColumnReader<C> cb(lds);
+    RowReader<ES, C::PA> rows_a(tile_a), rows_b(tile_b);
+    const RowReader<ES, C::PP> rp(tp);
+    ColumnReader<C> cb(tile_b);
     // 16 x 64 tokens of c: its columns of a wave alone, rows of 16 numbers
     const char* const c_lo = ES == 2 ? tc + (8 * kg + (ln >> 2)) * 32 + (ln & 3) * 8 : tc + kg * 256 + ln * 4;
 
@@ -537,14 +581,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         if (stored) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         stored = false;
-        __syncthreads();
+        lds_barrier();
         if constexpr (TWO) {
             if (more) {
                 if (last_head) load_a(tn, ba ^ 1);
                 load_b(tn, hn, bb ^ 1);
             }
         }
-        const int oa = ba * C::TILE, ob = C::OFF_B + bb * C::TILE;
 
         // reversed, the initial state belongs to the last token itself: no decay before it
         const int e0 = (rev && initial_seg && left == n_chunks) ? 0 : 1;
@@ -587,13 +630,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int m = 0; m < C::NM; ++m)
-                        O::mma(s, rows.template get<F>(kb, m, ob), rows.template get<F>(qb, m, oa));
+                        O::mma(s, rows_b.template get<F>(kb, m), rows_a.template get<F>(qb, m));
                     const bool diag = hi == lo;
-                    const float f = hi - lo <= 1 ? 1.0f : (hi - lo == 2 ? g16 : g16 * g16);
+                    const float f = near1 * (hi - lo <= 1 ? 1.0f : (hi - lo == 2 ? g16 : g16 * g16));
                     float p[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float w = diag ? near0[i] : near1[i] * f;
+                        const float w = diag ? near0[i] : f * ge[i];
                         p[i] = diag && w == 0.0f ? 0.0f : s[i] * w;  // (a NaN among the masked scores: 0)
                     }
                     const int row = 16 * qb + ln;
@@ -644,7 +687,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                             constexpr int ST = ES == 2 ? 2 : 1;
                             F st[ST], at[NQ];
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q) at[q] = rows.template get<F>(q, m, oa);
+                            for (int q = 0; q < NQ; ++q) at[q] = rows_a.template get<F>(q, m);
                             float v[KF];
 #pragma unroll
                             for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * inv_norm;
@@ -694,7 +737,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                         O::split(v, cw);
 #pragma unroll
                         for (int a = 0; a < C::NB; ++a) {
-                            const F bt = cb.get(a, m, ob);
+                            const F bt = cb.get(a, m);
 #pragma unroll
                             for (int x = 0; x < O::TERMS; ++x) O::mma(S[a], bt, cw[x]);
                         }
@@ -702,7 +745,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                     }
                 }
             }
-            __syncthreads();  // P is there; the tiles of a and b are free
+            lds_barrier();  // P is there; the tiles of a and b are free
             if constexpr (!TWO) {
                 if (more) {
                     if (last_head) load_a(tn, 0);
@@ -722,7 +765,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                     for (int m = 0; m < NM_T; ++m)
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) O::mma(acc[q], ct[m], rp.template get<F>(q, m, C::OFF_P));
+                        for (int q = 0; q < NQ; ++q) O::mma(acc[q], ct[m], rp.template get<F>(q, m));
                     if (odd) {
                         int lno = ln, kgo = kg;
                         asm volatile("" : "+v"(lno), "+v"(kgo));
@@ -781,8 +824,14 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         else if (n > 16) chunk(std::false_type{}, std::integral_constant<int, 4>{});
         else chunk(std::false_type{}, std::integral_constant<int, 1>{});
         if constexpr (TWO) {
+            const int step_b = bb ? -C::TILE : C::TILE;
+            rows_b.move(step_b);
+            cb.move(step_b);
             bb ^= 1;
-            if (last_head) ba ^= 1;
+            if (last_head) {
+                rows_a.move(ba ? -C::TILE : C::TILE);
+                ba ^= 1;
+            }
         }
         t = tn;
         hh = hn;

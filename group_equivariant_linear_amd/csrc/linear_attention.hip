@@ -15,17 +15,22 @@ namespace {
 
 using namespace mix;
 
-// Segments: none where the sequences and heads alone give two workgroups per CU;
-// otherwise runs of at least four chunks, as many as that takes.
+// Segments of long sequences: as many as fill the CUs once (each of the kernel's
+// workgroups per CU counted), of at least four chunks; none where the sequences and heads
+// alone half fill them.  Two passes that fill the CUs a little more than once would run
+// as long as two that fill them twice: f16, 32768 tokens, 10 heads of 112, 510 and 520
+// workgroups of a kernel with one per CU.
 struct Split {
     int64_t seg_len = 0, slots = 0;
 };
-Split split_for(int64_t T, int64_t batch, int heads, bool ragged) {
+Split split_for(int io, int heads, int D_k, int D_v, int64_t T, int64_t batch, bool ragged) {
     Split s;
     s.slots = batch;
     const int64_t mean = T / batch;
-    if (batch * heads >= 512 || mean < 8 * kChunk) return s;
-    const int64_t want = (512 + batch * heads - 1) / (batch * heads);
+    const int nw = waves_for(D_v > D_k ? D_v : D_k), kb = padded_a(D_v > D_k ? D_v : D_k);
+    const int64_t fill = 256 * (int64_t)waves_per_simd(io == kIoF32 ? 4 : 2, kb, nw) * 4 / nw;
+    if (2 * batch * heads > fill || mean < 8 * kChunk) return s;
+    const int64_t want = fill / (batch * heads);
     int64_t chunks = ((mean + kChunk - 1) / kChunk + want - 1) / want;
     chunks = chunks < 4 ? 4 : chunks;
     s.seg_len = chunks * kChunk;
@@ -66,16 +71,16 @@ hipError_t run_jobs(int io, Jobs& jobs, hipStream_t stream) {
 }  // namespace
 
 // The backward's parts: of dq and dk (D_v x D_k), then of dv (D_k x D_v).
-size_t linear_attention_workspace(int, int heads, int kv_heads, int D_k, int D_v, int64_t T, int64_t batch,
+size_t linear_attention_workspace(int io, int heads, int kv_heads, int D_k, int D_v, int64_t T, int64_t batch,
                                   bool backward) {
     if (T <= 0 || batch <= 0) return 0;
-    const Split s = split_for(T, batch, heads, true);  // packed sequences need the most slots
+    const Split s = split_for(io, heads, D_k, D_v, T, batch, true);  // packed sequences need the most slots
     const size_t n = part_bytes(s, kv_heads, D_k, D_v);
     return backward ? 2 * part_bytes(s, kv_heads, D_v, D_k) + n : n;
 }
 
 hipError_t launch_linear_attention(int io, const MixArgs& a, void* ws, hipStream_t stream) {
-    const Split s = split_for(a.T, a.batch, a.heads, a.offsets != nullptr);
+    const Split s = split_for(io, a.heads, a.D_k, a.D_v, a.T, a.batch, a.offsets != nullptr);
     Jobs jobs{};
     jobs.count = 1;
     jobs.j[0] = job(a.q, a.k, a.v, a.o, a.heads, a.kv_heads, a.D_k, a.D_v, 0, a, s, a.state_in, a.state_out, a.D_v, 1);
@@ -85,7 +90,7 @@ hipError_t launch_linear_attention(int io, const MixArgs& a, void* ws, hipStream
 
 // dk and dv first: with shared heads theirs are the longest workgroups.
 hipError_t launch_linear_attention_backward(int io, const MixArgs& a, void* ws, hipStream_t stream) {
-    const Split s = split_for(a.T, a.batch, a.heads, a.offsets != nullptr);
+    const Split s = split_for(io, a.heads, a.D_k, a.D_v, a.T, a.batch, a.offsets != nullptr);
     const size_t n = part_bytes(s, a.kv_heads, a.D_v, a.D_k);
     Job dk = job(a.v, a.d_o, a.q, a.dk, a.kv_heads, a.heads, a.D_v, a.D_k, 1, a, s, a.d_state_out, nullptr, 1, a.D_v);
     Job dv = job(a.k, a.q, a.d_o, a.dv, a.kv_heads, a.heads, a.D_k, a.D_v, 1, a, s, a.d_state_out, a.d_state_in, a.D_v, 1);
