@@ -40,6 +40,7 @@ struct Job {
     int64_t mean;      // T / batch
     uint32_t per_seq;  // segments of each sequence (no offsets)
     float* part;
+    uint32_t wgs;      // workgroups of this launch
     int out_vec;  // rows of out in whole pieces of four
 };
 
@@ -451,11 +452,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     constexpr int NS = C::NS, KF = O::KF, ES = C::ES;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
 
-    // consecutive workgroups (heads of one sequence, which may share b and c) on one XCD
-    const uint32_t wg = xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t wg = blockIdx.x;
     const int which = wg >= jobs.first[2] ? 2 : (wg >= jobs.first[1] ? 1 : 0);
     const Job j = which == 2 ? jobs.j[2] : (which == 1 ? jobs.j[1] : jobs.j[0]);
-    const uint32_t id = wg - jobs.first[which == 2 ? 2 : (which == 1 ? 1 : 0)];
+    const uint32_t first = jobs.first[which == 2 ? 2 : (which == 1 ? 1 : 0)];
+    // consecutive workgroups of a job (heads of one sequence, which may share b and c) on one
+    // XCD, and every job on all of them
+    const uint32_t id = xcd_remap(wg - first, j.wgs);
 
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kg = lane >> 4, ln = lane & 15;
@@ -922,9 +925,11 @@ hipError_t run_cfg(Jobs& jobs, hipStream_t stream) {
         for (int k = 0; k <= kMaxJobs; ++k) {
             jobs.first[k] = (uint32_t)n;
             if (k >= jobs.count) continue;
-            const Job& j = jobs.j[k];
-            n += j.slots * (out || j.Ha < j.Hb ? j.Ha : j.Hb);
+            Job& j = jobs.j[k];
+            const int64_t w = j.slots * (out || j.Ha < j.Hb ? j.Ha : j.Hb);
+            n += w;
             if (n > 0x7fffffff) return (int64_t)0;
+            j.wgs = (uint32_t)w;
         }
         for (int k = jobs.count; k <= kMaxJobs; ++k) jobs.first[k] = 0xffffffffu;  // never reached
         return n;
