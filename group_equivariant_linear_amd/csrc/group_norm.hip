@@ -422,7 +422,7 @@ __device__ __forceinline__ void channel_sums(const float (&v)[V], float* acc, in
 }
 
 template <typename IO, int V, int CP, int K, int NT>
-__global__ __launch_bounds__(NT, K == 6 && CP == 1 ? 4 : 2) void slab_backward_kernel(Norm s) {
+__global__ __launch_bounds__(NT, NT == 1024 ? 4 : 2) void slab_backward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
     __shared__ float red[NT / 64];
@@ -473,6 +473,7 @@ __global__ __launch_bounds__(NT, K == 6 && CP == 1 ? 4 : 2) void slab_backward_k
         for (int k = 0; k < K; ++k) {  // (pieces past the sample have dy = 0 and add nothing)
             __builtin_amdgcn_sched_barrier(0);  // piece by piece: mixed, they take twice the registers
             float z[V];
+            px[k].keep_packed();
             px[k].get(xh);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -872,11 +873,16 @@ int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // The smallest workgroup of the slab path whose registers hold a sample of `mean`
-// tokens, K pieces a thread; false: none.
-// (The backward holds x and dz: half the pieces at the largest.)
-bool slab_shape(Choice& c, int64_t mean, bool backward) {
-    const int shapes[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {6, 512}, {backward ? 8 : 16, 512}};
-    for (const auto& k : shapes)
+// tokens, K pieces a thread; false: none.  The backward holds x and dz, half the pieces
+// at the largest, and at CP = 1 spreads about 3000 pieces over 1024 threads, which
+// compile to under 128 registers: 30 us for 64 images of 197 x 96 x 8 (bf16, GELU) where
+// 6 each on 512 threads took 46.  Where a piece crosses channels the sums take registers
+// too, and the same step spills: 59 us against 39 at 64 x 300 x 96 x 6; so does K = 4.
+bool slab_shape(Choice& c, int64_t mean, bool backward, bool one) {
+    const int forward[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {6, 512}, {16, 512}};
+    const int wide[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {3, 1024}, {8, 512}};
+    const int crossing[6][2] = {{2, 64}, {8, 64}, {4, 256}, {8, 256}, {6, 512}, {8, 512}};
+    for (const auto& k : backward ? (one ? wide : crossing) : forward)
         if (c.cols <= k[1] && mean <= (int64_t)k[0] * (k[1] / c.cols)) {
             c.K = k[0];
             c.NT = k[1];
@@ -904,7 +910,7 @@ Choice choose(int V, int C, int N, int groups, int64_t T, int64_t batch, bool ra
         c.wgs = round_up(want < cap ? want : cap, unit);
         c.step = c.wgs * per / groups;
         c.part = backward ? (size_t)c.wgs * 2 * C * 4 : 0;
-    } else if (slab_shape(c, mean, backward) && (c.K <= 8 || batch * groups >= 128)) {
+    } else if (slab_shape(c, mean, backward, N % V == 0) && (c.K <= 8 || batch * groups >= 128)) {
         c.path = kSlab;
         c.rows = c.NT / c.cols;
         const int64_t cap = (backward ? 2048 : 8192) / groups;
@@ -1008,7 +1014,10 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
 #define EQL_SLAB(k, nt)                                                                                       \
     if (c.K == k && c.NT == nt)                                                                                \
         hipLaunchKernelGGL((slab_backward_kernel<IO, V, CP, k, nt>), grid, dim3(nt), 0, stream, s);
-        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256) EQL_SLAB(6, 512) EQL_SLAB(8, 512)
+        EQL_SLAB(2, 64) EQL_SLAB(8, 64) EQL_SLAB(4, 256) EQL_SLAB(8, 256)
+        if constexpr (CP == 1) { EQL_SLAB(3, 1024) }
+        if constexpr (CP > 1) { EQL_SLAB(6, 512) }
+        EQL_SLAB(8, 512)
 #undef EQL_SLAB
         parts = c.step;
     } else {
