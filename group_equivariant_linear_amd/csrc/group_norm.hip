@@ -11,7 +11,15 @@
 //          a second pass.
 // The variance is a mean of squared differences from the mean (in registers), or, over
 // blocks, merged from such by mean and squared sum (Chan, Golub, LeVeque 1983).
-// Everything is bound by memory; the sums run in a fixed order.
+// The sums run in a fixed order.  Memory is the floor of all three; measured, 96 x 8
+// numbers a token in bf16:
+//   token  12608 tokens: forward 12.8 us (38.7 MB, 3.0 TB/s), backward 17.6 and 4.3 for the
+//          sums of dgamma and dbeta;
+//   slab   64 images of 197 tokens: forward 23 us, backward 30 to 37 (the lengths equal, or
+//          one to twice as long); bound by GELU's arithmetic and by workgroups of one
+//          pass each: all loads first, then all sums, then all stores;
+//   split  one map of 32768 tokens (160 x 7, f16): sums 24 us, join 6, outputs 28 (147 MB,
+//          5.3 TB/s); x is read twice, the second time partly from the last-level cache.
 #include "activation.h"
 #include "eq_device.h"
 #include "eq_launch.h"
@@ -580,13 +588,21 @@ __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb
     n = nn;
 }
 
+// the 64 lanes' sets, in lane 0
+__device__ __forceinline__ void merge_wave(float& n, float& mean, float& m2) {
+    for (int o = 32; o > 0; o >>= 1) {
+        const float nb = __shfl_down(n, o), mb = __shfl_down(mean, o), m2b = __shfl_down(m2, o);
+        merge(n, mean, m2, nb, mb, m2b);
+    }
+}
+
 // One workgroup per (block of tokens, group): mean and squared differences.
 template <typename IO, int V>
 __global__ __launch_bounds__(256) void moments_kernel(Norm s) {
     constexpr int BATCH = 8;  // pieces in flight and averaged at once
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
-    __shared__ float red[3][256];
+    __shared__ float red[3][4];
     const int tid = (int)threadIdx.x, g = (int)(blockIdx.x % (uint32_t)a.groups);
     const int64_t slot = blockIdx.x / (uint32_t)a.groups;
     const Block k = block_of(s, slot);
@@ -625,15 +641,14 @@ __global__ __launch_bounds__(256) void moments_kernel(Norm s) {
             }
         merge(n, mean, m2, nb, mb, sq);
     }
-    red[0][tid] = n, red[1][tid] = mean, red[2][tid] = m2;
-    for (int o = 128; o > 0; o >>= 1) {
-        __syncthreads();
-        if (tid < o) {
-            merge(n, mean, m2, red[0][tid + o], red[1][tid + o], red[2][tid + o]);
-            red[0][tid] = n, red[1][tid] = mean, red[2][tid] = m2;
-        }
+    merge_wave(n, mean, m2);
+    const int wave = tid >> 6;
+    if ((tid & 63) == 0) red[0][wave] = n, red[1][wave] = mean, red[2][wave] = m2;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < 4; ++w) merge(n, mean, m2, red[0][w], red[1][w], red[2][w]);
+        *reinterpret_cast<float2*>(s.moments + 2 * blockIdx.x) = float2{mean, m2};
     }
-    if (tid == 0) *reinterpret_cast<float2*>(s.moments + 2 * blockIdx.x) = float2{mean, m2};
 }
 
 // One wave per slab: the blocks' moments to mean and 1/sqrt(var + eps).
@@ -649,10 +664,7 @@ __global__ __launch_bounds__(64) void join_moments_kernel(Norm s) {
         const int64_t left = tokens - k * s.block;
         merge(n, mean, m2, (float)(left < s.block ? left : s.block) * (float)s.W, m.x, m.y);
     }
-    for (int o = 32; o > 0; o >>= 1) {
-        const float nb = __shfl_down(n, o), mb = __shfl_down(mean, o), m2b = __shfl_down(m2, o);
-        merge(n, mean, m2, nb, mb, m2b);
-    }
+    merge_wave(n, mean, m2);
     if (lane == 0) {
         const float2 r = n > 0.0f ? float2{mean, 1.0f / sqrtf(m2 / n + a.eps)} : float2{0.0f, 0.0f};
         *reinterpret_cast<float2*>(s.joined + 2 * blockIdx.x) = r;
