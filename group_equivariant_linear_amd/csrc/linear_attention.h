@@ -445,11 +445,11 @@ constexpr int kWaves = waves_per_simd(C::ES, C::KB, C::NW);
 // OUT: the whole; else step 3 alone, and the state goes to part[slot].
 //
 // Memory is the floor (a prompt of 12608 tokens, 12 heads of 64 in bf16 moves 90 MB: 19 us
-// at a large copy's 4.7 TB/s), the chunks' own instructions the bound: its 26 us were 22 with
-// the loads left out, and 22 with the arithmetic left out.  A chunk is a chain of steps on
-// one tile, so what pays is other workgroups beside it: 64 tokens and not 128 keep two to
-// three workgroups' tiles in LDS at heads of 64, and the next chunk's loads fly meanwhile.
-// Per-chunk rates: bf16 heads of 64 in 26 us for 197 tokens on three workgroups a CU; f16
+// at a large copy's 4.7 TB/s), the chunks' own instructions the bound: with the next chunk's
+// loads waited for at each barrier it took 32 us, 22 with the loads left out and 22 with the
+// arithmetic left out; in flight behind the products, 26.  A chunk is a chain of steps on
+// one tile, so other workgroups have to fill its gaps: at 64 tokens three workgroups' tiles
+// (two buffers, heads of 64) fit the LDS of a CU.  Measured: bf16 heads of 64 in 26 us for 197 tokens on three workgroups a CU; f16
 // heads of 112 (88 KB of LDS, one workgroup a CU) 112 us for 128 tokens on each of 250; fp32
 // heads of 64, 8 us a chunk, 3.4 of them the fp32 matrix instructions' own time.
 template <class C, bool VEC>

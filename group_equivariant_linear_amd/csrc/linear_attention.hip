@@ -17,9 +17,8 @@ using namespace mix;
 
 // Segments of long sequences: as many as fill the CUs once (each of the kernel's
 // workgroups per CU counted), of at least four chunks; none where the sequences and heads
-// alone half fill them.  Where a kernel has one workgroup per CU, 260 run as long as 512:
-// f16, 32768 tokens, 10 heads of 112 take 155 us in 25 segments a head (state pass 42, join
-// 11, outputs 112), 225 in 52.
+// alone half fill them.  f16, 32768 tokens, 10 heads of 112: 155 us in 25 segments a head
+// (state pass 42, join 11, outputs 112), 170 with twice as many.
 struct Split {
     int64_t seg_len = 0, slots = 0;
 };
