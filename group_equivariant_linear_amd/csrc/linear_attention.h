@@ -250,6 +250,10 @@ struct Cfg {
     static constexpr int OFF_B = OUT_ ? (TWO ? 2 : 1) * TILE : 0;
     static constexpr int OFF_C = OFF_B + (TWO ? 2 : 1) * TILE;
     static constexpr int OFF_P = OFF_C + NW * CTILE, LDS = OFF_P + (OUT_ ? kChunk * PP * 16 : 0);
+    static constexpr bool ROWS = OUT_ && std::is_same_v<IO_, _Float16>;  // rows of P may carry scales
+    // fp16: scores (and with them the outputs until they are stored) times 64, so that
+    // ordinary ones lie in the middle of the range
+    static constexpr float SCORE = ROWS ? 64.0f : 1.0f;
     static constexpr int NPA = (PA + NW - 1) / NW;  // loads of a wave per a or b tile, 64 pieces each
 };
 
@@ -339,6 +343,35 @@ template <class C>
 __device__ __forceinline__ int state_row(int a, int kg, int i) {
     if constexpr (C::ES == 2) return 32 * (a >> 1) + 8 * kg + 4 * (a & 1) + i;
     else return 16 * a + 4 * kg + i;
+}
+
+// The power of two that takes a largest number m (finite: of biased exponent e) to
+// [2^13, 2^14), out of fp16's reach on either side; held between 2^-115 and 2^64, so that it
+// has an inverse and an accumulator times it stays finite where the result fits fp16.
+__device__ __forceinline__ float range_scale(float m) {
+    int e = 267 - (int)(__float_as_uint(m) >> 23);
+    e = e > 191 ? 191 : e;
+    return __uint_as_float((uint32_t)e << 23);
+}
+__device__ __forceinline__ float inverse_of_power(float p) {
+    return __uint_as_float(0x7f000000u - __float_as_uint(p));
+}
+
+// fp16: a row of decayed scores (times Cfg::SCORE) whose largest is m enters its product as it
+// is where no score of it overflows and those that count against the largest are not below
+// fp16's normal numbers (2^-8: the floor 2^-25 is 2^-17 of the largest); else times
+// range_scale(m).  Whether any row needs it is seen from scores past kRowHigh and from rows whose
+// 16 x 16 block on the diagonal has none of kRowLow or more: about one chunk in 5000 of scores
+// near 1, whose first rows are one score each there.
+constexpr float kRowLow = 0.00390625f, kRowHigh = 32768.0f;
+__device__ __forceinline__ float row_scale(float m) {
+    return m >= kRowHigh || (m > 0.0f && m < kRowLow) ? range_scale(m) : 1.0f;
+}
+// Of 16 rows (lane % 16), those for which a lane says yes
+__device__ __forceinline__ uint32_t rows_with(bool yes) {
+    const uint64_t b = __ballot(yes);
+    const uint32_t x = (uint32_t)b | (uint32_t)(b >> 32);
+    return (x | x >> 16) & 0xffffu;
 }
 
 __device__ __forceinline__ float uniform(float v) {
@@ -433,7 +466,8 @@ constexpr int kWaves = waves_per_simd(C::ES, C::KB, C::NW);
 // Chunks of 64 tokens, in time order or (reversed) from the end.  Per chunk, and per
 // head of b and c that shares the state:
 //   1. scores P[t][s] = scale g^|t-s| (a_t . b_s) of the causal half, to LDS in the
-//      plan dtype, split over the waves by 16 x 16 blocks;
+//      plan dtype, split over the waves by 16 x 16 blocks (fp16: rows that its range does
+//      not hold come a second time, times a power of two, which step 4 undoes);
 //   2. wave w, for its 16 columns of out^T: the old state (two terms) times a, decayed
 //      per token in fp32;
 //   3. the state's 16 columns: S = g^n S + b^T (decayed c), the decayed c in as many
@@ -493,6 +527,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 
     char *const tile_a = lds, *const tile_b = lds + C::OFF_B;
     char *const tc = lds + C::OFF_C + wave * C::CTILE, *const tp = lds + C::OFF_P;
+    // fp16, in the quarter of P that step 4 does not read (rows 0 .. 31, tokens 32 .. 63; reversed:
+    // rows 32 .. 63, tokens 0 .. 31), 64 bytes of every fourth row: 0 .. 3 the bits of the largest
+    // |score| of rows 16 q + lane % 16; 4 + half (of this chunk and the next) word 0, whether the
+    // rows have to be looked at.
+    auto row_word = [&](int row, int word) {
+        return reinterpret_cast<uint32_t*>(tp + (rev ? 32 * C::PP * 16 : 64) + word * 4 + row * (4 * C::PP * 16));
+    };
     const Loader<IO, C::PA, C::NPA, true, VEC> la(j.a, j.Da, 0, wave, C::NW), lb(j.b, j.Da, 0, wave, C::NW);
     const Loader<IO, C::PC, C::PC, false, VEC> lc(j.c, j.Dc, 16 * wave, 0, 1);
     auto rows_of = [&](int64_t t) { return (int)(seg.t1 - t < kChunk ? seg.t1 - t : kChunk); };
@@ -543,16 +584,17 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     // block apart; g^16 per further block), of the old state at a token (g^16 per block
     // of tokens), of a token's weight in the new state (step m and lane group; element e).
     float near0[4], near1 = 0.0f, wb[NS], we[KF], ge[4];
+    const float scale = C::SCORE * j.scale;  // of what acc holds
     const float g16 = uniform(power(l2, 16)), g64 = uniform(power(l2, kChunk));
     float old = 0.0f;
     if constexpr (OUT) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int d = sgn * (ln - (4 * kg + i));  // t - s (s - t reversed) on the diagonal
-            near0[i] = d >= 0 ? j.scale * power(l2, d) : 0.0f;
+            near0[i] = d >= 0 ? scale * power(l2, d) : 0.0f;
         }
-        near1 = j.scale * power(l2, rev ? 16 - ln + 4 * kg : 13 + ln - 4 * kg);  // and ge[i]: g^(16 + d)
-        old = j.scale * power(l2, rev ? 16 - ln : 1 + ln);
+        near1 = scale * power(l2, rev ? 16 - ln + 4 * kg : 13 + ln - 4 * kg);  // and ge[i]: g^(16 + d)
+        old = scale * power(l2, rev ? 16 - ln : 1 + ln);
         // blocks of P above (reversed: below) the diagonal that step 4 reads with their neighbours
         for (int i = tid; i < kChunk * C::PP; i += C::NT) reinterpret_cast<u32x4*>(tp)[i] = u32x4{0u, 0u, 0u, 0u};
     }
@@ -578,11 +620,14 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     const char* const c_lo = ES == 2 ? tc + (8 * kg + (ln >> 2)) * 32 + (ln & 3) * 8 : tc + kg * 256 + ln * 4;
 
     // the rows of out: element offsets of this lane's four columns at token 16 q + ln
-    const uint32_t out_row = (uint32_t)j.out.ts * ES, out_at = (uint32_t)ln * out_row + (uint32_t)(16 * wave + 4 * kg) * ES;
+    const uint32_t out_row = (uint32_t)j.out.ts * ES;
+    auto out_place = [&](int ln, int kg) { return (uint32_t)ln * out_row + (uint32_t)(16 * wave + 4 * kg) * ES; };
+    const uint32_t out_first = out_place(ln, kg);
 
     f32x4 acc[4];
     int hh = 0, left = n_chunks;  // chunks from this one on
     int ba = 0, bb = 0;           // tiles in use
+    int half = 0;                 // fp16: this chunk's of row_word
     bool stored = false;          // four stores went out after this wave's last loads
     for (int it = 0; it < total; ++it) {
         const int n = rows_of(t), nq = (n + 15) / 16;
@@ -627,36 +672,65 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                     }
                 }
             }
+            // 1. blocks of the lower triangle, row by row; reversed its transpose, with the keys
+            // of a part of a chunk in whole steps of 32
+            auto block_of = [&](int idx, int& qb, int& kb) {  // false: past the chunk's end
+                const int hi = idx >= 6 ? 3 : (idx >= 3 ? 2 : (idx >= 1 ? 1 : 0));
+                const int lo = idx - hi * (hi + 1) / 2;
+                qb = rev ? lo : hi, kb = rev ? hi : lo;
+                return idx < (NQ == 1 ? 3 : 10) && (FULL || qb < nq);
+            };
+            auto scores = [&](int qb, int kb, float(&p)[4]) {
+                f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int m = 0; m < C::NM; ++m)
+                    O::mma(s, rows_b.template get<F>(kb, m), rows_a.template get<F>(qb, m));
+                const int apart = rev ? kb - qb : qb - kb;
+                const bool diag = apart == 0;
+                const float f = near1 * (apart <= 1 ? 1.0f : (apart == 2 ? g16 : g16 * g16));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = diag ? near0[i] : f * ge[i];
+                    p[i] = diag && w == 0.0f ? 0.0f : s[i] * w;  // (a NaN among the masked scores: 0)
+                }
+            };
+            auto put_scores = [&](int qb, int kb, int ln, int kg, const float(&p)[4]) {
+                const int row = 16 * qb + ln;
+                if constexpr (ES == 2)
+                    *reinterpret_cast<u32x2*>(tp + place<ES, C::PP>(row, 2 * kb + (kg >> 1)) + (kg & 1) * 8) =
+                        u32x2{Half<IO>::pack2(p[0], p[1]), Half<IO>::pack2(p[2], p[3])};
+                else
+                    *reinterpret_cast<f32x4*>(tp + place<ES, C::PP>(row, 4 * kb + kg)) = f32x4{p[0], p[1], p[2], p[3]};
+            };
+            constexpr int OWN = ((NQ == 1 ? 3 : 10) + C::NW - 1) / C::NW;  // blocks of a wave
+            auto largest = [](const float(&p)[4]) {
+                return fmaxf(fmaxf(fabsf(p[0]), fabsf(p[1])), fmaxf(fabsf(p[2]), fabsf(p[3])));
+            };
+            uint32_t small = 0;
+            float most = 0.0f;
             if constexpr (OUT) {
-                // 1. blocks of the lower triangle, row by row; reversed its transpose, with the keys
-                // of a part of a chunk in whole steps of 32
-                constexpr int BLOCKS = NQ == 1 ? 3 : 10;
 #pragma unroll
-                for (int k = 0; k < (BLOCKS + C::NW - 1) / C::NW; ++k) {
-                    const int idx = wave + k * C::NW;
-                    if (idx >= BLOCKS) continue;
-                    const int hi = idx >= 6 ? 3 : (idx >= 3 ? 2 : (idx >= 1 ? 1 : 0));
-                    const int lo = idx - hi * (hi + 1) / 2;
-                    const int qb = rev ? lo : hi, kb = rev ? hi : lo;
-                    if (!FULL && qb >= nq) continue;
-                    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int m = 0; m < C::NM; ++m)
-                        O::mma(s, rows_b.template get<F>(kb, m), rows_a.template get<F>(qb, m));
-                    const bool diag = hi == lo;
-                    const float f = near1 * (hi - lo <= 1 ? 1.0f : (hi - lo == 2 ? g16 : g16 * g16));
+                for (int k = 0; k < OWN; ++k) {
+                    int qb, kb;
+                    if (!block_of(wave + k * C::NW, qb, kb)) continue;
                     float p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = diag ? near0[i] : f * ge[i];
-                        p[i] = diag && w == 0.0f ? 0.0f : s[i] * w;  // (a NaN among the masked scores: 0)
+                    scores(qb, kb, p);
+                    if constexpr (C::ROWS) {
+                        const float m = largest(p);
+                        most = fmaxf(most, m);
+                        const uint32_t rows = FULL || n - 16 * qb >= 16 ? 0xffffu : (1u << (n - 16 * qb)) - 1;
+                        small |= (qb == kb ? rows : 0u) & ~rows_with(m >= kRowLow);
                     }
-                    const int row = 16 * qb + ln;
-                    if constexpr (ES == 2)
-                        *reinterpret_cast<u32x2*>(tp + place<ES, C::PP>(row, 2 * kb + (kg >> 1)) + (kg & 1) * 8) =
-                            u32x2{Half<IO>::pack2(p[0], p[1]), Half<IO>::pack2(p[2], p[3])};
-                    else
-                        *reinterpret_cast<f32x4*>(tp + place<ES, C::PP>(row, 4 * kb + kg)) = f32x4{p[0], p[1], p[2], p[3]};
+                    put_scores(qb, kb, ln, kg, p);
+                }
+            }
+            if constexpr (C::ROWS) {
+                if (small || __any(most >= kRowHigh)) [[unlikely]] *row_word(4 + half, 0) = 1;
+            }
+            if constexpr (C::ROWS) {  // the last chunk's readers are past this chunk's first barrier
+                if (wave == 0) {
+                    *row_word(kg, ln) = 0;
+                    *row_word(4 + (half ^ 1), 0) = 0;
                 }
             }
             // the columns of c are in registers: the next chunk's may take their place, unless
@@ -712,7 +786,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                         }
                         if constexpr (FULL) {
                             float d[4];
-                            d[0] = norm * (e0 ? old : j.scale * power(l2, 15 - ln));
+                            d[0] = norm * (e0 ? old : scale * power(l2, 15 - ln));
                             d[1] = d[0] * g16, d[2] = d[1] * g16, d[3] = d[2] * g16;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) acc[q] *= rev ? d[3 - q] : d[q];
@@ -720,7 +794,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                             for (int q = 0; q < NQ; ++q) {
                                 const int tq = 16 * q + lnp, d = (rev ? n - 1 - tq : tq) + e0;
-                                acc[q] *= norm * j.scale * power(l2, d > 0 ? d : 0);
+                                acc[q] *= norm * scale * power(l2, d > 0 ? d : 0);
                             }
                         }
                     }
@@ -764,6 +838,59 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                     load_b(tn, hn, 0);
                 }
             }
+            bool ranged = false;  // rows of P carry scales
+            // fp16: the fragments of P that step 4 takes, read along with the flags: whole blocks of
+            // rows 0 and 1 (first half of the chunk's tokens), 2 and 3 (second half), and the other
+            // half of the two blocks that have one (reversed 0 and 1, else 2 and 3)
+            constexpr int NP = !C::ROWS ? 1 : (NQ == 4 ? 6 : 1);
+            F pf[NP];
+            auto read_p = [&] {
+                pf[0] = rp.template get<F>(0, 0);
+                if constexpr (NP == 6) {
+                    pf[1] = rp.template get<F>(1, 0);
+                    pf[2] = rp.template get<F>(2, 1);
+                    pf[3] = rp.template get<F>(3, 1);
+                    const char* const more = rev ? rp.base[1] + 64 : rp.base[0] + 2 * (16 * C::PP * 16);
+                    pf[4] = *reinterpret_cast<const F*>(more);
+                    pf[5] = *reinterpret_cast<const F*>(more + 16 * C::PP * 16);
+                }
+            };
+            auto scale_of = [&](int q) { return row_scale(__uint_as_float(*row_word(q, ln))); };
+            if constexpr (C::ROWS) {
+                const uint32_t look = *row_word(4 + half, 0);
+                read_p();
+#pragma unroll
+                for (int i = 0; i < NP; ++i) asm volatile("" : "+v"(pf[i]));  // here, not past the branch
+                ranged = __builtin_amdgcn_readfirstlane(look) != 0;
+                if (ranged) [[unlikely]] {
+                    float p[OWN][4];
+#pragma unroll
+                    for (int k = 0; k < OWN; ++k) {
+                        int qb, kb;
+                        if (!block_of(wave + k * C::NW, qb, kb)) continue;
+                        scores(qb, kb, p[k]);
+                        atomicMax(row_word(qb, ln), __float_as_uint(largest(p[k])));
+                    }
+                    lds_barrier();
+                    int lns = ln, kgs = kg;
+                    asm volatile("" : "+v"(lns), "+v"(kgs));  // (as above)
+#pragma unroll
+                    for (int k = 0; k < OWN; ++k) {
+                        int qb, kb;
+                        if (!block_of(wave + k * C::NW, qb, kb)) continue;
+                        const float sc = scale_of(qb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[k][i] *= sc;
+                        put_scores(qb, kb, lns, kgs, p[k]);
+                    }
+                    if (own) {
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) acc[q] *= scale_of(q);
+                    }
+                    lds_barrier();
+                    read_p();
+                }
+            }
             if constexpr (OUT) {
                 if (own) {
                     // 4.  An infinity or NaN among the chunk's values: 0 times it must not reach the
@@ -774,10 +901,27 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                         for (int m = 0; m < NM_T; ++m) ct[m] = O::finite(ct[m]);
                     }
                     // (P is 0 in the blocks that are not written)
+                    if constexpr (NP == 6) {
+                        if (!rev) {
+                            O::mma(acc[2], ct[0], pf[4]);
+                            O::mma(acc[3], ct[0], pf[5]);
+                        }
+                        O::mma(acc[0], ct[0], pf[0]);
+                        O::mma(acc[1], ct[0], pf[1]);
+                        O::mma(acc[2], ct[1], pf[2]);
+                        O::mma(acc[3], ct[1], pf[3]);
+                        if (rev) {
+                            O::mma(acc[0], ct[1], pf[4]);
+                            O::mma(acc[1], ct[1], pf[5]);
+                        }
+                    } else if constexpr (C::ROWS) {
+                        O::mma(acc[0], ct[0], pf[0]);
+                    } else {
 #pragma unroll
-                    for (int m = 0; m < NM_T; ++m)
+                        for (int m = 0; m < NM_T; ++m)
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) O::mma(acc[q], ct[m], rp.template get<F>(q, m));
+                            for (int q = 0; q < NQ; ++q) O::mma(acc[q], ct[m], rp.template get<F>(q, m));
+                    }
                     if (odd) {
                         int lno = ln, kgo = kg;
                         asm volatile("" : "+v"(lno), "+v"(kgo));
@@ -797,13 +941,29 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                         if (more) load_c(tn, hn);
                     }
+                    if constexpr (C::ROWS) {
+                        if (ranged) [[unlikely]] {
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) acc[q] *= inverse_of_power(scale_of(q));
+                        }
+                    }
                     if (last_head) {
+                        if constexpr (C::SCORE != 1.0f) {
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) acc[q] *= 1.0f / C::SCORE;
+                        }
                         IO* out = (IO*)const_cast<void*>(j.out.p) + t * j.out.ts + hx * j.out.hs;
                         if (j.out_vec) {
                             asm volatile("" ::: "memory");  // the loads above stay older than these
                             __builtin_amdgcn_sched_barrier(0);
                             const __amdgpu_buffer_rsrc_t ro = make_rsrc(out, (uint32_t)(((n - 1) * j.out.ts + j.Dc) * ES));
                             const bool in = 16 * wave + 4 * kg < j.Dc;
+                            uint32_t out_at = out_first;
+                            if constexpr (C::ROWS) {  // not kept: the fp16 kernels need its register
+                                int lno = ln, kgo = kg;
+                                asm volatile("" : "+v"(lno), "+v"(kgo));
+                                out_at = out_place(lno, kgo);
+                            }
 #pragma unroll
                             for (int q = 0; q < NQ; ++q) {
                                 const uint32_t at = in && (FULL || 16 * q + lnp < n) ? out_at + 16 * q * out_row : kOOB;
@@ -847,6 +1007,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         }
         t = tn;
         hh = hn;
+        half ^= 1;
         if (last_head) --left;
     }
 

@@ -496,8 +496,10 @@ size_t eqlinear_linear_attention_workspace(eqlinear_plan_t plan, int64_t T, int6
  *             empty sequence passes its state through.  16-byte aligned
  *   workspace at least eqlinear_linear_attention_workspace bytes, 256-byte aligned
  * 16-bit plans round the decayed scores to the plan dtype before their product
- * with v; the state keeps fp32 between tokens and enters the matrix cores as two
- * terms of the plan dtype.  Asynchronous on stream, no allocation; deterministic. */
+ * with v (fp16: times a power of two where its range asks for one, so that scores
+ * may be larger or smaller than fp16's numbers); the state keeps fp32 between
+ * tokens and enters the matrix cores as two terms of the plan dtype.
+ * Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_linear_attention(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
                                           const eqlinear_heads* v, const float* log_decay, float scale,
                                           const int64_t* offsets, int64_t batch, const float* state_in,
