@@ -125,7 +125,8 @@ struct Op {  // __bf16, _Float16
     using F = typename Half<IO>::x8;
     static constexpr int KS = 32, KF = 8, ES = 2;
     static constexpr bool BF = std::is_same_v<IO, __bf16>;
-    // terms in which an fp32 number enters a product without loss of its fp32 accuracy
+    // terms in which an fp32 number of the middle of IO's range enters a product: 24 bits of
+    // it (bf16) or 21 to 22 (fp16)
     static constexpr int TERMS = BF ? 3 : 2;
     static __device__ __forceinline__ void mma(f32x4& acc, const F& a, const F& b) {
         if constexpr (BF) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
@@ -146,8 +147,9 @@ struct Op {  // __bf16, _Float16
         for (int e = 0; e < KF; ++e) f[e] = fabsf((float)f[e]) < __builtin_inff() ? f[e] : (IO)0.0f;
         return f;
     }
-    // v (8 numbers) as N fragments, each what the ones before left, cut off (not rounded:
-    // the next term holds the rest exactly; three bf16 or two fp16 terms hold 22 bits or more)
+    // v (8 numbers) as N fragments, each what the ones before left, cut off (not rounded: the
+    // next term holds the rest exactly).  Three bf16 terms hold all 24 bits; two fp16 terms hold
+    // 22 of a number of 2^-3 or more, below that its bits down to 2^-24: hence kColumnLow, kValueLow
     template <int N>
     static __device__ __forceinline__ void split(const float (&v)[8], F (&out)[N]) {
         float r[8];
@@ -177,14 +179,18 @@ struct Op {  // __bf16, _Float16
             out[t] = __builtin_bit_cast(F, u);
         }
     }
-    // whether a fragment holds an infinity or a NaN
-    static __device__ __forceinline__ bool odd(const F& f) {
-        const u32x4 v = __builtin_bit_cast(u32x4, f);
-        constexpr unsigned short top = BF ? 0x7f80 : 0x7c00;
+    // the largest |number| of N fragments, its 16 bits (kInf or more: an infinity or a NaN)
+    static constexpr uint32_t kInf = BF ? 0x7f80 : 0x7c00;
+    template <int N>
+    static __device__ __forceinline__ uint32_t top(const F (&f)[N]) {
         u16x2 m = {0, 0};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[q] & 0x7fff7fffu));
-        return m[0] >= top || m[1] >= top;
+        for (int i = 0; i < N; ++i) {
+            const u32x4 v = __builtin_bit_cast(u32x4, f[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[q] & 0x7fff7fffu));
+        }
+        return m[0] > m[1] ? m[0] : m[1];
     }
 };
 
@@ -207,9 +213,16 @@ struct Op<float> {
     static __device__ __forceinline__ void split(const float (&v)[4], F (&out)[N]) {
         out[0] = F{v[0], v[1], v[2], v[3]};
     }
-    static __device__ __forceinline__ bool odd(const F& f) {
-        return !(fabsf(f[0]) < __builtin_inff() && fabsf(f[1]) < __builtin_inff() && fabsf(f[2]) < __builtin_inff() &&
-                 fabsf(f[3]) < __builtin_inff());
+    // 1 if a fragment holds an infinity or a NaN
+    static constexpr uint32_t kInf = 1;
+    template <int N>
+    static __device__ __forceinline__ uint32_t top(const F (&f)[N]) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < KF; ++e) odd |= !(fabsf(f[i][e]) < __builtin_inff());
+        return odd;
     }
 };
 
@@ -254,6 +267,9 @@ struct Cfg {
     // fp16: scores (and with them the outputs until they are stored) times 64, so that
     // ordinary ones lie in the middle of the range
     static constexpr float SCORE = ROWS ? 64.0f : 1.0f;
+    // fp16: likewise the states in registers and in `part`
+    static constexpr bool COLS = std::is_same_v<IO_, _Float16>;
+    static constexpr float STATE = COLS ? 64.0f : 1.0f;
     static constexpr int NPA = (PA + NW - 1) / NW;  // loads of a wave per a or b tile, 64 pieces each
 };
 
@@ -374,6 +390,30 @@ __device__ __forceinline__ uint32_t rows_with(bool yes) {
     return (x | x >> 16) & 0xffffu;
 }
 
+// fp16: the operands that become two terms (step 2: the state; step 3: the decayed rows of c)
+// do so as they are while each column's largest keeps their floor of 2^-24 below 2^-21 of it
+// (state) or 2^-27 (rows, before their decays), and none passes the range; else times
+// range_scale of that largest.  In units of Cfg::STATE; of c its bits.
+constexpr float kColumnLow = 1.0f, kColumnHigh = 32768.0f;
+constexpr uint32_t kValueLow = 0x3000, kValueHigh = 0x6000;  // 2^-3, 2^9
+
+// Whether the bits m of a largest |number| are neither 0 nor in low .. high.  That of any lane asks
+// for a look at the columns' own, which decide.
+__device__ __forceinline__ bool outside(uint32_t m, uint32_t low, uint32_t high) {
+    return m - 1 < low - 1 || m > high;
+}
+
+// Largest over the four lanes of a column (lane % 16)
+template <typename T>
+__device__ __forceinline__ T column_max(T v) {
+#pragma unroll
+    for (int o = 16; o <= 32; o <<= 1) {
+        const T w = __shfl_xor(v, o);
+        v = w > v ? w : v;
+    }
+    return v;
+}
+
 __device__ __forceinline__ float uniform(float v) {
     return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
@@ -470,8 +510,8 @@ constexpr int kWaves = waves_per_simd(C::ES, C::KB, C::NW);
 //      not hold come a second time, times a power of two, which step 4 undoes);
 //   2. wave w, for its 16 columns of out^T: the old state (two terms) times a, decayed
 //      per token in fp32;
-//   3. the state's 16 columns: S = g^n S + b^T (decayed c), the decayed c in as many
-//      terms as keep the state's fp32 accuracy;
+//   3. the state's 16 columns: S = g^n S + b^T (decayed c), the decayed c in three terms
+//      (bf16) or two (fp16);
 //   4. out^T += c^T P^T, and the rows of out go to memory.
 // The state never leaves its wave's registers: the accumulator of step 3 is, in its
 // lanes, the operand of step 2.  Two barriers a chunk: the tiles of a and b are there;
@@ -563,7 +603,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
             for (int a = 0; a < C::NB; ++a) S[a] = *reinterpret_cast<const f32x4*>(p + a * 256);
         } else if (j.S0) {
-            const float s0 = rev && n_tok ? 1.0f / j.scale : 1.0f;
+            const float s0 = n_tok ? (rev ? 1.0f / j.scale : 1.0f) * C::STATE : 1.0f;
 #pragma unroll
             for (int a = 0; a < C::NB; ++a)
 #pragma unroll
@@ -584,7 +624,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     // block apart; g^16 per further block), of the old state at a token (g^16 per block
     // of tokens), of a token's weight in the new state (step m and lane group; element e).
     float near0[4], near1 = 0.0f, wb[NS], we[KF], ge[4];
-    const float scale = C::SCORE * j.scale;  // of what acc holds
+    const float scale = C::SCORE * j.scale, from_state = C::SCORE / C::STATE * j.scale;  // in what acc holds
     const float g16 = uniform(power(l2, 16)), g64 = uniform(power(l2, kChunk));
     float old = 0.0f;
     if constexpr (OUT) {
@@ -594,13 +634,13 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
             near0[i] = d >= 0 ? scale * power(l2, d) : 0.0f;
         }
         near1 = scale * power(l2, rev ? 16 - ln + 4 * kg : 13 + ln - 4 * kg);  // and ge[i]: g^(16 + d)
-        old = scale * power(l2, rev ? 16 - ln : 1 + ln);
+        old = from_state * power(l2, rev ? 16 - ln : 1 + ln);
         // blocks of P above (reversed: below) the diagonal that step 4 reads with their neighbours
         for (int i = tid; i < kChunk * C::PP; i += C::NT) reinterpret_cast<u32x4*>(tp)[i] = u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int m = 0; m < NS; ++m)
-        wb[m] = power(l2, rev ? O::KS * m + KF * kg : kChunk - O::KS * m - KF * (kg + 1));
+        wb[m] = C::STATE * power(l2, rev ? O::KS * m + KF * kg : kChunk - O::KS * m - KF * (kg + 1));
     {
         const float g1 = power(l2, 1);
         float up[KF];
@@ -736,10 +776,10 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
             // the columns of c are in registers: the next chunk's may take their place, unless
             // step 4 has to come back to them
             bool odd = false;
+            uint32_t top = 0;
             if (own) {
-#pragma unroll
-                for (int m = 0; m < NM_T; ++m) odd |= O::odd(ct[m]);
-                odd = OUT && __any(odd);
+                top = O::top(ct);
+                odd = OUT && __any(top >= O::kInf);
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (more && !odd) load_c(tn, hn);
             }
@@ -751,21 +791,19 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                     if (hh == 0) {
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-                        float norm = 1.0f, inv_norm = 1.0f;  // fp16: a state out of its range scaled by a power of two
-                        if constexpr (std::is_same_v<IO, _Float16>) {
+                        float norm = 1.0f;  // of this lane's column
+                        bool normed = false;
+                        if constexpr (C::COLS) {
                             float mx = 0.0f;
 #pragma unroll
                             for (int a = 0; a < C::NB; ++a)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[a][i]));
-                            if (__any(mx > 32768.0f) || (!__any(mx > 0.03125f) && __any(mx > 0.0f))) {
-#pragma unroll
-                                for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-                                int ex = 0;
-                                if (mx < __builtin_inff()) (void)frexpf(mx, &ex);
-                                ex = ex < -100 ? -100 : ex;
-                                norm = uniform(ldexpf(1.0f, ex));
-                                inv_norm = uniform(ldexpf(1.0f, -ex));
+                            normed = __any(outside(__float_as_uint(mx), __float_as_uint(kColumnLow), __float_as_uint(kColumnHigh)));
+                            if (normed) [[unlikely]] {
+                                mx = column_max(mx);
+                                if (outside(__float_as_uint(mx), __float_as_uint(kColumnLow), __float_as_uint(kColumnHigh)))
+                                    norm = range_scale(mx);
                             }
                         }
 #pragma unroll
@@ -776,7 +814,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                             for (int q = 0; q < NQ; ++q) at[q] = rows_a.template get<F>(q, m);
                             float v[KF];
 #pragma unroll
-                            for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * inv_norm;
+                            for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * norm;
                             O::split(v, st);
 #pragma unroll
                             for (int x = 0; x < ST; ++x)
@@ -784,9 +822,17 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                                 for (int q = 0; q < NQ; ++q) O::mma(acc[q], st[x], at[q]);
                             if (m % 2) __builtin_amdgcn_sched_barrier(0);
                         }
+                        if (normed) [[unlikely]] {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float back = inverse_of_power(__shfl(norm, 4 * kg + i));
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q) acc[q][i] *= back;
+                            }
+                        }
                         if constexpr (FULL) {
                             float d[4];
-                            d[0] = norm * (e0 ? old : scale * power(l2, 15 - ln));
+                            d[0] = (e0 ? old : from_state * power(l2, 15 - ln));
                             d[1] = d[0] * g16, d[2] = d[1] * g16, d[3] = d[2] * g16;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) acc[q] *= rev ? d[3 - q] : d[q];
@@ -794,7 +840,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                             for (int q = 0; q < NQ; ++q) {
                                 const int tq = 16 * q + lnp, d = (rev ? n - 1 - tq : tq) + e0;
-                                acc[q] *= norm * scale * power(l2, d > 0 ? d : 0);
+                                acc[q] *= from_state * power(l2, d > 0 ? d : 0);
                             }
                         }
                     }
@@ -802,10 +848,30 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                 // 3.
                 __builtin_amdgcn_sched_barrier(0);
                 if (keep) {
+                    float lift = 1.0f;  // of this lane's column of c and of the state
+                    bool lifted = false;
+                    if constexpr (C::COLS) {
+                        lifted = __any(outside(top, kValueLow, kValueHigh));
+                        if (lifted) [[unlikely]] {
+                            const uint32_t most = column_max(top);
+                            if (outside(most, kValueLow, kValueHigh))
+                                lift = range_scale(C::STATE * (float)__builtin_bit_cast(_Float16, (uint16_t)most));
+                            float mx = 0.0f;  // the state stays finite
+#pragma unroll
+                            for (int a = 0; a < C::NB; ++a)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[a][i]));
+                            const int room = 379 - (int)(__float_as_uint(column_max(mx)) >> 23);
+                            lift = fminf(lift, __uint_as_float((uint32_t)(room < 127 ? 127 : (room > 254 ? 254 : room)) << 23));
+                        }
+                    }
                     if (hh == 0) {
-                        const float carry = FULL ? (e0 ? g64 : power(l2, kChunk - 1)) : power(l2, n - 1 + e0);
+                        const float carry = lift * (FULL ? (e0 ? g64 : power(l2, kChunk - 1)) : power(l2, n - 1 + e0));
 #pragma unroll
                         for (int a = 0; a < C::NB; ++a) S[a] *= carry;
+                    } else if (lifted) [[unlikely]] {
+#pragma unroll
+                        for (int a = 0; a < C::NB; ++a) S[a] *= lift;
                     }
 #pragma unroll
                     for (int m = 0; m < NM_T; ++m) {
@@ -813,10 +879,10 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                         for (int e = 0; e < KF; ++e) {
                             if constexpr (FULL) {
-                                v[e] = O::get(ct[m], e) * we[e] * wb[m];
+                                v[e] = O::get(ct[m], e) * we[e] * (C::COLS ? wb[m] * lift : wb[m]);
                             } else {
                                 const int s = O::KS * m + KF * kgp + e, d = rev ? s : n - 1 - s;
-                                v[e] = O::get(ct[m], e) * power(l2, d > 0 ? d : 0);
+                                v[e] = O::get(ct[m], e) * power(l2, d > 0 ? d : 0) * (C::STATE * lift);
                             }
                         }
                         F cw[O::TERMS];
@@ -828,6 +894,10 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                             for (int x = 0; x < O::TERMS; ++x) O::mma(S[a], bt, cw[x]);
                         }
                         __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (lifted) [[unlikely]] {
+#pragma unroll
+                        for (int a = 0; a < C::NB; ++a) S[a] *= inverse_of_power(lift);
                     }
                 }
             }
@@ -1017,7 +1087,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
         for (int a = 0; a < C::NB; ++a) *reinterpret_cast<f32x4*>(p + a * 256) = S[a];
     } else if (j.S1 && final_seg && hx % r == 0) {
-        const float s1 = rev && n_tok ? power(l2, 1) * j.scale : 1.0f;
+        const float s1 = n_tok ? (rev ? power(l2, 1) * j.scale : 1.0f) * (1.0f / C::STATE) : 1.0f;
 #pragma unroll
         for (int a = 0; a < C::NB; ++a)
 #pragma unroll
@@ -1050,7 +1120,7 @@ __global__ __launch_bounds__(256) void join_kernel(Jobs jobs) {
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
     if (j.S0) {
         const int64_t at = (b * Hkv + kv) * (int64_t)j.Da * j.Dc;
-        const float s0 = j.reverse && t1 > t0 ? 1.0f / j.scale : 1.0f;
+        const float s0 = t1 > t0 ? (j.reverse ? 1.0f / j.scale : 1.0f) * C::STATE : 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int da = state_row<C>(a, lane >> 4, i);

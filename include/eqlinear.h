@@ -498,7 +498,9 @@ size_t eqlinear_linear_attention_workspace(eqlinear_plan_t plan, int64_t T, int6
  * 16-bit plans round the decayed scores to the plan dtype before their product
  * with v (fp16: times a power of two where its range asks for one, so that scores
  * may be larger or smaller than fp16's numbers); the state keeps fp32 between
- * tokens and enters the matrix cores as two terms of the plan dtype.
+ * tokens.  It enters the matrix cores as two terms of the plan dtype, and the
+ * decayed rows that join it as three (bf16: 24 bits) or two (fp16: 21 bits or
+ * more of a column's largest, whatever its size).
  * Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_linear_attention(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
                                           const eqlinear_heads* v, const float* log_decay, float scale,

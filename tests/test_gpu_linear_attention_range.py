@@ -78,7 +78,7 @@ def check(p, what, names):
                                     f"{np.max(err / np.maximum(tol, 1e-300)):.3g} times")
 
 
-def run(p, what, names=("o", "dq")):
+def run(p, what, names=ROWS):
     import torch
     p.forward()
     p.backward()
@@ -131,3 +131,40 @@ def test_small_scores(eq, size, f):
 def test_scale_far_from_one(eq):
     run(sized(problem(eq, SIZES[1], 25, scale=2.0 ** -20), v=2000.0, k=100.0, S0=2000.0, dS1=0.1), "scale 2^-20")
     run(sized(problem(eq, SIZES[1], 26, scale=4096.0), q=0.01, v=0.01, S0=0.01, d_o=0.01, k=0.01, dS1=0.01), "scale 4096")
+
+
+# --- states -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+@pytest.mark.parametrize("f", [1e-2, 1e-3, 1e-4, 1e-5, 100.0])
+@pytest.mark.parametrize("which", ["v", "d_o"])
+def test_states_of_small_and_large_rows(eq, size, f, which):
+    """state_out is made of v, d_state_in of d_o: both keep fp32's accuracy whatever the size of either."""
+    p = problem(eq, size, 27, state=False)
+    p.dS1 = None
+    run(sized(p, **{which: f}), f"{size} {which} {f}", STATES)
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_columns_of_unlike_sizes(eq, size):
+    """Channels of v, q and d_o from 1 down to 1e-5 side by side, and states to match."""
+    p = problem(eq, size, 28)
+    channels = lambda d: 10.0 ** -(np.arange(d) % 6)[:, None]  # noqa: E731
+    numbers = lambda d: np.repeat(10.0 ** -(np.arange(d) % 6), p.N)  # noqa: E731
+    sized(p, v=channels(p.dv), d_o=channels(p.dv), S0=numbers(p.dv), dS1=numbers(p.dv))
+    run(p, f"{size}", ROWS + STATES)
+
+
+@pytest.mark.parametrize("lens", [[40, 100], [1100]], ids=str)
+def test_large_state_with_small_rows(eq, lens):
+    """A state of 1e30 keeps its size while rows of 1e-5 join it, and a state near fp32's top stays finite."""
+    import torch
+    for big in (1e30, 2.0 ** 119):
+        p = Problem(eq, F16, 8, 2, 1, 8, 8, lens, len(lens) > 1, 29, log_decay=[-0.001])
+        sized(p, v=1e-5)
+        p.S0.fill_(big)
+        p.forward()
+        torch.cuda.synchronize()
+        for b, n in enumerate(lens):
+            want = big * np.exp(np.float64(np.float32(-0.001)) * n)
+            assert np.all(np.abs(to_f64(p.S1[b]) / want - 1) <= (n + 64) * E32)
