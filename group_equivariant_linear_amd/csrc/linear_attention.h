@@ -141,10 +141,10 @@ struct Op {  // __bf16, _Float16
         return __builtin_bit_cast(F, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     static __device__ __forceinline__ float get(const F& f, int e) { return (float)f[e]; }
-    // infinities and NaN as 0
-    static __device__ __forceinline__ F finite(F f) {
+    // infinities and NaN as 0 (or, rest, all else)
+    static __device__ __forceinline__ F finite(F f, bool rest = false) {
 #pragma unroll
-        for (int e = 0; e < KF; ++e) f[e] = fabsf((float)f[e]) < __builtin_inff() ? f[e] : (IO)0.0f;
+        for (int e = 0; e < KF; ++e) f[e] = (fabsf((float)f[e]) < __builtin_inff()) != rest ? f[e] : (IO)0.0f;
         return f;
     }
     // v (8 numbers) as N fragments, each what the ones before left, cut off (not rounded: the
@@ -204,9 +204,9 @@ struct Op<float> {
         for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
     }
     static __device__ __forceinline__ float get(const F& f, int e) { return f[e]; }
-    static __device__ __forceinline__ F finite(F f) {
+    static __device__ __forceinline__ F finite(F f, bool rest = false) {
 #pragma unroll
-        for (int e = 0; e < KF; ++e) f[e] = fabsf(f[e]) < __builtin_inff() ? f[e] : 0.0f;
+        for (int e = 0; e < KF; ++e) f[e] = (fabsf(f[e]) < __builtin_inff()) != rest ? f[e] : 0.0f;
         return f;
     }
     template <int N>
@@ -620,6 +620,16 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         }
     }
 
+    bool inf_state = false;  // the state may hold an infinity
+    if constexpr (OUT && ES == 2) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int a = 0; a < C::NB; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[a][i]));
+        inf_state = __any(mx == __builtin_inff());
+    }
+
     // Decays, the same in every whole chunk: of the scores (within a diagonal block, one
     // block apart; g^16 per further block), of the old state at a token (g^16 per block
     // of tokens), of a token's weight in the new state (step m and lane group; element e).
@@ -701,16 +711,19 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
             if constexpr (!FULL) asm volatile("" : "+v"(lnp), "+v"(kgp));
             // the chunk's columns of c, contraction over its tokens
             F ct[NM_T];
+            auto column_of_c = [&](int m) {
+                F f;
+                if constexpr (ES == 2) {
+                    f = O::column(c_lo + m * 1024, c_lo + m * 1024 + 128);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(c_lo + m * 1024 + e * 64);
+                }
+                return f;
+            };
             if (own) {
 #pragma unroll
-                for (int m = 0; m < NM_T; ++m) {
-                    if constexpr (ES == 2) {
-                        ct[m] = O::column(c_lo + m * 1024, c_lo + m * 1024 + 128);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) ct[m][e] = *reinterpret_cast<const float*>(c_lo + m * 1024 + e * 64);
-                    }
-                }
+                for (int m = 0; m < NM_T; ++m) ct[m] = column_of_c(m);
             }
             // 1. blocks of the lower triangle, row by row; reversed its transpose, with the keys
             // of a part of a chunk in whole steps of 32
@@ -774,12 +787,21 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
                 }
             }
             // the columns of c are in registers: the next chunk's may take their place, unless
-            // step 4 has to come back to them
+            // steps 3 and 4 have to come back to them
             bool odd = false;
             uint32_t top = 0;
             if (own) {
                 top = O::top(ct);
-                odd = OUT && __any(top >= O::kInf);
+                // An infinity or NaN among the chunk's values: the products of steps 3 (where it would
+                // be split) and 4 (where rows before it would see 0 times it) take 0 in its place, so
+                // that all else keeps its bits, and it joins apart.
+                odd = (OUT || ES == 2) && __any(top >= O::kInf);
+                if (ES == 2 && odd) {
+#pragma unroll
+                    for (int m = 0; m < NM_T; ++m) ct[m] = O::finite(ct[m]);
+                    top = O::top(ct);
+                    inf_state = true;
+                }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (more && !odd) load_c(tn, hn);
             }
@@ -816,6 +838,9 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                             for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * norm;
                             O::split(v, st);
+                            if constexpr (ES == 2) {  // an infinity is its first term (the second would be inf - inf)
+                                if (inf_state) [[unlikely]] st[1] = O::finite(st[1]);
+                            }
 #pragma unroll
                             for (int x = 0; x < ST; ++x)
 #pragma unroll
@@ -899,6 +924,30 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                         for (int a = 0; a < C::NB; ++a) S[a] *= inverse_of_power(lift);
                     }
+                    if (ES == 2 && odd) [[unlikely]] {
+                        // what is not finite, as one term and without its decay, which takes nothing off it
+                        // (a decay of 0, no memory, would make it NaN: the next chunk's carry does)
+#pragma unroll
+                        for (int m = 0; m < NM_T; ++m) {
+                            const F rest = O::finite(column_of_c(m), true);
+#pragma unroll
+                            for (int a = 0; a < C::NB; ++a) O::mma(S[a], cb.get(a, m), rest);
+                        }
+                        // (times the zeros past D_a)
+                        int kgo = kg;
+                        asm volatile("" : "+v"(kgo));
+#pragma unroll
+                        for (int a = 0; a < C::NB; ++a)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (state_row<C>(a, kgo, i) >= j.Da) S[a][i] = 0.0f;
+                    }
+                }
+            }
+            if constexpr (!OUT && ES == 2) {
+                if (odd) {
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    if (more) load_c(tn, hn);
                 }
             }
             lds_barrier();  // P is there; the tiles of a and b are free
@@ -963,10 +1012,9 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
             }
             if constexpr (OUT) {
                 if (own) {
-                    // 4.  An infinity or NaN among the chunk's values: 0 times it must not reach the
-                    // outputs that do not see it, so the product takes 0 in its place (the other
-                    // outputs keep their bits) and those that do see it add it one by one.
-                    if (odd) {
+                    // 4.  What is not finite among the chunk's values is added one by one by the rows
+                    // that see it.
+                    if (ES == 4 && odd) {
 #pragma unroll
                         for (int m = 0; m < NM_T; ++m) ct[m] = O::finite(ct[m]);
                     }

@@ -501,6 +501,9 @@ size_t eqlinear_linear_attention_workspace(eqlinear_plan_t plan, int64_t T, int6
  * tokens.  It enters the matrix cores as two terms of the plan dtype, and the
  * decayed rows that join it as three (bf16: 24 bits) or two (fp16: 21 bits or
  * more of a column's largest, whatever its size).
+ * A number that is not finite reaches what depends on it and nothing else.  An
+ * infinity in v or in a state is one in the states that it enters; one in q or k
+ * may arrive as NaN.
  * Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_linear_attention(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
                                           const eqlinear_heads* v, const float* log_decay, float scale,
