@@ -32,11 +32,13 @@ struct Norm {
     NormArgs a;
     int W, cols, cpg;      // numbers and pieces of a slab's token; channels per group
     int lps;               // token path: lanes per slab (a power of two)
+    int pg, unit;          // token path: groups of a token, padded; workgroups that share a part, or 0
     int rows;              // slab, split paths: tokens that a workgroup covers at once
     int64_t step;          // token path: tokens from one pass to the next; slab path: samples
     int64_t block, slots;  // split path: tokens of a block, blocks
     float* part;           // dgamma and dbeta of part of the tokens: [..][2][C]
     float* moments;        // split path: [slots][groups][2]
+    float* sums;           // split path, backward: [slots][tiles + groups][2]
     float* joined;         // split path: [batch][groups][2]
 };
 
@@ -189,17 +191,26 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // --- token path -----------------------------------------------------------------------
-// Slabs are numbered token by token, group by group; a wave takes 64 / lps of them at
-// once, a lane K pieces of its slab.  Waves step by whole tokens, so a lane keeps its
-// group.  The next token's pieces load while the current one's are worked on.
+// Slabs are numbered token by token, group by group (pg of them, of which those past the
+// last group are nobody's); a wave takes 64 / lps of them at once, a lane K pieces of its
+// slab.  Waves step by whole tokens, so a lane keeps its group.  The next token's pieces load
+// while the current one's are worked on.
+struct Slab {
+    int64_t t;
+    int g;
+    __device__ __forceinline__ Slab(const Norm& s, int64_t slab) : t(slab / s.pg), g((int)(slab - t * s.pg)) {
+        if (g >= s.a.groups) t = s.a.T, g = 0;  // no token
+    }
+};
 template <typename IO, int V, int CP, int K>
 __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
     const int lane = (int)threadIdx.x & 63, sub = lane & (s.lps - 1);
     const int64_t slab = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / s.lps) + lane / s.lps;
-    int64_t t = slab / a.groups;
-    const int g = (int)(slab - t * a.groups), e0 = g * s.W;
+    const Slab first(s, slab);
+    int64_t t = first.t;
+    const int g = first.g, e0 = g * s.W;
     float gm[K][CP], be[K][CP];
     bool in[K];
 #pragma unroll
@@ -249,7 +260,8 @@ __global__ __launch_bounds__(256) void token_forward_kernel(Norm s) {
 }
 
 // The same slabs; the lane's sums of dz xh and dz over its tokens go, through LDS, to
-// part[workgroup] as sums per channel.
+// part as sums per channel.  Where a token takes `unit` whole workgroups, each has channels of
+// its own, and unit of them make one part; else every workgroup makes one.
 template <typename IO, int V, int CP, int K>
 __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
     const NormArgs& a = s.a;
@@ -258,8 +270,9 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
     const int lane = (int)threadIdx.x & 63, sub = lane & (s.lps - 1), spw = 64 / s.lps;
     const int here = (int)(threadIdx.x >> 6) * spw + lane / s.lps;
     const int64_t base = (int64_t)blockIdx.x * 4 * spw, slab = base + here;
-    int64_t t = slab / a.groups;
-    const int g = (int)(slab - t * a.groups), e0 = g * s.W;
+    const Slab first(s, slab);
+    int64_t t = first.t;
+    const int g = first.g, e0 = g * s.W;
     float gm[K][CP], be[K][CP], dg[K][CP], db[K][CP];
     bool in[K];
 #pragma unroll
@@ -314,7 +327,9 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
         t += s.step;
     }
     if (!s.part) return;
-    const int width = s.lps * K * CP, per = a.N * CP / V, g0 = (int)(base % a.groups), slabs = 4 * spw;
+    const int width = s.lps * K * CP, per = a.N * CP / V, g0 = (int)(base % s.pg), slabs = 4 * spw;
+    const int64_t row = s.unit ? blockIdx.x / (uint32_t)s.unit : blockIdx.x;
+    const int c0 = s.unit ? g0 * s.cpg : 0, c1 = s.unit && g0 + slabs < a.groups ? (g0 + slabs) * s.cpg : a.C;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         __syncthreads();
@@ -324,12 +339,12 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
             for (int i = 0; i < CP; ++i)
                 acc[here * width + (sub + k * s.lps) * CP + i] = q == 0 ? dg[k][i] : db[k][i];
         __syncthreads();
-        for (int c = (int)threadIdx.x; c < a.C; c += 256) {
+        for (int c = c0 + (int)threadIdx.x; c < c1; c += 256) {
             const int gc = c / s.cpg, at = (c - gc * s.cpg) * per;
             float v = 0.0f;
-            for (int j = (gc - g0 + a.groups) % a.groups; j < slabs; j += a.groups)
+            for (int j = (gc - g0 + s.pg) % s.pg; j < slabs; j += s.pg)
                 for (int n = 0; n < per; ++n) v += acc[j * width + at + n];
-            s.part[((int64_t)blockIdx.x * 2 + q) * a.C + c] = v;
+            s.part[(row * 2 + q) * a.C + c] = v;
         }
     }
 }
@@ -672,6 +687,9 @@ __global__ __launch_bounds__(64) void join_moments_kernel(Norm s) {
     }
 }
 
+// The largest power of two below n (n > 1), else 0
+__device__ __forceinline__ int half_of(int n) { return n > 1 ? 1 << (31 - __builtin_clz(n - 1)) : 0; }
+
 // Tile of columns of the row kernels: 256 pieces from blockIdx.y 256 on; rows of the
 // workgroup when a row is narrower than that.
 template <typename IO, int V>
@@ -715,46 +733,83 @@ __global__ __launch_bounds__(256) void apply_forward_kernel(Norm s) {
     }
 }
 
-// Sums of dz xh and dz over a block's tokens, per channel: part[slot].  Tiles of
-// columns cut channels where a tile's end is inside one; such a channel's two parts
-// meet in the LDS of neither, so the sums are kept per number, [slot][2][C N], and the
-// join adds the N of a channel.
+// Sums of gamma dz and gamma dz xh over each block's tokens, per group: sums[slot][tile +
+// group] (a tile of columns and a group meet in one run, and the next run is in the next tile or
+// the next group).  A workgroup walks the blocks blockIdx.x, blockIdx.x + gridDim.x, ... and
+// keeps the sums of dz xh and dz over all of them, per number (a tile may end inside a channel;
+// the join adds the N of a channel): part[blockIdx.x], as many as there are workgroups and not
+// as there are blocks, of which short samples make one each.
 template <typename IO, int V>
 __global__ __launch_bounds__(256) void sums_kernel(Norm s) {
     constexpr int U = 4;
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
     __shared__ float acc[256 * V];
-    const Block k = block_of(s, blockIdx.x);
+    __shared__ float red[2][256];
     const RowTile<IO, V> rt(s);
-    const int tid = (int)threadIdx.x;
+    const int tid = (int)threadIdx.x, col = tid - rt.row * rt.cols;
+    // this thread's run of pieces: its place in it, and the run's length
+    const int c0 = (int)blockIdx.y * 256, from = rt.g * s.cols - c0 > 0 ? rt.g * s.cols - c0 : 0;
+    const int end = (rt.g + 1) * s.cols - c0 < rt.cols ? (rt.g + 1) * s.cols - c0 : rt.cols;
+    const int pos = col - from, len = end - from, longest = s.cols < rt.cols ? s.cols : rt.cols;
+    const int64_t runs = (int64_t)gridDim.y + a.groups;
     float gm[V], be[V], dg[V], db[V], xh[V], dz[V];
     affine<IO>(a, rt.e, gm, be);
 #pragma unroll
     for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
-    if (!k.idle && rt.on) {
-        const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * (k.b * a.groups + rt.g));
-        const IO* x = (const IO*)a.x + rt.e;
-        const IO* dy = (const IO*)a.dy + rt.e;
-        for (int64_t t = k.t0 + rt.row; t < k.t1; t += U * rt.rows) {
-            P px[U], pd[U];
+    for (int64_t slot = blockIdx.x; slot < s.slots; slot += gridDim.x) {
+        const Block k = block_of(s, slot);
+        if (k.idle) continue;
+        float s1 = 0.0f, s2 = 0.0f;
+        if (rt.on) {
+            const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * (k.b * a.groups + rt.g));
+            const IO* x = (const IO*)a.x + rt.e;
+            const IO* dy = (const IO*)a.dy + rt.e;
+            float sg[V], sb[V];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = t + u * rt.rows < k.t1;
-                px[u] = in ? P::load(x + (t + u * rt.rows) * a.ldx) : P::zero();
-                pd[u] = in ? P::load(dy + (t + u * rt.rows) * a.lddy) : P::zero();
+            for (int i = 0; i < V; ++i) sg[i] = sb[i] = 0.0f;
+            for (int64_t t = k.t0 + rt.row; t < k.t1; t += U * rt.rows) {
+                P px[U], pd[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = t + u * rt.rows < k.t1;
+                    px[u] = in ? P::load(x + (t + u * rt.rows) * a.ldx) : P::zero();
+                    pd[u] = in ? P::load(dy + (t + u * rt.rows) * a.lddy) : P::zero();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t + u * rt.rows < k.t1) {
+                        get_dz<IO>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            sg[i] = fmaf(dz[i], xh[i], sg[i]);
+                            sb[i] += dz[i];
+                        }
+                    }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u * rt.rows < k.t1) {
-                    get_dz<IO>(a, px[u], pd[u], st.x, st.y, gm, be, xh, dz);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        dg[i] = fmaf(dz[i], xh[i], dg[i]);
-                        db[i] += dz[i];
-                    }
-                }
+            for (int i = 0; i < V; ++i) {
+                dg[i] += sg[i], db[i] += sb[i];
+                s1 = fmaf(sb[i], gm[i], s1);
+                s2 = fmaf(sg[i], gm[i], s2);
+            }
         }
+        // over the rows, then over each run, by halves
+        __syncthreads();
+        red[0][tid] = s1, red[1][tid] = s2;
+        __syncthreads();
+        for (int o = half_of(rt.rows); o > 0; o >>= 1) {
+            if (rt.row < o && rt.row + o < rt.rows)
+                red[0][tid] += red[0][tid + o * rt.cols], red[1][tid] += red[1][tid + o * rt.cols];
+            __syncthreads();
+        }
+        for (int o = half_of(longest); o > 0; o >>= 1) {
+            if (rt.row == 0 && pos < o && pos + o < len)
+                red[0][tid] += red[0][tid + o], red[1][tid] += red[1][tid + o];
+            __syncthreads();
+        }
+        if (rt.row == 0 && pos == 0)
+            *reinterpret_cast<float2*>(s.sums + 2 * (slot * runs + blockIdx.y + rt.g)) = float2{red[0][tid], red[1][tid]};
     }
     const int64_t width = (int64_t)s.W * a.groups;
     float* to = s.part + (int64_t)blockIdx.x * 2 * width + (int64_t)blockIdx.y * 256 * V;
@@ -772,34 +827,25 @@ __global__ __launch_bounds__(256) void sums_kernel(Norm s) {
     }
 }
 
-// One workgroup per slab: m1 and m2 from its blocks' sums.
-template <typename IO>
-__global__ __launch_bounds__(1024) void join_sums_kernel(Norm s) {
+// One wave per slab: m1 and m2 from its blocks' sums.
+__global__ __launch_bounds__(64) void join_sums_kernel(Norm s) {
     const NormArgs& a = s.a;
-    __shared__ float red[16];
-    const int64_t b = blockIdx.x / (uint32_t)a.groups, width = (int64_t)s.W * a.groups;
-    const int g = (int)(blockIdx.x % (uint32_t)a.groups), tid = (int)threadIdx.x;
+    const int64_t b = blockIdx.x / (uint32_t)a.groups;
+    const int g = (int)(blockIdx.x % (uint32_t)a.groups);
     int64_t first, count, n;
     blocks_of(s, b, first, count, n);
-    const int wide = s.W < 1024 ? s.W : 1024, rows = 1024 / wide, r = tid / wide;
+    const int64_t tiles = ((int64_t)s.cols * a.groups + 255) / 256, runs = tiles + a.groups;
+    const int64_t y0 = (int64_t)g * s.cols / 256, ny = ((int64_t)(g + 1) * s.cols - 1) / 256 - y0 + 1;
     float s1 = 0.0f, s2 = 0.0f;
-    if (r < rows)
-        for (int i = tid - r * wide; i < s.W; i += wide) {
-            const int e = g * s.W + i;
-            const float gm = a.gamma ? (float)((const IO*)a.gamma)[e / a.N] : 1.0f;
-            const float* p = s.part + first * 2 * width + e;
-            float dg = 0.0f, db = 0.0f;
-#pragma unroll 8
-            for (int64_t k = r; k < count; k += rows) {
-                dg += p[k * 2 * width];
-                db += p[(k * 2 + 1) * width];
-            }
-            s1 = fmaf(db, gm, s1);
-            s2 = fmaf(dg, gm, s2);
-        }
-    s1 = block_sum<1024>(s1, red);
-    s2 = block_sum<1024>(s2, red);
-    if (tid == 0) {
+    for (int64_t i = threadIdx.x; i < count * ny; i += 64) {
+        const int64_t k = i / ny;
+        const float2 v = *reinterpret_cast<const float2*>(s.sums + 2 * ((first + k) * runs + y0 + (i - k * ny) + g));
+        s1 += v.x;
+        s2 += v.y;
+    }
+    s1 = lane_sum(s1, 64);
+    s2 = lane_sum(s2, 64);
+    if (threadIdx.x == 0) {
         const float inv = n ? 1.0f / ((float)n * (float)s.W) : 0.0f;
         *reinterpret_cast<float2*>(s.joined + 2 * blockIdx.x) = float2{s1 * inv, s2 * inv};
     }
@@ -872,13 +918,18 @@ __global__ __launch_bounds__(256) void empty_stats_kernel(float* p, int64_t n) {
 
 enum Path { kToken, kSlab, kSplit };
 
+// Token path: up to here every workgroup may keep sums of all channels.
+constexpr int64_t kStraddleBytes = (int64_t)16 << 20;
+
 struct Choice {
     Path path;
     int V, cols;
     int lps, K, NT, rows;
     int64_t wgs, step;     // token, slab paths
+    int64_t parts;         // sums of dgamma and dbeta
+    int pg, unit;          // token path
     int64_t block, slots;  // split path
-    size_t part, total;    // workspace bytes: of dgamma and dbeta parts, in all
+    size_t part, sums, total;  // workspace bytes: of those sums, of the split path's, in all
 };
 
 int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
@@ -917,17 +968,29 @@ Choice choose(int V, int C, int N, int groups, int64_t T, int64_t batch, bool ra
         while (c.lps < c.cols && c.lps < 64) c.lps *= 2;
         c.K = 1;
         while (c.K * c.lps < c.cols) c.K *= 2;
-        const int per = 4 * (64 / c.lps), unit = groups / gcd(groups, per);  // slabs of a workgroup; whole tokens
-        const int64_t want = (T * groups + per - 1) / per, cap = backward ? 1024 : 2048;
-        c.wgs = round_up(want < cap ? want : cap, unit);
-        c.step = c.wgs * per / groups;
-        c.part = backward ? (size_t)c.wgs * 2 * C * 4 : 0;
+        // slabs of a workgroup; the workgroups step by whole tokens.  Groups that do not divide
+        // into them so that few workgroups are a step are padded: one token of 8191 groups
+        // would take 8191 workgroups
+        const int per = 4 * (64 / c.lps), cap = backward ? 1024 : 2048;
+        c.pg = groups;
+        int step = groups / gcd(groups, per);
+        if (groups % per && (step > 16 || (int64_t)(cap + step) * C * 8 > kStraddleBytes)) {
+            c.pg = (int)round_up(groups, groups > per ? per : (per + 15) / 16);
+            step = c.pg / gcd(c.pg, per);
+        }
+        c.unit = c.pg % per == 0 ? step : 0;
+        const int64_t want = (T * c.pg + per - 1) / per;
+        c.wgs = round_up(want < cap ? want : cap, step);
+        c.step = c.wgs * per / c.pg;
+        c.parts = c.unit ? c.wgs / c.unit : c.wgs;
+        c.part = backward ? (size_t)c.parts * 2 * C * 4 : 0;
     } else if (slab_shape(c, mean, backward, N % V == 0) && (c.K <= 8 || batch * groups >= 128)) {
         c.path = kSlab;
         c.rows = c.NT / c.cols;
         const int64_t cap = (backward ? 2048 : 8192) / groups;
         c.step = batch < cap ? batch : (cap < 1 ? 1 : cap);
         c.wgs = c.step * groups;
+        c.parts = c.step;
         c.part = backward ? (size_t)c.step * 2 * C * 4 : 0;
     } else {
         c.path = kSplit;
@@ -935,11 +998,16 @@ Choice choose(int V, int C, int N, int groups, int64_t T, int64_t batch, bool ra
         const int64_t b = (T + 511) / 512;
         c.block = b < 16 ? 16 : b;
         c.slots = T / c.block + batch;
-        c.part = backward ? (size_t)c.slots * 2 * C * N * 4 : (size_t)c.slots * groups * 2 * 4;
+        // about four workgroups per CU keep sums of dgamma and dbeta
+        const int64_t tiles = ((int64_t)c.cols * groups + 255) / 256, walkers = 1024 / tiles < 1 ? 1 : 1024 / tiles;
+        c.parts = c.slots < walkers ? c.slots : walkers;
+        c.part = backward ? (size_t)c.parts * 2 * C * N * 4 : 0;
+        c.sums = (size_t)c.slots * (backward ? tiles + groups : groups) * 2 * 4;
         c.total = (size_t)batch * groups * 2 * 4;
     }
     c.part = (size_t)round_up((int64_t)c.part, 256);
-    c.total = c.part + (size_t)round_up((int64_t)c.total, 256);
+    c.sums = (size_t)round_up((int64_t)c.sums, 256);
+    c.total = c.part + c.sums + (size_t)round_up((int64_t)c.total, 256);
     return c;
 }
 
@@ -961,10 +1029,12 @@ Norm norm_of(const NormArgs& a, const Choice& c, void* ws, bool backward) {
     s.step = c.step;
     s.block = c.block;
     s.slots = !a.offsets && c.path == kSplit ? a.batch * ((a.T / a.batch + c.block - 1) / c.block) : c.slots;
+    s.pg = c.pg;
+    s.unit = c.unit;
     char* w = static_cast<char*>(ws);
-    if (backward) s.part = reinterpret_cast<float*>(w);
-    else s.moments = reinterpret_cast<float*>(w);
-    s.joined = reinterpret_cast<float*>(w + c.part);
+    s.part = reinterpret_cast<float*>(w);
+    s.moments = s.sums = reinterpret_cast<float*>(w + c.part);
+    s.joined = reinterpret_cast<float*>(w + c.part + c.sums);
     return s;
 }
 
@@ -1007,7 +1077,7 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     Norm s = norm_of(a, c, ws, true);
     const bool params = a.dgamma || a.dbeta;
     const dim3 pgrid((uint32_t)((a.C + 31) / 32), 2);
-    int64_t parts = 0;
+    int64_t parts = c.parts;
     int per = 1;
     if (c.path == kToken) {
         if (!params) s.part = nullptr;
@@ -1018,7 +1088,6 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
             case 2: hipLaunchKernelGGL((token_backward_kernel<IO, V, CP, 2>), grid, dim3(256), 0, stream, s); break;
             default: hipLaunchKernelGGL((token_backward_kernel<IO, V, CP, 4>), grid, dim3(256), 0, stream, s);
         }
-        parts = c.wgs;
     } else if (c.path == kSlab) {
         if (!params) s.part = nullptr;
         if (c.wgs > 0x7fffffff) return hipErrorNotSupported;
@@ -1031,15 +1100,15 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
         if constexpr (CP > 1) { EQL_SLAB(6, 512) }
         EQL_SLAB(8, 512)
 #undef EQL_SLAB
-        parts = c.step;
     } else {
         const int64_t tiles = ((int64_t)c.cols * a.groups + 255) / 256;
         if (s.slots > 0x7fffffff || a.batch * a.groups > 0x7fffffff || tiles > 65535) return hipErrorNotSupported;
         const dim3 grid((uint32_t)s.slots, (uint32_t)tiles);
-        hipLaunchKernelGGL((sums_kernel<IO, V>), grid, dim3(256), 0, stream, s);
-        hipLaunchKernelGGL((join_sums_kernel<IO>), dim3((uint32_t)(a.batch * a.groups)), dim3(1024), 0, stream, s);
+        const int64_t walkers = s.slots < c.parts ? s.slots : c.parts;
+        hipLaunchKernelGGL((sums_kernel<IO, V>), dim3((uint32_t)walkers, (uint32_t)tiles), dim3(256), 0, stream, s);
+        hipLaunchKernelGGL(join_sums_kernel, dim3((uint32_t)(a.batch * a.groups)), dim3(64), 0, stream, s);
         hipLaunchKernelGGL((apply_backward_kernel<IO, V>), grid, dim3(256), 0, stream, s);
-        parts = s.slots;
+        parts = walkers;
         per = a.N;
     }
     if (params)

@@ -544,7 +544,10 @@ eqlinear_status eqlinear_norm_plan(eqlinear_plan_t* out, int N, int C, int group
                                    eqlinear_dtype dt);
 
 /* Bytes of workspace of eqlinear_group_norm, or with backward != 0 of either
- * call (0: none needed); 0 for other plans and negative sizes. */
+ * call (0: none needed); 0 for other plans and negative sizes.  It serves every
+ * alignment, so it does not depend on the tensors' own.  At most 72 MiB (backward)
+ * and, per sample and per 16 tokens, 8 bytes for each group and each 256 numbers of
+ * a token. */
 size_t eqlinear_group_norm_workspace(eqlinear_plan_t plan, int64_t T, int64_t batch, int backward);
 
 /* Group norm, channels last: for every sample b and group j, over the sample's
