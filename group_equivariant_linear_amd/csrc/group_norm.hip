@@ -349,16 +349,92 @@ __global__ __launch_bounds__(256) void token_backward_kernel(Norm s) {
     }
 }
 
+// (n, mean, m2) of two sets together
+__device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb, float m2b) {
+    const float nn = n + nb;
+    if (nn == 0.0f) return;
+    const float d = mb - mean, f = nb / nn;
+    mean = fmaf(d, f, mean);
+    m2 = m2 + m2b + d * d * n * f;
+    n = nn;
+}
+
+// the 64 lanes' sets, in lane 0
+__device__ __forceinline__ void merge_wave(float& n, float& mean, float& m2) {
+    for (int o = 32; o > 0; o >>= 1) {
+        const float nb = __shfl_down(n, o), mb = __shfl_down(mean, o), m2b = __shfl_down(m2, o);
+        merge(n, mean, m2, nb, mb, m2b);
+    }
+}
+
 // --- slab path ------------------------------------------------------------------------
 // A workgroup takes one group of samples b, b + step, ...: thread (row, piece) holds
 // tokens row, row + rows, ... of its piece, K of them in registers; tokens past those
 // (in packed batches, where one sample can be much longer than the mean) are read again
-// in each pass.
+// in each pass.  Past kLong times as many, the sums would be as long as the sample: its
+// statistics are merged from short runs, and its gradients' sums carry what their additions lose.
+// A sample is one workgroup's whatever its length.
+constexpr int kLong = 4;
+
+// sum += v, with the rounding of the addition kept in `lost` for the next one (Kahan 1965)
+__device__ __forceinline__ void add_kept(float& sum, float& lost, float v) {
+    const float y = v - lost, z = sum + y;
+    lost = (z - sum) - y;
+    sum = z;
+}
+
+// Mean and variance of a sample longer than the registers hold: moments of runs of R tokens
+// about `pivot` (a number near the mean), merged per thread, with what the additions lose, per
+// wave and over the waves.
+template <typename IO, int V, int NT>
+__device__ __forceinline__ float2 long_moments(const IO* x, int64_t ld, int64_t n, int row, int rows, bool on, float pivot,
+                                               float* red) {
+    using P = Piece<IO, V>;
+    constexpr int R = 4, WAVES = NT / 64;
+    float cn = 0.0f, cmean = 0.0f, cm2 = 0.0f, lmean = 0.0f, lm2 = 0.0f, v[V];
+    for (int64_t t0 = on ? row : n; t0 < n; t0 += (int64_t)R * rows) {
+        P q[R];
+        const int64_t left = (n - t0 + rows - 1) / rows;
+        const int m = left < R ? (int)left : R;
+#pragma unroll
+        for (int u = 0; u < R; ++u) q[u] = u < m ? P::load(x + (t0 + (int64_t)u * rows) * ld) : P::zero();
+        float d = 0.0f, d2 = 0.0f;
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (u < m) {
+                q[u].get(v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d += v[i] - pivot;
+            }
+        const float nb = (float)(m * V), mb = d / nb;
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (u < m) {
+                q[u].keep_packed();
+                q[u].get(v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d2 = fmaf(v[i] - pivot - mb, v[i] - pivot - mb, d2);
+            }
+        const float gap = mb - cmean, f = nb / (cn + nb);
+        add_kept(cmean, lmean, gap * f);
+        add_kept(cm2, lm2, d2 + gap * gap * cn * f);
+        cn += nb;
+    }
+    merge_wave(cn, cmean, cm2);
+    const int wave = (int)threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = cn, red[WAVES + wave] = cmean, red[2 * WAVES + wave] = cm2;
+    __syncthreads();
+    cn = red[0], cmean = red[WAVES], cm2 = red[2 * WAVES];
+    for (int w = 1; w < WAVES; ++w) merge(cn, cmean, cm2, red[w], red[WAVES + w], red[2 * WAVES + w]);
+    __syncthreads();
+    return float2{pivot + cmean, cm2 / cn};
+}
+
 template <typename IO, int V, int CP, int K, int NT>
 __global__ __launch_bounds__(NT) void slab_forward_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
-    __shared__ float red[NT / 64];
+    __shared__ float red[3 * (NT / 64)];
     const int g = (int)(blockIdx.x % (uint32_t)a.groups), tid = (int)threadIdx.x;
     const int row = tid / s.cols, col = tid - row * s.cols;
     const bool on = row < s.rows;
@@ -378,13 +454,31 @@ __global__ __launch_bounds__(NT) void slab_forward_kernel(Norm s) {
             const int64_t t = row + (int64_t)k * s.rows;
             p[k] = on && t < n ? P::load(x + t * a.ldx) : P::zero();
         }
-        const int64_t over = on ? row + (int64_t)K * s.rows : n;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             p[k].get(v);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += v[i];
         }
+        if (n > (int64_t)kLong * K * s.rows) [[unlikely]] {
+            sum = block_sum<NT>(sum, red) / ((float)(K * s.rows) * (float)s.W);
+            const float2 st = long_moments<IO, V, NT>(x, a.ldx, n, row, s.rows, on, sum, red);
+            const float mean = st.x, rstd = 1.0f / sqrtf(st.y + a.eps);
+            constexpr int U = 4;
+            for (int64_t t = on ? row : n; t < n; t += U * s.rows) {
+                P q[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    q[u] = t + u * s.rows < n ? P::load(x + (t + u * s.rows) * a.ldx) : P::zero();
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t + u * s.rows < n) put_y<IO>(a, y + (t + u * s.rows) * a.ldy, q[u], mean, rstd, gm, be);
+            }
+            if (a.stats && tid == 0)
+                *reinterpret_cast<float2*>(a.stats + 2 * (b * a.groups + g)) = float2{mean, rstd};
+            continue;
+        }
+        const int64_t over = on ? row + (int64_t)K * s.rows : n;
         for (int64_t t = over; t < n; t += s.rows) {
             P::load(x + t * a.ldx).get(v);
 #pragma unroll
@@ -467,6 +561,41 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : 2) void slab_backward_kernel(N
         const IO* dy = (const IO*)a.dy + t0 * a.lddy + e;
         IO* dx = (IO*)a.dx + t0 * a.lddx + e;
         const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * (b * a.groups + g));
+        if (n > (int64_t)kLong * K * s.rows) [[unlikely]] {
+            // sums of runs of eight tokens, added with what the additions lose
+            float xh[V], dz[V], hg[CP], hb[CP], lg[CP], lb[CP], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CP; ++i) hg[i] = hb[i] = lg[i] = lb[i] = 0.0f;
+            for (int64_t t0 = on ? row : n; t0 < n; t0 += 8 * s.rows) {
+                float sg[CP], sb[CP];
+#pragma unroll
+                for (int i = 0; i < CP; ++i) sg[i] = sb[i] = 0.0f;
+                for (int64_t t = t0; t < n && t < t0 + 8 * s.rows; t += s.rows) {
+                    get_dz<IO>(a, P::load(x + t * a.ldx), P::load(dy + t * a.lddy), st.x, st.y, gm, be, xh, dz);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        sg[i % CP] = fmaf(dz[i], xh[i], sg[i % CP]);
+                        sb[i % CP] += dz[i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < CP; ++i) add_kept(hg[i], lg[i], sg[i]), add_kept(hb[i], lb[i], sb[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < CP; ++i) {
+                s1 = fmaf(hb[i], gm[i], s1);
+                s2 = fmaf(hg[i], gm[i], s2);
+                dg[i] += hg[i];
+                db[i] += hb[i];
+            }
+            const float inv = 1.0f / ((float)n * (float)s.W);
+            const float m1 = block_sum<NT>(s1, red) * inv, m2 = block_sum<NT>(s2, red) * inv;
+            for (int64_t t = on ? row : n; t < n; t += s.rows) {
+                get_dz<IO>(a, P::load(x + t * a.ldx), P::load(dy + t * a.lddy), st.x, st.y, gm, be, xh, dz);
+                put_dx<IO>(dx + t * a.lddx, xh, dz, gm, m1, m2, st.y);
+            }
+            continue;
+        }
         P px[K];
         float d[K][V];  // dy, then dz: the slope is the costly part, and taken once
         float xh[V], dz[V], sg[CP], sb[CP];
@@ -591,24 +720,6 @@ __device__ __forceinline__ void blocks_of(const Norm& s, int64_t b, int64_t& fir
     n = t1 - t0;
     count = (n + s.block - 1) / s.block;
     first = s.a.offsets ? t0 / s.block + b : b * count;
-}
-
-// (n, mean, m2) of two sets together
-__device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb, float m2b) {
-    const float nn = n + nb;
-    if (nn == 0.0f) return;
-    const float d = mb - mean, f = nb / nn;
-    mean = fmaf(d, f, mean);
-    m2 = m2 + m2b + d * d * n * f;
-    n = nn;
-}
-
-// the 64 lanes' sets, in lane 0
-__device__ __forceinline__ void merge_wave(float& n, float& mean, float& m2) {
-    for (int o = 32; o > 0; o >>= 1) {
-        const float nb = __shfl_down(n, o), mb = __shfl_down(mean, o), m2b = __shfl_down(m2, o);
-        merge(n, mean, m2, nb, mb, m2b);
-    }
 }
 
 // One workgroup per (block of tokens, group): mean and squared differences.

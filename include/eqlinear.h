@@ -562,7 +562,13 @@ size_t eqlinear_group_norm_workspace(eqlinear_plan_t plan, int64_t T, int64_t ba
  *   stats fp32 [batch][groups][2] out: mean and 1/sqrt(var + eps) for the
  *         backward, or NULL; an empty sample has (0, 0); 8-byte aligned
  * Statistics are fp32 and do not cancel when the mean is large against the
- * spread.  Asynchronous on stream, no allocation; deterministic. */
+ * spread, whatever the lengths.  Packed lengths are on the device, so the mean
+ * length chooses the kernels: a sample many times longer than the others is read
+ * by one workgroup per group (64 samples of 96 x 8 bf16 numbers a token, forward
+ * and backward: 63 us at a mean of 197 tokens, 677 us with one of 11348 among 63
+ * of 20; 105008 tokens of 132 fp32 numbers among 15000 samples of one: 132 ms), and
+ * belongs in a call of its own.  Asynchronous on stream, no allocation;
+ * deterministic. */
 eqlinear_status eqlinear_group_norm(eqlinear_plan_t plan, const void* x, int64_t x_stride, const void* gamma,
                                     const void* beta, const int64_t* offsets, int64_t batch, void* y,
                                     int64_t y_stride, float* stats, int64_t T, void* workspace,
