@@ -48,16 +48,27 @@ bool writable(const Span& s) {
     return s.ts >= s.run && (s.n_heads == 1 || s.hs >= (s.T - 1) * s.ts + s.run);  // head after head
 }
 
-// Whether two tensors may share an element.  Equal token strides: each token's run
-// of heads is one interval modulo the stride.
+// Whether two tensors may share an element.  Apart are: address ranges that do not meet; with
+// equal token strides, rows (all of a token's runs) that do not meet modulo the stride; and with
+// equal head strides besides, runs that do not meet modulo the head stride (heads of q, k and v
+// in turn).
 bool collide(const Span& a, const Span& b) {
     if (!overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
+    if (a.es != b.es) return true;
+    const int64_t es = (int64_t)a.es, d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    auto rest = [](int64_t x, int64_t m) { return ((x % m) + m) % m; };
+    auto clear = [&](int64_t at, int64_t run_a, int64_t run_b, int64_t m) { return at >= run_a * es && at + run_b * es <= m; };
+    const int64_t head = (a.n_heads > 1 ? a.hs : b.hs) * es;
+    const bool one_head = a.n_heads == 1 && b.n_heads == 1;
+    const bool heads_alike = !one_head && head > 0 && (a.n_heads == 1 || b.n_heads == 1 || a.hs == b.hs);
+    if (a.T == 1 && b.T == 1) return !heads_alike || !clear(rest(d, head), a.run, b.run, head);
     const int64_t ra = a.row(), rb = b.row();
-    if (a.ts != b.ts || a.es != b.es || ra < 0 || rb < 0 || ra > a.ts || rb > b.ts) return true;
-    const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
-    const int64_t step = a.ts * (int64_t)a.es;
-    const int64_t at = ((d % step) + step) % step;  // byte offset of b's runs in a's rows
-    return at < ra * (int64_t)a.es || at + rb * (int64_t)a.es > step;
+    if (a.ts != b.ts || ra < 0 || rb < 0 || ra > a.ts || rb > b.ts) return true;
+    const int64_t step = a.ts * es, at = rest(d, step);  // byte offset of b's runs in a's rows
+    // b's row may meet the row of a that it starts in, and the next one
+    const bool this_row = at < ra * es, next_row = at + rb * es > step;
+    auto meet = [&](int64_t from) { return !heads_alike || !clear(rest(from, head), a.run, b.run, head); };
+    return (this_row && meet(at)) || (next_row && meet(at - step));
 }
 
 bool same_place(const Span& a, const Span& b) {

@@ -405,7 +405,8 @@ eqlinear_status eqlinear_dense_forward(eqlinear_plan_t plan, const void* x,
  *    faster.  Strides are in elements, >= 0; a stride of 0 repeats an input.
  *    Outputs must not repeat elements and must not overlap inputs or each
  *    other, except where a call allows its input as output.  Tensors whose
- *    address ranges interleave must have the same token stride.
+ *    address ranges interleave must have the same token stride, and those whose
+ *    rows do (heads of q, k and v in turn) the same head stride.
  *  - offsets: device, batch + 1 int64 values, the first token of each sequence
  *    and the end of the last (offsets[0] = 0, offsets[batch] = T, not
  *    decreasing; equal neighbours are an empty sequence); 8-byte aligned.
