@@ -2,6 +2,7 @@
 // positions, linear attention, group norm; declared in include/eqlinear.h): plans,
 // argument checks and dispatch.  Checks run before any HIP call.
 #include <cmath>
+#include <initializer_list>
 #include <new>
 
 #include "eq_plan.h"
@@ -85,6 +86,23 @@ bool batch_ok(const int64_t* offsets, int64_t batch, int64_t T) {
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
     return need == 0 || (ws && ((uintptr_t)ws & 255u) == 0 && bytes >= need);
+}
+
+// Flat buffers of a call (null or empty: not given): what it writes shares no byte with
+// anything else of it.
+struct Range {
+    const void* p;
+    uint64_t n;
+};
+bool disjoint(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    auto meet = [](const Range& a, const Range& b) { return a.p && b.p && a.n && b.n && overlaps(a.p, a.n, b.p, b.n); };
+    for (auto w = written.begin(); w != written.end(); ++w) {
+        for (auto v = written.begin(); v != w; ++v)
+            if (meet(*v, *w)) return false;
+        for (const Range& r : read)
+            if (meet(*w, r)) return false;
+    }
+    return true;
 }
 
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
@@ -256,6 +274,8 @@ eqlinear_status eqlinear_linear_attention(eqlinear_plan_t p, const eqlinear_head
     if (!log_decay || !aligned(log_decay, 4) || !state_ok(state_in, state_out, sb)) return EQL_ERR_INVALID;
     const size_t need = eqlinear_linear_attention_workspace(p, T, batch, 0);
     if (!workspace_ok(workspace, workspace_bytes, need)) return EQL_ERR_INVALID;
+    const Range decays{log_decay, (uint64_t)p->kv_heads * 4}, ends{offsets, (uint64_t)(batch + 1) * 8};
+    if (!disjoint({{state_out, sb}, {workspace, need}}, {decays, ends, {state_in, sb}})) return EQL_ERR_INVALID;
     eql::MixArgs a = mix_args(p, nullptr, nullptr, nullptr, log_decay, scale, offsets, batch, 0);
     if (T > 0) {
         if (!q || !k || !v || !o) return EQL_ERR_INVALID;
@@ -263,7 +283,8 @@ eqlinear_status eqlinear_linear_attention(eqlinear_plan_t p, const eqlinear_head
                             span_of(*v, T, p->kv_heads, Dv, es)};
         const Span to[1] = {span_of(*o, T, p->heads, Dv, es)};
         if (!tensors_ok(in, 3, to, 1)) return EQL_ERR_INVALID;
-        if (!apart(state_out, sb, in, 3) || !apart(state_out, sb, to, 1) || !apart(state_in, sb, to, 1))
+        if (!apart(state_out, sb, in, 3) || !apart(state_out, sb, to, 1) || !apart(state_in, sb, to, 1) ||
+            !apart(decays.p, decays.n, to, 1) || !apart(ends.p, ends.n, to, 1))
             return EQL_ERR_INVALID;
         if (need && (!apart(workspace, need, in, 3) || !apart(workspace, need, to, 1))) return EQL_ERR_INVALID;
         a = mix_args(p, q, k, v, log_decay, scale, offsets, batch, T);
@@ -293,6 +314,9 @@ eqlinear_status eqlinear_linear_attention_backward(eqlinear_plan_t p, const eqli
         return EQL_ERR_INVALID;
     const size_t need = eqlinear_linear_attention_workspace(p, T, batch, 1);
     if (!workspace_ok(workspace, workspace_bytes, need)) return EQL_ERR_INVALID;
+    const Range decays{log_decay, (uint64_t)p->kv_heads * 4}, ends{offsets, (uint64_t)(batch + 1) * 8};
+    if (!disjoint({{d_state_in, sb}, {workspace, need}}, {decays, ends, {state_in, sb}, {d_state_out, sb}}))
+        return EQL_ERR_INVALID;
     eql::MixArgs a = mix_args(p, nullptr, nullptr, nullptr, log_decay, scale, offsets, batch, 0);
     if (T > 0) {
         if (!q || !k || !v || !d_o || !dq || !dk || !dv) return EQL_ERR_INVALID;
@@ -302,7 +326,7 @@ eqlinear_status eqlinear_linear_attention_backward(eqlinear_plan_t p, const eqli
                             span_of(*dv, T, p->kv_heads, Dv, es)};
         if (!tensors_ok(in, 4, to, 3)) return EQL_ERR_INVALID;
         if (!apart(d_state_in, sb, in, 4) || !apart(d_state_in, sb, to, 3) || !apart(state_in, sb, to, 3) ||
-            !apart(d_state_out, sb, to, 3))
+            !apart(d_state_out, sb, to, 3) || !apart(decays.p, decays.n, to, 3) || !apart(ends.p, ends.n, to, 3))
             return EQL_ERR_INVALID;
         if (need && (!apart(workspace, need, in, 4) || !apart(workspace, need, to, 3))) return EQL_ERR_INVALID;
         a = mix_args(p, q, k, v, log_decay, scale, offsets, batch, T);
@@ -330,6 +354,8 @@ eqlinear_status eqlinear_linear_attention_step(eqlinear_plan_t p, const eqlinear
                         span_of(*v, batch, p->kv_heads, Dv, es)};
     const Span to[1] = {span_of(*o, batch, p->heads, Dv, es)};
     if (!tensors_ok(in, 3, to, 1) || !apart(state, sb, in, 3) || !apart(state, sb, to, 1)) return EQL_ERR_INVALID;
+    const uint64_t db = (uint64_t)p->kv_heads * 4;
+    if (!disjoint({{state, sb}}, {{log_decay, db}}) || !apart(log_decay, db, to, 1)) return EQL_ERR_INVALID;
     eql::MixArgs a = mix_args(p, q, k, v, log_decay, scale, nullptr, batch, batch);
     a.o = heads_of(*o);
     a.state_in = a.state_out = state;
@@ -391,15 +417,16 @@ eqlinear_status eqlinear_group_norm(eqlinear_plan_t p, const void* x, int64_t x_
     if (stats && !aligned(stats, 8)) return EQL_ERR_INVALID;
     const size_t need = eqlinear_group_norm_workspace(p, T, batch, 0);
     if (!workspace_ok(workspace, workspace_bytes, need)) return EQL_ERR_INVALID;
+    const uint64_t sb = (uint64_t)batch * p->groups * 8, cb = (uint64_t)p->C_in * es;
+    const Range ends{offsets, (uint64_t)(batch + 1) * 8};
+    if (!disjoint({{stats, sb}, {workspace, need}}, {{gamma, cb}, {beta, cb}, ends})) return EQL_ERR_INVALID;
     eql::NormArgs a = norm_args(p, x, x_stride, gamma, beta, offsets, batch, T);
     if (T > 0) {
         const Span in{x, T, x_stride, 1, 0, W, es}, to{y, T, y_stride, 1, 0, W, es};
         if (!readable(in) || !writable(to) || (!same_place(in, to) && collide(to, in))) return EQL_ERR_INVALID;
-        const size_t cb = (size_t)p->C_in * es;
         for (const void* v : {gamma, beta})
             if (v && (!aligned(v, es) || !apart(v, cb, &to, 1))) return EQL_ERR_INVALID;
-        const uint64_t sb = (uint64_t)batch * p->groups * 8;
-        if (!apart(stats, sb, &in, 1) || !apart(stats, sb, &to, 1)) return EQL_ERR_INVALID;
+        if (!apart(stats, sb, &in, 1) || !apart(stats, sb, &to, 1) || !apart(ends.p, ends.n, &to, 1)) return EQL_ERR_INVALID;
         if (need && (!apart(workspace, need, &in, 1) || !apart(workspace, need, &to, 1))) return EQL_ERR_INVALID;
         a.y = y;
         a.ldy = y_stride;
@@ -422,6 +449,10 @@ eqlinear_status eqlinear_group_norm_backward(eqlinear_plan_t p, const void* dy, 
     const int64_t W = (int64_t)p->C_in * p->N;
     const size_t need = eqlinear_group_norm_workspace(p, T, batch, 1);
     if (!workspace_ok(workspace, workspace_bytes, need)) return EQL_ERR_INVALID;
+    const uint64_t sb = (uint64_t)batch * p->groups * 8, cb = (uint64_t)p->C_in * es;
+    const Range ends{offsets, (uint64_t)(batch + 1) * 8};
+    if (!disjoint({{dgamma, gb}, {dbeta, gb}, {workspace, need}}, {{gamma, cb}, {beta, cb}, {stats, sb}, ends}))
+        return EQL_ERR_INVALID;
     eql::NormArgs a = norm_args(p, x, x_stride, gamma, beta, offsets, batch, T);
     if (T > 0) {
         if (!stats || !aligned(stats, 8)) return EQL_ERR_INVALID;
@@ -429,11 +460,9 @@ eqlinear_status eqlinear_group_norm_backward(eqlinear_plan_t p, const void* dy, 
         const Span to{dx, T, dx_stride, 1, 0, W, es};
         if (!readable(in[0]) || !readable(in[1]) || !writable(to) || collide(to, in[0])) return EQL_ERR_INVALID;
         if (!same_place(in[1], to) && collide(to, in[1])) return EQL_ERR_INVALID;
-        const size_t cb = (size_t)p->C_in * es;
         for (const void* v : {gamma, beta})
             if (v && (!aligned(v, es) || !apart(v, cb, &to, 1))) return EQL_ERR_INVALID;
-        const uint64_t sb = (uint64_t)batch * p->groups * 8;
-        if (!apart(stats, sb, &to, 1)) return EQL_ERR_INVALID;
+        if (!apart(stats, sb, &to, 1) || !apart(ends.p, ends.n, &to, 1)) return EQL_ERR_INVALID;
         for (const float* v : {dgamma, dbeta})
             if (!apart(v, gb, in, 2) || !apart(v, gb, &to, 1)) return EQL_ERR_INVALID;
         if (need && (!apart(workspace, need, in, 2) || !apart(workspace, need, &to, 1))) return EQL_ERR_INVALID;

@@ -404,7 +404,8 @@ eqlinear_status eqlinear_dense_forward(eqlinear_plan_t plan, const void* x,
  *    element alignment only; whole 16-byte rows (address and strides) run
  *    faster.  Strides are in elements, >= 0; a stride of 0 repeats an input.
  *    Outputs must not repeat elements and must not overlap inputs or each
- *    other, except where a call allows its input as output.  Tensors whose
+ *    other (states, statistics, parameters, offsets and the workspace among them),
+ *    except where a call allows its input as output.  Tensors whose
  *    address ranges interleave must have the same token stride, and those whose
  *    rows do (heads of q, k and v in turn) the same head stride.
  *  - offsets: device, batch + 1 int64 values, the first token of each sequence
