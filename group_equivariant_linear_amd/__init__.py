@@ -7,7 +7,9 @@ All arithmetic runs in the library's HIP kernels; there is no fallback path.
 If the library has not been built, loading fails loudly.
 
 Tensor arguments may be torch tensors on a ROCm device, or plain integers
-(raw device addresses, for callers that manage memory themselves).
+(raw device addresses, for callers that manage memory themselves); where a call
+takes strides, an address stands for contiguous rows, or comes with its strides
+as an eqlinear_heads.
 """
 from __future__ import annotations
 
@@ -485,10 +487,13 @@ def _raw_stream(stream):
 
 
 def _heads(t, plan: Plan, T: int, heads: int, d: int, name: str):
-    """A tensor [T, heads, d, N] (the last two axes contiguous) or an eqlinear_heads as it is."""
+    """A tensor [T, heads, d, N] (the last two axes contiguous), the address of a contiguous one, or an
+    eqlinear_heads as it is."""
     if type(t) is eqlinear_heads:
         return t
     N = plan.N
+    if type(t) is int:
+        return eqlinear_heads(t, heads * d * N, d * N)
     _gpu(t, name, plan.torch_dtype)
     if t.shape != (T, heads, d, N):
         raise ValueError(f"{name}: expected shape {(T, heads, d, N)}, got {tuple(t.shape)}")
@@ -637,8 +642,13 @@ def eqlinear_group_norm_workspace(plan: Plan, T: int, batch: int, backward: bool
 
 
 def _tokens_of(t, plan: Plan, T: int, name: str):
-    """(address, token stride) of a tensor [T, C, N] with the last two axes contiguous."""
+    """(address, token stride) of a tensor [T, C, N] with the last two axes contiguous, of a contiguous one's
+    address, or of an eqlinear_heads."""
     C, N = plan.C, plan.N
+    if type(t) is int:
+        return t, C * N
+    if type(t) is eqlinear_heads:
+        return t.ptr, t.token_stride
     _gpu(t, name, plan.torch_dtype)
     if t.shape != (T, C, N):
         raise ValueError(f"{name}: expected shape {(T, C, N)}, got {tuple(t.shape)}")
@@ -649,13 +659,13 @@ def _tokens_of(t, plan: Plan, T: int, name: str):
 
 
 def eqlinear_group_norm(plan: Plan, x, gamma, beta, y, stats=None, offsets=None, batch: int | None = None,
-                        workspace=None, stream=None):
+                        workspace=None, T: int | None = None, stream=None):
     """y = act(gamma (x - mean) / sqrt(var + eps) + beta), statistics over each sample's tokens, a group's
     channels and their group elements; x, y [T, C, N].  The samples are offsets (int64 [batch + 1]) or batch
     equal runs (default: one)."""
     torch = _torch()
     _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm")
-    T, C, dt = x.shape[0], plan.C, plan.torch_dtype
+    T, C, dt = _count(x, T, "x"), plan.C, plan.torch_dtype
     off, B = _sequences(offsets, batch)
     ws, nb = _workspace(workspace)
     _check(plan._lib.eqlinear_group_norm(
@@ -665,11 +675,11 @@ def eqlinear_group_norm(plan: Plan, x, gamma, beta, y, stats=None, offsets=None,
 
 
 def eqlinear_group_norm_backward(plan: Plan, dy, x, gamma, beta, stats, dx, dgamma, dbeta, offsets=None,
-                                 batch: int | None = None, workspace=None, stream=None):
+                                 batch: int | None = None, workspace=None, T: int | None = None, stream=None):
     """Gradients of eqlinear_group_norm: dx [T, C, N] in the plan dtype, dgamma and dbeta fp32 [C] (or None)."""
     torch = _torch()
     _kind(plan, EQL_KIND_NORM, "eqlinear_group_norm_backward")
-    T, C, dt = x.shape[0], plan.C, plan.torch_dtype
+    T, C, dt = _count(x, T, "x"), plan.C, plan.torch_dtype
     off, B = _sequences(offsets, batch)
     ws, nb = _workspace(workspace)
     _check(plan._lib.eqlinear_group_norm_backward(
