@@ -478,11 +478,21 @@ def _torch():
     return torch
 
 
+@functools.lru_cache(maxsize=None)
+def _current_stream():
+    """A function to the current device's current hipStream_t: torch's own short one where this torch has it (0.2 us;
+    2.7 us through torch.cuda.current_stream(), of the 7 us that a call takes)."""
+    torch = _torch()
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _raw_stream(stream):
     """hipStream_t of a torch stream or an address; None: the current stream of the current device."""
     if stream is None:
-        c = _torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        return _current_stream()()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

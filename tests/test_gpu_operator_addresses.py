@@ -1,4 +1,4 @@
-"""The operators given device addresses instead of tensors: the same bits."""
+"""The operators given device addresses instead of tensors: the same bits.  And the stream they run on by default."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +80,12 @@ def test_group_norm(eq, strided, offsets):
         res.append((y, st, dx, dg, db))
     for a, b in zip(*res):
         assert torch.equal(a, b)
+
+
+def test_default_stream(eq):
+    """No stream given: torch's current one, also where torch lacks its short way to it."""
+    import torch
+    s = torch.cuda.Stream()
+    assert eq._raw_stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(s):
+        assert eq._raw_stream(None) == s.cuda_stream == eq._raw_stream(s) == eq._raw_stream(s.cuda_stream)

@@ -32,3 +32,19 @@ def test_addresses_pass_the_rows_strides(eq):
     r = eq.eqlinear_rotary_plan(8, 2, 1, 4, 4, 0, eq.EQL_F32)
     h = eq._heads(1 << 32, r, 5, 2, 4, "q")
     assert (h.ptr, h.token_stride, h.head_stride) == (1 << 32, 64, 32)
+
+
+def test_current_stream_without_the_short_way(eq, monkeypatch):
+    import torch
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    eq._current_stream.cache_clear()
+
+    # (a fake: no GPU here)
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    try:
+        assert eq._raw_stream(None) == 77
+    finally:
+        eq._current_stream.cache_clear()
