@@ -99,6 +99,15 @@ hipError_t launch_dn_to_regular(int n, int io, const void* y_four, void* y_reg, 
 
 // --- operators between the layers ---------------------------------------------------
 
+// launch(base, n) for workgroups base .. base + n - 1 of blocks, `threads` each: a launch holds
+// fewer than 2^32 threads (with more the runtime starts the rest modulo 2^32 and reports success).
+template <typename F>
+inline void in_pieces(int64_t blocks, int threads, F&& launch) {
+    const int64_t most = (int64_t)0xffffffff / threads / 8 * 8;  // whole rounds of the XCDs
+    for (int64_t base = 0; base < blocks; base += most)
+        launch((uint32_t)base, (uint32_t)(blocks - base < most ? blocks - base : most));
+}
+
 // Tensor [T][heads][D], the last axis contiguous; strides in elements.
 struct Heads {
     const void* p;

@@ -36,6 +36,7 @@ struct Norm {
     int rows;              // slab, split paths: tokens that a workgroup covers at once
     int64_t step;          // token path: tokens from one pass to the next; slab path: samples
     int64_t block, slots;  // split path: tokens of a block, blocks
+    uint32_t base;         // split path: first workgroup of this launch
     float* part;           // dgamma and dbeta of part of the tokens: [..][2][C]
     float* moments;        // split path: [slots][groups][2]
     float* sums;           // split path, backward: [slots][tiles + groups][2]
@@ -729,8 +730,9 @@ __global__ __launch_bounds__(256) void moments_kernel(Norm s) {
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
     __shared__ float red[3][4];
-    const int tid = (int)threadIdx.x, g = (int)(blockIdx.x % (uint32_t)a.groups);
-    const int64_t slot = blockIdx.x / (uint32_t)a.groups;
+    const uint32_t wg = blockIdx.x + s.base;
+    const int tid = (int)threadIdx.x, g = (int)(wg % (uint32_t)a.groups);
+    const int64_t slot = wg / (uint32_t)a.groups;
     const Block k = block_of(s, slot);
     if (k.idle) return;
     const IO* x = (const IO*)a.x + k.t0 * a.ldx + g * s.W;
@@ -773,15 +775,16 @@ __global__ __launch_bounds__(256) void moments_kernel(Norm s) {
     __syncthreads();
     if (tid == 0) {
         for (int w = 1; w < 4; ++w) merge(n, mean, m2, red[0][w], red[1][w], red[2][w]);
-        *reinterpret_cast<float2*>(s.moments + 2 * blockIdx.x) = float2{mean, m2};
+        *reinterpret_cast<float2*>(s.moments + 2 * (int64_t)wg) = float2{mean, m2};
     }
 }
 
 // One wave per slab: the blocks' moments to mean and 1/sqrt(var + eps).
 __global__ __launch_bounds__(64) void join_moments_kernel(Norm s) {
     const NormArgs& a = s.a;
-    const int64_t b = blockIdx.x / (uint32_t)a.groups;
-    const int g = (int)(blockIdx.x % (uint32_t)a.groups), lane = (int)threadIdx.x;
+    const uint32_t wg = blockIdx.x + s.base;
+    const int64_t b = wg / (uint32_t)a.groups;
+    const int g = (int)(wg % (uint32_t)a.groups), lane = (int)threadIdx.x;
     int64_t first, count, tokens;
     blocks_of(s, b, first, count, tokens);
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
@@ -793,8 +796,8 @@ __global__ __launch_bounds__(64) void join_moments_kernel(Norm s) {
     merge_wave(n, mean, m2);
     if (lane == 0) {
         const float2 r = n > 0.0f ? float2{mean, 1.0f / sqrtf(m2 / n + a.eps)} : float2{0.0f, 0.0f};
-        *reinterpret_cast<float2*>(s.joined + 2 * blockIdx.x) = r;
-        if (a.stats) *reinterpret_cast<float2*>(a.stats + 2 * blockIdx.x) = r;
+        *reinterpret_cast<float2*>(s.joined + 2 * (int64_t)wg) = r;
+        if (a.stats) *reinterpret_cast<float2*>(a.stats + 2 * (int64_t)wg) = r;
     }
 }
 
@@ -824,7 +827,7 @@ __global__ __launch_bounds__(256) void apply_forward_kernel(Norm s) {
     constexpr int U = 4;
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
-    const Block k = block_of(s, blockIdx.x);
+    const Block k = block_of(s, blockIdx.x + s.base);
     if (k.idle) return;
     const RowTile<IO, V> rt(s);
     if (!rt.on) return;
@@ -941,8 +944,9 @@ __global__ __launch_bounds__(256) void sums_kernel(Norm s) {
 // One wave per slab: m1 and m2 from its blocks' sums.
 __global__ __launch_bounds__(64) void join_sums_kernel(Norm s) {
     const NormArgs& a = s.a;
-    const int64_t b = blockIdx.x / (uint32_t)a.groups;
-    const int g = (int)(blockIdx.x % (uint32_t)a.groups);
+    const uint32_t wg = blockIdx.x + s.base;
+    const int64_t b = wg / (uint32_t)a.groups;
+    const int g = (int)(wg % (uint32_t)a.groups);
     int64_t first, count, n;
     blocks_of(s, b, first, count, n);
     const int64_t tiles = ((int64_t)s.cols * a.groups + 255) / 256, runs = tiles + a.groups;
@@ -958,7 +962,7 @@ __global__ __launch_bounds__(64) void join_sums_kernel(Norm s) {
     s2 = lane_sum(s2, 64);
     if (threadIdx.x == 0) {
         const float inv = n ? 1.0f / ((float)n * (float)s.W) : 0.0f;
-        *reinterpret_cast<float2*>(s.joined + 2 * blockIdx.x) = float2{s1 * inv, s2 * inv};
+        *reinterpret_cast<float2*>(s.joined + 2 * (int64_t)wg) = float2{s1 * inv, s2 * inv};
     }
 }
 
@@ -967,7 +971,7 @@ __global__ __launch_bounds__(256) void apply_backward_kernel(Norm s) {
     constexpr int U = 4;
     const NormArgs& a = s.a;
     using P = Piece<IO, V>;
-    const Block k = block_of(s, blockIdx.x);
+    const Block k = block_of(s, blockIdx.x + s.base);
     if (k.idle) return;
     const RowTile<IO, V> rt(s);
     if (!rt.on) return;
@@ -1020,8 +1024,8 @@ __global__ __launch_bounds__(1024) void param_sums_kernel(const float* part, int
     if (r == 0 && c < C) to[c] = acc[0][lc];
 }
 
-__global__ __launch_bounds__(256) void empty_stats_kernel(float* p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void empty_stats_kernel(float* p, int64_t n, uint32_t base) {
+    const int64_t i = (int64_t)(blockIdx.x + base) * 256 + threadIdx.x;
     if (i < n) p[i] = 0.0f;
 }
 
@@ -1152,7 +1156,7 @@ Norm norm_of(const NormArgs& a, const Choice& c, void* ws, bool backward) {
 template <typename IO, int V, int CP>
 hipError_t forward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     const Choice c = choose(V, a.C, a.N, a.groups, a.T, a.batch, a.offsets != nullptr, false);
-    const Norm s = norm_of(a, c, ws, false);
+    Norm s = norm_of(a, c, ws, false);
     if (c.path == kToken) {
         if (c.wgs > 0x7fffffff) return hipErrorNotSupported;
         const dim3 grid((uint32_t)c.wgs);
@@ -1174,10 +1178,18 @@ hipError_t forward_v(const NormArgs& a, void* ws, hipStream_t stream) {
         if (s.slots * a.groups > 0x7fffffff || a.batch * a.groups > 0x7fffffff || tiles > 65535 ||
             c.block * (int64_t)c.cols > 0x3fffffff)
             return hipErrorNotSupported;
-        hipLaunchKernelGGL((moments_kernel<IO, V>), dim3((uint32_t)(s.slots * a.groups)), dim3(256), 0, stream, s);
-        hipLaunchKernelGGL(join_moments_kernel, dim3((uint32_t)(a.batch * a.groups)), dim3(64), 0, stream, s);
-        hipLaunchKernelGGL((apply_forward_kernel<IO, V>), dim3((uint32_t)s.slots, (uint32_t)tiles), dim3(256), 0, stream,
-                           s);
+        in_pieces(s.slots * a.groups, 256, [&](uint32_t base, uint32_t n) {
+            s.base = base;
+            hipLaunchKernelGGL((moments_kernel<IO, V>), dim3(n), dim3(256), 0, stream, s);
+        });
+        in_pieces(a.batch * a.groups, 64, [&](uint32_t base, uint32_t n) {
+            s.base = base;
+            hipLaunchKernelGGL(join_moments_kernel, dim3(n), dim3(64), 0, stream, s);
+        });
+        in_pieces(s.slots, 256, [&](uint32_t base, uint32_t n) {
+            s.base = base;
+            hipLaunchKernelGGL((apply_forward_kernel<IO, V>), dim3(n, (uint32_t)tiles), dim3(256), 0, stream, s);
+        });
     }
     return hipGetLastError();
 }
@@ -1214,11 +1226,16 @@ hipError_t backward_v(const NormArgs& a, void* ws, hipStream_t stream) {
     } else {
         const int64_t tiles = ((int64_t)c.cols * a.groups + 255) / 256;
         if (s.slots > 0x7fffffff || a.batch * a.groups > 0x7fffffff || tiles > 65535) return hipErrorNotSupported;
-        const dim3 grid((uint32_t)s.slots, (uint32_t)tiles);
         const int64_t walkers = s.slots < c.parts ? s.slots : c.parts;
         hipLaunchKernelGGL((sums_kernel<IO, V>), dim3((uint32_t)walkers, (uint32_t)tiles), dim3(256), 0, stream, s);
-        hipLaunchKernelGGL(join_sums_kernel, dim3((uint32_t)(a.batch * a.groups)), dim3(64), 0, stream, s);
-        hipLaunchKernelGGL((apply_backward_kernel<IO, V>), grid, dim3(256), 0, stream, s);
+        in_pieces(a.batch * a.groups, 64, [&](uint32_t base, uint32_t n) {
+            s.base = base;
+            hipLaunchKernelGGL(join_sums_kernel, dim3(n), dim3(64), 0, stream, s);
+        });
+        in_pieces(s.slots, 256, [&](uint32_t base, uint32_t n) {
+            s.base = base;
+            hipLaunchKernelGGL((apply_backward_kernel<IO, V>), dim3(n, (uint32_t)tiles), dim3(256), 0, stream, s);
+        });
         parts = walkers;
         per = a.N;
     }
@@ -1266,7 +1283,9 @@ hipError_t launch_group_norm(int io, const NormArgs& a, void* ws, hipStream_t st
     if (a.T == 0) {  // empty samples alone
         const int64_t n = a.batch * a.groups * 2;
         if ((n + 255) / 256 > 0x7fffffff) return hipErrorNotSupported;
-        hipLaunchKernelGGL(empty_stats_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, stream, a.stats, n);
+        in_pieces((n + 255) / 256, 256, [&](uint32_t base, uint32_t wgs) {
+            hipLaunchKernelGGL(empty_stats_kernel, dim3(wgs), dim3(256), 0, stream, a.stats, n, base);
+        });
         return hipGetLastError();
     }
     return io == kIoF32 ? forward<float>(io, a, ws, stream)

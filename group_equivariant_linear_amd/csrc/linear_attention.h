@@ -49,6 +49,7 @@ constexpr int kMaxJobs = 3;
 struct Jobs {
     Job j[kMaxJobs];
     uint32_t first[kMaxJobs + 1];
+    uint32_t base;  // of this launch
     int count;
 };
 
@@ -535,7 +536,7 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     constexpr int NS = C::NS, KF = O::KF, ES = C::ES;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
 
-    const uint32_t wg = blockIdx.x;
+    const uint32_t wg = blockIdx.x + jobs.base;
     const int which = wg >= jobs.first[2] ? 2 : (wg >= jobs.first[1] ? 1 : 0);
     const Job j = which == 2 ? jobs.j[2] : (which == 1 ? jobs.j[1] : jobs.j[0]);
     const uint32_t first = jobs.first[which == 2 ? 2 : (which == 1 ? 1 : 0)];
@@ -1225,16 +1226,22 @@ hipError_t run_cfg(Jobs& jobs, hipStream_t stream) {
     if (jobs.j[0].seg_len) {
         const int64_t n = grid(false);
         if (n == 0) return hipErrorNotSupported;
-        hipLaunchKernelGGL((chunk_kernel<CS, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
+        in_pieces(n, C::NT, [&](uint32_t base, uint32_t wgs) {
+            jobs.base = base;
+            hipLaunchKernelGGL((chunk_kernel<CS, VEC>), dim3(wgs), dim3(C::NT), 0, stream, jobs);
+        });
         const Job& j = jobs.j[0];
         const int64_t threads = j.batch * (j.Ha < j.Hb ? j.Ha : j.Hb) * (C::NW * C::NB * 64);
-        if ((threads + 255) / 256 > 0x7fffffff) return hipErrorNotSupported;
+        if (threads > 0x7fffffff) return hipErrorNotSupported;  // (segments are for few sequences)
         hipLaunchKernelGGL((join_kernel<C>), dim3((uint32_t)((threads + 255) / 256), (uint32_t)jobs.count), dim3(256), 0,
                            stream, jobs);
     }
     const int64_t n = grid(true);
     if (n == 0) return hipErrorNotSupported;
-    hipLaunchKernelGGL((chunk_kernel<C, VEC>), dim3((uint32_t)n), dim3(C::NT), 0, stream, jobs);
+    in_pieces(n, C::NT, [&](uint32_t base, uint32_t wgs) {
+        jobs.base = base;
+        hipLaunchKernelGGL((chunk_kernel<C, VEC>), dim3(wgs), dim3(C::NT), 0, stream, jobs);
+    });
     return hipGetLastError();
 }
 

@@ -123,15 +123,16 @@ namespace {
 // sequences, 4 kv heads of 128 x 128 (273 MB): 59.5 us, 4.6 TB/s, a copy's rate; 8
 // sequences: 4.9 us of one launch.
 template <typename IO, bool VEC, int HB>
-__global__ __launch_bounds__(256) void step_kernel(MixArgs a, int cols) {
+__global__ __launch_bounds__(256) void step_kernel(MixArgs a, int cols, uint32_t base) {
     constexpr int U = 4, W = VEC ? 4 : 1;  // columns of a thread
     __shared__ float vk[kMaxD], vq[HB][kMaxD], red[HB][256 * W];
-    const int64_t b = blockIdx.x / (uint32_t)a.kv_heads;
-    const int kv = (int)(blockIdx.x % (uint32_t)a.kv_heads), r = a.heads / a.kv_heads, tid = (int)threadIdx.x;
+    const uint32_t wg = blockIdx.x + base;
+    const int64_t b = wg / (uint32_t)a.kv_heads;
+    const int kv = (int)(wg % (uint32_t)a.kv_heads), r = a.heads / a.kv_heads, tid = (int)threadIdx.x;
     const int rows = 256 / cols, row = tid / cols, c = (tid - row * cols) * W;
     const bool on = row < rows;
     using R = std::conditional_t<VEC, f32x4, float>;
-    float* S = a.state_out + (int64_t)blockIdx.x * a.D_k * a.D_v + c;
+    float* S = a.state_out + (int64_t)wg * a.D_k * a.D_v + c;
     const float g = power(a.log_decay[kv] * kLog2e, 1);
     R v{};
     if (on) {
@@ -191,16 +192,16 @@ __global__ __launch_bounds__(256) void step_kernel(MixArgs a, int cols) {
 
 template <typename IO>
 hipError_t step(const MixArgs& a, hipStream_t stream) {
-    const dim3 grid((uint32_t)(a.batch * a.kv_heads));
     const int r = a.heads / a.kv_heads;
-    if (a.D_v % 4 == 0) {
-        const int cols = a.D_v / 4;
-        if (r == 1) hipLaunchKernelGGL((step_kernel<IO, true, 1>), grid, dim3(256), 0, stream, a, cols);
-        else if (r == 2) hipLaunchKernelGGL((step_kernel<IO, true, 2>), grid, dim3(256), 0, stream, a, cols);
-        else hipLaunchKernelGGL((step_kernel<IO, true, 4>), grid, dim3(256), 0, stream, a, cols);
-    } else {
-        hipLaunchKernelGGL((step_kernel<IO, false, 2>), grid, dim3(256), 0, stream, a, a.D_v);
-    }
+    const bool vec = a.D_v % 4 == 0;
+    const int cols = vec ? a.D_v / 4 : a.D_v;
+    in_pieces(a.batch * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
+        const dim3 grid(wgs);
+        if (!vec) hipLaunchKernelGGL((step_kernel<IO, false, 2>), grid, dim3(256), 0, stream, a, cols, base);
+        else if (r == 1) hipLaunchKernelGGL((step_kernel<IO, true, 1>), grid, dim3(256), 0, stream, a, cols, base);
+        else if (r == 2) hipLaunchKernelGGL((step_kernel<IO, true, 2>), grid, dim3(256), 0, stream, a, cols, base);
+        else hipLaunchKernelGGL((step_kernel<IO, true, 4>), grid, dim3(256), 0, stream, a, cols, base);
+    });
     return hipGetLastError();
 }
 

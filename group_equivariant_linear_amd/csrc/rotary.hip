@@ -65,13 +65,13 @@ struct Vec {  // E numbers
 };
 
 template <typename IO, int MODE, int U>
-__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryFreq f, Items it) {
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryFreq f, Items it, uint32_t base) {
     constexpr int E = MODE == kSingle ? 1 : 16 / (int)sizeof(IO);
     using V = Vec<IO, E>;
     using R = typename V::R;
     __shared__ float2 cs[kMaxAngles];
     const int half = a.rot / 2, tid = (int)threadIdx.x;
-    const int64_t t0 = (int64_t)blockIdx.x * it.tokens;
+    const int64_t t0 = (int64_t)(blockIdx.x + base) * it.tokens;
     const int n = (int)(a.T - t0 < it.tokens ? a.T - t0 : it.tokens);
     for (int i = tid; i < n * half; i += kThreads) {
         const int t = i / half;
@@ -180,9 +180,11 @@ hipError_t launch_mode(const RotaryArgs& a, const RotaryFreq& f, Items it, hipSt
     it.tokens = four ? 4 * it.rows : it.rows;
     const int64_t wgs = (a.T + it.tokens - 1) / it.tokens;
     if (wgs > 0x7fffffff || tiles > 65535) return hipErrorNotSupported;
-    const dim3 grid((uint32_t)wgs, (uint32_t)tiles);
-    if (four) hipLaunchKernelGGL((rotary_kernel<IO, MODE, 4>), grid, dim3(kThreads), 0, stream, a, f, it);
-    else hipLaunchKernelGGL((rotary_kernel<IO, MODE, 1>), grid, dim3(kThreads), 0, stream, a, f, it);
+    in_pieces(wgs, kThreads, [&](uint32_t base, uint32_t n) {
+        const dim3 grid(n, (uint32_t)tiles);
+        if (four) hipLaunchKernelGGL((rotary_kernel<IO, MODE, 4>), grid, dim3(kThreads), 0, stream, a, f, it, base);
+        else hipLaunchKernelGGL((rotary_kernel<IO, MODE, 1>), grid, dim3(kThreads), 0, stream, a, f, it, base);
+    });
     return hipGetLastError();
 }
 
