@@ -13,13 +13,13 @@
 // blocks, merged from such by mean and squared sum (Chan, Golub, LeVeque 1983).
 // The sums run in a fixed order.  Memory is the floor of all three; measured, 96 x 8
 // numbers a token in bf16:
-//   token  12608 tokens: forward 12.8 us (38.7 MB, 3.0 TB/s), backward 17.6 and 4.3 for the
+//   token  12608 tokens: forward 12.7 us (38.7 MB, 3.0 TB/s), backward 18.0 and 4.2 for the
 //          sums of dgamma and dbeta;
-//   slab   64 images of 197 tokens: forward 23 us, backward 30 (equal lengths) or 37
+//   slab   64 images of 197 tokens: forward 23 us, backward 30 (equal lengths) or 38
 //          (unequal ones); bound by GELU's arithmetic and by workgroups of one
 //          pass each: all loads first, then all sums, then all stores;
-//   split  one map of 32768 tokens (160 x 7, f16): sums 24 us, join 6, outputs 28 (147 MB,
-//          5.3 TB/s); x is read twice, the second time partly from the last-level cache.
+//   split  one map of 32768 tokens (160 x 7, f16): sums 25 us, join 6, outputs 28 (147 MB,
+//          5.2 TB/s); x is read twice, the second time partly from the last-level cache.
 #include "activation.h"
 #include "eq_device.h"
 #include "eq_launch.h"

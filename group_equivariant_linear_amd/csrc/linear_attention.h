@@ -524,9 +524,11 @@ constexpr int kWaves = waves_per_simd(C::ES, C::KB, C::NW);
 // loads waited for at each barrier it took 32 us, 22 with the loads left out and 22 with the
 // arithmetic left out; in flight behind the products, 26.  A chunk is a chain of steps on
 // one tile, so other workgroups have to fill its gaps: at 64 tokens three workgroups' tiles
-// (two buffers, heads of 64) fit the LDS of a CU.  Measured: bf16 heads of 64 in 26 us for 197 tokens on three workgroups a CU; f16
-// heads of 112 (88 KB of LDS, one workgroup a CU) 112 us for 128 tokens on each of 250; fp32
-// heads of 64, 8 us a chunk, 3.4 of them the fp32 matrix instructions' own time.
+// (two buffers, heads of 64) fit the LDS of a CU.  Measured: bf16 heads of 64 in 26 us for 197
+// tokens on three workgroups a CU; f16 heads of 112 (88 KB of LDS, one workgroup a CU) 104 us for
+// 1344 tokens on each of 250; fp32 heads of 64, 8 us a chunk, 3.4 of them the fp32 matrix
+// instructions' own time.  fp16 takes 3 to 5 percent longer than bf16 for the checks of its range;
+// packed training whose every chunk needs scales (gradients of 1e-5) takes 152 us in place of 122.
 template <class C, bool VEC>
 __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
     using IO = typename C::IO;
@@ -701,8 +703,8 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
         const int e0 = (rev && initial_seg && left == n_chunks) ? 0 : 1;
         const bool keep = !OUT || left > 1 || (j.S1 && final_seg && hx % r == 0);  // the state is needed on
 
-        // The chunk's arithmetic, without branches between its products: a whole chunk; part
-        // of one; at most 16 tokens.
+        // The chunk's arithmetic, without branches that ordinary numbers take: a whole chunk;
+        // part of one; at most 16 tokens.
         auto chunk = [&](auto full_c, auto nq_c) {
             constexpr bool FULL = decltype(full_c)::value;
             constexpr int NQ = decltype(nq_c)::value, NM_T = (16 * NQ + O::KS - 1) / O::KS;  // blocks, steps of tokens
@@ -839,7 +841,10 @@ __global__ __launch_bounds__(C::NT, kWaves<C>) void chunk_kernel(Jobs jobs) {
 #pragma unroll
                             for (int e = 0; e < KF; ++e) v[e] = S[(KF * m + e) / 4][e & 3] * norm;
                             O::split(v, st);
-                            if constexpr (ES == 2) {  // an infinity is its first term (the second would be inf - inf)
+                            // An infinity is its first term (the second would be inf - inf).  The branch also
+                            // keeps each step's loads and products together: bf16 packed training takes
+                            // 117 us with it, 127 where the compiler mixes the steps.
+                            if constexpr (ES == 2) {
                                 if (inf_state) [[unlikely]] st[1] = O::finite(st[1]);
                             }
 #pragma unroll

@@ -17,8 +17,10 @@ using namespace mix;
 
 // Segments of long sequences: as many as fill the CUs once (each of the kernel's
 // workgroups per CU counted), of at least four chunks; none where the sequences and heads
-// alone half fill them.  f16, 32768 tokens, 10 heads of 112: 155 us in 25 segments a head
-// (state pass 42, join 11, outputs 112), 170 with twice as many.
+// alone half fill them.  f16, 32768 tokens, 10 heads of 112: 142 us in 25 segments a head
+// (state pass 47, join 11, outputs 104); twice as many took a tenth longer.  Lengths are on
+// the device, so the rule goes by their mean: one sequence far longer than the others is one
+// workgroup's a head.
 struct Split {
     int64_t seg_len = 0, slots = 0;
 };
@@ -120,8 +122,8 @@ namespace {
 // row + rows, ... of the state, and adds them into the outputs of HB query heads that
 // share it; further heads, HB at a time, read the state again.  The state, read and
 // written once, is all the traffic that counts; its loads go out U at a time.  512
-// sequences, 4 kv heads of 128 x 128 (273 MB): 59.5 us, 4.6 TB/s, a copy's rate; 8
-// sequences: 4.9 us of one launch.
+// sequences, 4 kv heads of 128 x 128 (273 MB): 60.0 us, 4.5 TB/s, a copy's rate; 8
+// sequences: 4.8 us of one launch.
 template <typename IO, bool VEC, int HB>
 __global__ __launch_bounds__(256) void step_kernel(MixArgs a, int cols, uint32_t base) {
     constexpr int U = 4, W = VEC ? 4 : 1;  // columns of a thread
