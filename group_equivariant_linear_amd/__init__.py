@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_PKG, "libeqlinear.so")
 
 EQL_OK, EQL_ERR_INVALID, EQL_ERR_UNSUPPORTED, EQL_ERR_HIP, EQL_ERR_NOMEM = range(5)
 EQL_F32, EQL_BF16, EQL_F16 = 0, 1, 2
-EQL_KIND_CN, EQL_KIND_D8, EQL_KIND_ROTARY, EQL_KIND_MIXER, EQL_KIND_NORM = range(5)
+EQL_KIND_CN, EQL_KIND_D8, EQL_KIND_ROTARY, EQL_KIND_MIXER, EQL_KIND_NORM, EQL_KIND_ATTENTION = range(6)
 EQL_ACT_NONE, EQL_ACT_GELU, EQL_ACT_SILU = range(3)
 EQL_ROTARY_HALF, EQL_ROTARY_INTERLEAVED = 0, 1
 EQL_ROTARY_PLAIN, EQL_ROTARY_LINEAR, EQL_ROTARY_RAISED_BASE, EQL_ROTARY_BANDED = range(4)
@@ -40,6 +40,9 @@ ABI_FUNCTIONS = (
     "eqlinear_rotary_plan", "eqlinear_rotary", "eqlinear_mixer_plan", "eqlinear_linear_attention_workspace",
     "eqlinear_linear_attention", "eqlinear_linear_attention_backward", "eqlinear_linear_attention_step",
     "eqlinear_norm_plan", "eqlinear_group_norm_workspace", "eqlinear_group_norm", "eqlinear_group_norm_backward",
+    "eqlinear_attention_plan", "eqlinear_attention_bucket", "eqlinear_attention_workspace", "eqlinear_attention",
+    "eqlinear_attention_backward", "eqlinear_attention_step_workspace", "eqlinear_attention_step",
+    "eqlinear_cache_tables_workspace", "eqlinear_cache_tables", "eqlinear_cache_store",
 )
 
 # Size of the library-held scratch array of eqlinear_backward_weight_noalloc.
@@ -72,6 +75,13 @@ class eqlinear_heads(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class eqlinear_pages(ctypes.Structure):
+    """A cache [blocks][block_size][kv_heads][d][N] with the last two axes contiguous; strides in elements."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -89,6 +99,7 @@ def load_library(path: str | None = None):
         vp, i32, i64, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int
         plan_p = ctypes.POINTER(ctypes.c_void_p)
         hp, f32, f64 = ctypes.POINTER(eqlinear_heads), ctypes.c_float, ctypes.c_double
+        pp, size = ctypes.POINTER(eqlinear_pages), ctypes.c_size_t
         sig = {
             "eqlinear_status_string": ([st], ctypes.c_char_p),
             "eqlinear_plan": ([plan_p, i32, i32, i32, i32], st),
@@ -127,6 +138,17 @@ def load_library(path: str | None = None):
             "eqlinear_group_norm": ([vp, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, ctypes.c_size_t, vp], st),
             "eqlinear_group_norm_backward": ([vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp,
                                               ctypes.c_size_t, vp], st),
+            "eqlinear_attention_plan": ([plan_p] + [i32] * 9, st),
+            "eqlinear_attention_bucket": ([vp, i64], i32),
+            "eqlinear_attention_workspace": ([vp, i64, i64, i64, i32], size),
+            "eqlinear_attention": ([vp, hp, hp, hp, f32, vp, vp, vp, i64, hp, vp, i64, i64, vp, size, vp], st),
+            "eqlinear_attention_backward": ([vp, hp, hp, hp, hp, hp, vp, f32, vp, vp, vp, i64, hp, hp, hp, vp, i64, i64,
+                                             vp, size, vp], st),
+            "eqlinear_attention_step_workspace": ([vp, i64], size),
+            "eqlinear_attention_step": ([vp, hp, pp, pp, i64, i32, vp, i64, vp, f32, vp, hp, vp, i64, vp, size, vp], st),
+            "eqlinear_cache_tables_workspace": ([i64], size),
+            "eqlinear_cache_tables": ([vp, vp, vp, i64, vp, vp, i64, i32, vp, vp, vp, vp, vp, i64, i64, vp, size, vp], st),
+            "eqlinear_cache_store": ([vp, hp, hp, vp, pp, pp, i64, i32, i64, vp], st),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -697,6 +719,176 @@ def eqlinear_group_norm_backward(plan: Plan, dy, x, gamma, beta, stats, dx, dgam
         _dense(beta, "beta", dt, (C,)), _dense(stats, "stats", torch.float32, (B, plan.groups, 2)), off, B,
         *_tokens_of(dx, plan, T, "dx"), _dense(dgamma, "dgamma", torch.float32, (C,)),
         _dense(dbeta, "dbeta", torch.float32, (C,)), T, ws, nb, _raw_stream(stream)), "eqlinear_group_norm_backward")
+
+
+# --- softmax attention and its paged cache -------------------------------------------
+
+def eqlinear_attention_plan(N: int, heads: int, kv_heads: int, d_k: int, d_v: int, dtype: int, causal: bool = False,
+                            buckets: int = 0, max_distance: int = 0) -> Plan:
+    """Plan of softmax attention: heads of d_k (queries, keys) and d_v (values) channels; with buckets > 0 its calls
+    may take a bias for every head and bucket of distances."""
+    lib = load_library()
+    h = ctypes.c_void_p()
+    _check(lib.eqlinear_attention_plan(ctypes.byref(h), N, heads, kv_heads, d_k, d_v, int(bool(causal)), buckets,
+                                       max_distance, int(dtype)), "eqlinear_attention_plan")
+    p = Plan(h.value, lib)
+    p.heads, p.kv_heads, p.d_k, p.d_v, p.buckets = heads, kv_heads, d_k, d_v, buckets
+    return p
+
+
+def eqlinear_attention_bucket(plan: Plan, distance: int) -> int:
+    """Bucket of a distance (query's position less key's); -1: none."""
+    return int(plan._lib.eqlinear_attention_bucket(plan.handle, int(distance)))
+
+
+def eqlinear_attention_workspace(plan: Plan, T: int, T_kv: int, batch: int, backward: bool = False) -> int:
+    return int(plan._lib.eqlinear_attention_workspace(plan.handle, int(T), int(T_kv), int(batch), int(bool(backward))))
+
+
+def _two_sequences(offsets, kv_offsets, batch, T, T_kv):
+    """(address of offsets, of kv_offsets, number of sequences); keys without offsets of their own share the queries'."""
+    off, B = _sequences(offsets, batch)
+    if kv_offsets is not None:
+        kv, n = _sequences(kv_offsets, B if isinstance(kv_offsets, int) else None)
+        if n != B and (offsets is not None or batch is not None):
+            raise ValueError(f"kv_offsets: expected batch + 1 = {B + 1} values, got {n + 1}")
+        return off, kv, n
+    if off is not None and T != T_kv:
+        raise ValueError("kv_offsets is required where k and v have other tokens than q")
+    return off, off, B
+
+
+def eqlinear_attention(plan: Plan, q, k, v, o, scale: float, bias=None, lse=None, offsets=None, kv_offsets=None,
+                       batch: int | None = None, workspace=None, T: int | None = None, T_kv: int | None = None,
+                       stream=None):
+    """Softmax attention: o [T, heads, d_v, N] of q [T, heads, d_k, N] over k [T_kv, kv_heads, d_k, N] and
+    v [T_kv, kv_heads, d_v, N]; bias [heads, buckets]; lse fp32 [heads, T] out (or None).  The sequences are offsets
+    (int64 [batch + 1]; kv_offsets those of k and v, default: the same) or batch equal runs (default: one)."""
+    torch = _torch()
+    _kind(plan, EQL_KIND_ATTENTION, "eqlinear_attention")
+    T, S = _count(q, T, "q"), _count(k, T_kv, "k")
+    H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    off, kv_off, B = _two_sequences(offsets, kv_offsets, batch, T, S)
+    ws, nb = _workspace(workspace)
+    _check(plan._lib.eqlinear_attention(
+        plan.handle, _heads(q, plan, T, H, dk, "q"), _heads(k, plan, S, K, dk, "k"), _heads(v, plan, S, K, dv, "v"),
+        scale, _dense(bias, "bias", plan.torch_dtype, (H, plan.buckets)), off, kv_off, B,
+        _heads(o, plan, T, H, dv, "o"), _dense(lse, "lse", torch.float32, (H, T)), T, S, ws, nb, _raw_stream(stream)),
+        "eqlinear_attention")
+
+
+def eqlinear_attention_backward(plan: Plan, q, k, v, o, do, lse, dq, dk, dv, scale: float, bias=None, dbias=None,
+                                offsets=None, kv_offsets=None, batch: int | None = None, workspace=None,
+                                T: int | None = None, T_kv: int | None = None, stream=None):
+    """Gradients dq, dk, dv (and dbias, fp32 [heads, buckets]) of eqlinear_attention from its o and lse."""
+    torch = _torch()
+    _kind(plan, EQL_KIND_ATTENTION, "eqlinear_attention_backward")
+    T, S = _count(q, T, "q"), _count(k, T_kv, "k")
+    H, K, ck, cv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    off, kv_off, B = _two_sequences(offsets, kv_offsets, batch, T, S)
+    ws, nb = _workspace(workspace)
+    _check(plan._lib.eqlinear_attention_backward(
+        plan.handle, _heads(q, plan, T, H, ck, "q"), _heads(k, plan, S, K, ck, "k"), _heads(v, plan, S, K, cv, "v"),
+        _heads(o, plan, T, H, cv, "o"), _heads(do, plan, T, H, cv, "do"), _dense(lse, "lse", torch.float32, (H, T)),
+        scale, _dense(bias, "bias", plan.torch_dtype, (H, plan.buckets)), off, kv_off, B,
+        _heads(dq, plan, T, H, ck, "dq"), _heads(dk, plan, S, K, ck, "dk"), _heads(dv, plan, S, K, cv, "dv"),
+        _dense(dbias, "dbias", torch.float32, (H, plan.buckets)), T, S, ws, nb, _raw_stream(stream)),
+        "eqlinear_attention_backward")
+
+
+def _pages(t, plan: Plan, d: int, blocks: int, block_size: int, name: str):
+    """A cache [blocks, block_size, kv_heads, d, N] (the last two axes contiguous), the address of a contiguous one, or
+    an eqlinear_pages as it is."""
+    if type(t) is eqlinear_pages:
+        return t
+    K, N = plan.kv_heads, plan.N
+    if type(t) is int:
+        return eqlinear_pages(t, block_size * K * d * N, K * d * N, d * N)
+    _gpu(t, name, plan.torch_dtype)
+    if t.shape != (blocks, block_size, K, d, N):
+        raise ValueError(f"{name}: expected shape {(blocks, block_size, K, d, N)}, got {tuple(t.shape)}")
+    bs, ts, hs, sd, sn = t.stride()
+    if (sn != 1 and N > 1) or (sd != N and d > 1):
+        raise ValueError(f"{name}: the channel and group axes must be contiguous")
+    return eqlinear_pages(t.data_ptr(), bs, ts, hs)
+
+
+def _cache_shape(k_cache, blocks, block_size):
+    """(blocks, block_size) of a cache: a tensor's own, or as given with an address."""
+    if isinstance(k_cache, (int, eqlinear_pages)):
+        if blocks is None or block_size is None:
+            raise ValueError("blocks and block_size are required when k_cache is an address")
+        return int(blocks), int(block_size)
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def eqlinear_attention_step_workspace(plan: Plan, batch: int) -> int:
+    return int(plan._lib.eqlinear_attention_step_workspace(plan.handle, int(batch)))
+
+
+def eqlinear_attention_step(plan: Plan, q, k_cache, v_cache, table, lengths, o, scale: float, bias=None, lse=None,
+                            batch: int | None = None, blocks: int | None = None, block_size: int | None = None,
+                            max_blocks: int | None = None, workspace=None, stream=None):
+    """Attention of one new token for each of batch sequences: q [batch, heads, d_k, N] over the keys and values of
+    k_cache [blocks, block_size, kv_heads, d_k, N] and v_cache that table (int32 [batch, max_blocks]) names, the first
+    lengths[b] (int32) of them; o [batch, heads, d_v, N], lse fp32 [heads, batch] (or None)."""
+    torch = _torch()
+    _kind(plan, EQL_KIND_ATTENTION, "eqlinear_attention_step")
+    B = _count(q, batch, "q")
+    H, K, dk, dv = plan.heads, plan.kv_heads, plan.d_k, plan.d_v
+    nb, bs = _cache_shape(k_cache, blocks, block_size)
+    if max_blocks is None:
+        if isinstance(table, int):
+            raise ValueError("max_blocks is required when table is an address")
+        max_blocks = table.shape[1]
+    ws, n = _workspace(workspace)
+    _check(plan._lib.eqlinear_attention_step(
+        plan.handle, _heads(q, plan, B, H, dk, "q"), _pages(k_cache, plan, dk, nb, bs, "k_cache"),
+        _pages(v_cache, plan, dv, nb, bs, "v_cache"), nb, bs, _dense(table, "table", torch.int32, (B, max_blocks)),
+        max_blocks, _dense(lengths, "lengths", torch.int32, (B,)), scale,
+        _dense(bias, "bias", plan.torch_dtype, (H, plan.buckets)), _heads(o, plan, B, H, dv, "o"),
+        _dense(lse, "lse", torch.float32, (H, B)), B, ws, n, _raw_stream(stream)), "eqlinear_attention_step")
+
+
+def eqlinear_cache_tables_workspace(batch: int) -> int:
+    return int(load_library().eqlinear_cache_tables_workspace(int(batch)))
+
+
+def eqlinear_cache_tables(lengths, added, free_blocks, cursor, table, block_size: int, lengths_out, cursor_out, slots,
+                          positions, offsets, workspace, stream=None):
+    """Tables of a paged cache for the next step: requests of lengths (int32 [batch]) tokens get added more, whose
+    blocks come from free_blocks (int32) at cursor (int32 [1]) on; out: the new blocks in table (int32 [batch,
+    max_blocks]), lengths_out, cursor_out, and for the packed new tokens slots (int64 [T]), positions (int32 [T]) and
+    offsets (int64 [batch + 1]).  lengths_out may be lengths and cursor_out cursor."""
+    torch = _torch()
+    for t in (lengths, added, free_blocks, cursor, table, lengths_out, cursor_out, slots, positions, offsets):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("eqlinear_cache_tables: expected torch tensors (their sizes are checked)")
+    i32, B, T = torch.int32, lengths.numel(), slots.numel()
+    ws, nb = _workspace(workspace)
+    max_blocks = table.shape[-1]
+    _check(load_library().eqlinear_cache_tables(
+        _dense(lengths, "lengths", i32, (B,)), _dense(added, "added", i32, (B,)),
+        _dense(free_blocks, "free_blocks", i32, (free_blocks.numel(),)), free_blocks.numel(),
+        _dense(cursor, "cursor", i32, (1,)), _dense(table, "table", i32, (B, max_blocks)), max_blocks, int(block_size),
+        _dense(lengths_out, "lengths_out", i32, (B,)), _dense(cursor_out, "cursor_out", i32, (1,)),
+        _dense(slots, "slots", torch.int64, (T,)), _dense(positions, "positions", i32, (T,)),
+        _dense(offsets, "offsets", torch.int64, (B + 1,)), B, T, ws, nb, _raw_stream(stream)), "eqlinear_cache_tables")
+
+
+def eqlinear_cache_store(plan: Plan, k, v, slots, k_cache, v_cache, T: int | None = None, blocks: int | None = None,
+                         block_size: int | None = None, stream=None):
+    """Rows of k [T, kv_heads, d_k, N] and v [T, kv_heads, d_v, N] to slots (int64 [T]) of k_cache [blocks, block_size,
+    kv_heads, d_k, N] and v_cache; slots that the cache does not have are skipped."""
+    torch = _torch()
+    _kind(plan, EQL_KIND_ATTENTION, "eqlinear_cache_store")
+    T = _count(k, T, "k")
+    K, dk, dv = plan.kv_heads, plan.d_k, plan.d_v
+    nb, bs = _cache_shape(k_cache, blocks, block_size)
+    _check(plan._lib.eqlinear_cache_store(
+        plan.handle, _heads(k, plan, T, K, dk, "k"), _heads(v, plan, T, K, dv, "v"),
+        _dense(slots, "slots", torch.int64, (T,)), _pages(k_cache, plan, dk, nb, bs, "k_cache"),
+        _pages(v_cache, plan, dv, nb, bs, "v_cache"), nb, bs, T, _raw_stream(stream)), "eqlinear_cache_store")
 
 
 def built() -> bool:

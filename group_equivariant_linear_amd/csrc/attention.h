@@ -1,0 +1,827 @@
+// attention.h -- softmax attention on matrix cores: forward, and the gradients from
+// recomputed probabilities.
+//
+//   s_ij = scale q_i . k_j + bias[bucket(p_i - j)],  p_i = i + n_k - n_q
+//   P = softmax over the keys that query i sees,  o_i = sum_j P_ij v_j
+//   dP = d_o v^T,  dS = P (dP - delta),  delta_i = d_o_i . o_i
+//   dq = scale dS k,  dk = scale dS^T q,  dv = P^T d_o,  dbias[b] = sum of dS over bucket b
+//
+// One wave owns 32 rows (queries, or keys for dk and dv) as columns of its accumulators:
+// its scores come as S^T = K Q^T in blocks of 32 x 32, a lane holding 16 numbers of one of
+// its rows (lane % 32).  Statistics of a row are then a lane's own (and its partner's, lane
+// ^ 32), and the block, packed to the plan's type, is at once the operand of the next
+// product: the contraction runs over the numbers in the order in which the lane holds
+// them, and the other operand is read from its row-major tile in that order.
+#pragma once
+
+#include "tiles.h"
+
+namespace eql {
+namespace att {
+
+using namespace tile;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128;  // rows that a workgroup's four waves own
+constexpr int kTile = 64;   // rows of the tiles that they pass over
+constexpr int kPad = 96;    // a wave's rows and a tile span fewer distances than this
+constexpr float kInf = __builtin_inff();
+
+template <typename IO>
+struct Op32 : Op<IO> {  // __bf16, _Float16
+    using F = typename Half<IO>::x8;
+    static __device__ __forceinline__ void mma(f32x16& acc, const F& a, const F& b) {
+        if constexpr (Op<IO>::BF) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+        else acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc, 0, 0, 0);
+    }
+    static __device__ __forceinline__ F pack(const float* p) {
+        u32x4 u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = Half<IO>::pack2(p[2 * i], p[2 * i + 1]);
+        return __builtin_bit_cast(F, u);
+    }
+};
+template <>
+struct Op32<float> : Op<float> {
+    using F = f32x4;
+    static __device__ __forceinline__ void mma(f32x16& acc, const F& a, const F& b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], acc, 0, 0, 0);
+    }
+    static __device__ __forceinline__ F pack(const float* p) { return F{p[0], p[1], p[2], p[3]}; }
+};
+
+// Shapes for heads of up to 32 DB numbers.  Lane l: row (column) l % 32, half h = l / 32.
+// A step along a row takes two pieces of 16 bytes, one of each half; a step along the
+// columns of a tile (over its rows) 2 E rows, which are those of accumulators E t .. E t +
+// E - 1 of both halves: row 8 (i / 4) + 4 h + i % 4 of a block belongs to accumulator i.
+template <typename IO, int DB_>
+struct Shape {
+    static constexpr int ES = (int)sizeof(IO), E = 16 / ES, DB = DB_, D = 32 * DB_;
+    static constexpr int P = D / E, NS = P / 2, NT = 16 / E;
+    static constexpr int TILE = kTile * P * 16;
+};
+__device__ __forceinline__ constexpr int row_of(int i) { return 8 * (i >> 2) + (i & 3); }  // + 4 h
+
+// Fragments along the rows of a tile: block of 32 rows, step s.
+template <class C>
+struct RowFrags {
+    static constexpr int R = C::P % 16 == 0 ? 8 : (C::P % 8 == 0 ? 4 : 2), N = R < C::NS ? R : C::NS;
+    const char* base[N];
+    __device__ __forceinline__ explicit RowFrags(const char* t) {
+        const int lane = (int)threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) base[i] = t + place<C::ES, C::P>(lane & 31, 2 * i + (lane >> 5));
+    }
+    template <typename F>
+    __device__ __forceinline__ F get(int by, int block, int s) const {
+        return *reinterpret_cast<const F*>(base[s % N] + by + block * (32 * C::P * 16) + s / N * (N * 32));
+    }
+};
+
+// Fragments along its columns: columns 32 cb .. of rows 32 block + 2 E t ..
+template <class C, typename O>
+struct ColumnFrags {
+    static constexpr int R = C::P % 16 == 0 ? 4 : (C::P % 8 == 0 ? 2 : 1), N = R < C::DB ? R : C::DB;
+    const char* base[2][N];
+    const char* tile;
+    __device__ __forceinline__ explicit ColumnFrags(const char* t) : tile(t) {
+        if constexpr (C::ES == 2) {
+            const int lane = (int)threadIdx.x & 63, u = lane & 3, r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int piece = 4 * k + 2 * ((lane >> 4) & 1) + (u >> 1);
+                base[0][k] = t + place<C::ES, C::P>(r, piece) + (u & 1) * 8;
+                base[1][k] = t + place<C::ES, C::P>(r + 8, piece) + (u & 1) * 8;
+            }
+        }
+    }
+    __device__ __forceinline__ typename O::F get(int by, int block, int t, int cb) const {
+        if constexpr (C::ES == 2) {
+            const int off = by + cb / N * (N * 64) + (32 * block + 16 * t) * (C::P * 16);
+            return O::column(base[0][cb % N] + off, base[1][cb % N] + off);
+        } else {
+            const int lane = (int)threadIdx.x & 63, h = lane >> 5, ln = lane & 31;
+            typename O::F f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = *reinterpret_cast<const float*>(
+                    tile + by + place<C::ES, C::P>(32 * block + 8 * t + 4 * h + e, 8 * cb + (ln >> 2)) + (ln & 3) * 4);
+            return f;
+        }
+    }
+};
+
+// Number (row, d) of a tile.
+template <class C, typename IO>
+__device__ __forceinline__ float element(const char* tile, int row, int d) {
+    return (float)*reinterpret_cast<const IO*>(tile + place<C::ES, C::P>(row, d / C::E) + d % C::E * C::ES);
+}
+
+// What the products with finite operands left out: acc[d] += p_row x[row][d] for the
+// infinities and NaN of a tile of 64 rows, for those rows lo .. hi that the lane's own
+// row sees (and those alone: their p of 0 is no probability).
+template <class C, typename IO, int NB>
+__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, const f32x16 (&p)[NB], int lo, int hi) {
+    const int lane = (int)threadIdx.x & 63, h = lane >> 5;
+    for (int row = 0; row < 32 * NB; ++row) {
+        bool odd = false;
+        for (int d = lane; d < C::D; d += 64) odd |= !(fabsf(element<C, IO>(tile, row, d)) < kInf);
+        if (!__any(odd)) continue;
+        const int at = (row >> 5) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
+        float mine = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mine = at == 16 * b + i ? p[b][i] : mine;
+        const float other = __shfl_xor(mine, 32);
+        const float w = h == ((row >> 2) & 1) ? mine : other;
+        if (row < lo || row > hi) continue;
+#pragma unroll
+        for (int cb = 0; cb < C::DB; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = element<C, IO>(tile, row, 32 * cb + row_of(i) + 4 * h);
+                if (!(fabsf(x) < kInf)) acc[cb][i] += w * x;
+            }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void clear(f32x16 (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = f32x16{};
+}
+
+// Rows of one sequence.
+struct Seq {
+    int64_t q0, k0;  // first tokens
+    int n_q, n_k;
+};
+
+__device__ __forceinline__ int64_t clamped(const int64_t* offsets, int64_t b, int64_t T) {
+    const int64_t o = offsets[b];
+    return o < 0 ? 0 : (o > T ? T : o);
+}
+__device__ __forceinline__ void tokens_of(const int64_t* offsets, int64_t batch, int64_t T, int64_t b, int64_t& t0, int& n) {
+    if (offsets) {
+        const int64_t e = clamped(offsets, b + 1, T);
+        t0 = clamped(offsets, b, T);
+        n = e > t0 ? (int)(e - t0) : 0;
+    } else {
+        n = (int)(T / batch);
+        t0 = b * n;
+    }
+}
+
+// Slot `slot` of runs of kRows tokens: its sequence and first row.  Packed sequence b owns
+// the slots from offsets[b] / kRows + b on, at least as many as it has runs.
+__device__ __forceinline__ void slot_of(const int64_t* offsets, int64_t batch, int64_t T, uint32_t slot, int64_t& b, int64_t& row) {
+    if (!offsets) {
+        const int64_t n = T / batch;
+        const uint32_t per = (uint32_t)((n + kRows - 1) / kRows);
+        b = slot / per;
+        row = (int64_t)(slot - (uint32_t)b * per) * kRows;
+        return;
+    }
+    int64_t lo = 0, hi = batch - 1;  // last b whose first slot is at most `slot`
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo + 1) / 2;
+        if (clamped(offsets, mid, T) / kRows + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo;
+    row = ((int64_t)slot - clamped(offsets, lo, T) / kRows - lo) * kRows;
+}
+
+// Biases (times log2 e) of the distances -(reach + kPad) .. reach + kPad, at distance +
+// reach + kPad of `tab`.
+template <typename IO>
+__device__ __forceinline__ float bias_of(const AttentionArgs& a, const BucketMap& map, int head, int distance) {
+    const int n = distance < 0 ? -distance : distance;
+    const int b = map.of[n < a.reach ? n : a.reach] + (distance < 0 && !a.causal ? a.buckets / 2 : 0);
+    return (float)((const IO*)a.bias)[(int64_t)head * a.buckets + b];
+}
+template <typename IO>
+__device__ __forceinline__ void fill_biases(float* tab, const AttentionArgs& a, const BucketMap& map, int head) {
+    const int off = a.reach + kPad;
+    for (int x = (int)threadIdx.x; x <= 2 * off; x += 256) tab[x] = kLog2e * bias_of<IO>(a, map, head, x - off);
+}
+constexpr int kTab = 2 * (kMaxReach + kPad) + 1;
+
+// Fragments of 32 rows from memory, the operand of the products over the head's numbers.
+template <class C, typename IO, typename F, bool VEC>
+__device__ __forceinline__ void load_rows(F (&f)[C::NS], const Heads& x, int64_t t, int64_t head, int n, int D) {
+    const int lane = (int)threadIdx.x & 63, row = lane & 31, h = lane >> 5;
+    const IO* base = (const IO*)x.p + t * x.ts + head * x.hs;
+    if constexpr (VEC) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, n > 0 ? (uint32_t)(((int64_t)((n < 32 ? n : 32) - 1) * x.ts + D) * C::ES) : 0u);
+#pragma unroll
+        for (int s = 0; s < C::NS; ++s) {
+            const int col = (2 * s + h) * C::E;
+            const uint32_t off = col < D && row < n ? (uint32_t)(row * (int)x.ts + col) * C::ES : kOOB;
+            f[s] = __builtin_bit_cast(F, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < C::NS; ++s) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (row < n) v = load_piece<IO>(base + row * x.ts, (2 * s + h) * C::E, D);
+            f[s] = __builtin_bit_cast(F, v);
+        }
+    }
+}
+
+// Accumulators of 32 rows to memory, times m, rounded once.
+template <class C, typename IO>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[C::DB], const Heads& x, int64_t t, int64_t head, int n, int D,
+                                           float m, int vec) {
+    const int lane = (int)threadIdx.x & 63, row = lane & 31, h = lane >> 5;
+    if (row >= n) return;
+    IO* const p = (IO*)const_cast<void*>(x.p) + (t + row) * x.ts + head * x.hs;
+#pragma unroll
+    for (int cb = 0; cb < C::DB; ++cb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int d = 32 * cb + 8 * g + 4 * h;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = m * acc[cb][4 * g + e];
+            if (vec) {
+                if (d < D) {
+                    if constexpr (C::ES == 2)
+                        *reinterpret_cast<u32x2*>(p + d) = u32x2{Half<IO>::pack2(v[0], v[1]), Half<IO>::pack2(v[2], v[3])};
+                    else *reinterpret_cast<f32x4*>(p + d) = f32x4{v[0], v[1], v[2], v[3]};
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (d + e < D) p[d + e] = (IO)v[e];
+            }
+        }
+}
+
+// The power of two by which a lane's sums of dS times rows are held: fp16 takes dS only near
+// the middle of its range.  Starts high and comes down, like a running maximum.
+constexpr float kTopScale = 18446744073709551616.0f;  // 2^64
+
+// fp16: probabilities are held times 2^12 (at most 2^15, see kSlack), so that one of 2^-36 of
+// the largest still counts.
+template <typename IO>
+constexpr float kShift = std::is_same_v<IO, _Float16> ? 12.0f : 0.0f;
+// How far (in powers of two) a score may pass the running maximum before the sums are scaled
+// to a new one.
+template <typename IO>
+constexpr float kSlack = std::is_same_v<IO, _Float16> ? 3.0f : 8.0f;
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// --- forward --------------------------------------------------------------------------
+template <typename IO, int DB, bool VEC, bool BIAS>
+__global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+    using C = Shape<IO, DB>;
+    using O = Op32<IO>;
+    using F = typename O::F;
+    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
+    __shared__ float tab[BIAS ? kTab : 1];
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
+    const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    int64_t b, row0;
+    slot_of(a.offsets, a.batch, a.T, id % a.slots, b, row0);
+    Seq s;
+    tokens_of(a.offsets, a.batch, a.T, b, s.q0, s.n_q);
+    tokens_of(a.kv_offsets, a.batch, a.T_kv, b, s.k0, s.n_k);
+    if (row0 < 0 || row0 >= s.n_q) return;
+    const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
+    const int my = w0 + (lane & 31);
+    if constexpr (BIAS) fill_biases<IO>(tab, a, map, head);
+
+    F q[C::NS];
+    load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
+    f32x16 acc[DB];
+    clear(acc);
+    float top = -kInf, total = 0.0f;
+    const float scale = a.scale * kLog2e;
+    const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;  // last key that it sees
+    const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
+    const int wave_all = a.causal && w0 + shift < s.n_k - 1 ? w0 + shift : s.n_k - 1;          // all its rows see
+    const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
+
+    constexpr int NP = (C::P + 3) / 4;
+    const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
+    char *const tk = lds, *const tv = lds + C::TILE;
+    const RowFrags<C> rows(tk);
+    const ColumnFrags<C, O> cols(tv);
+    for (int j0 = 0; j0 < end; j0 += kTile) {
+        __syncthreads();
+        const int n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, tk);
+        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, tv);
+        wait_loads();
+        __syncthreads();
+        if (n_rows <= 0 || j0 >= wave_end) continue;
+        const bool edge = j0 + kTile - 1 > wave_all;
+        f32x16 x[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            x[kb] = f32x16{};
+#pragma unroll
+            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], rows.template get<F>(0, kb, st), q[st]);
+        }
+        if constexpr (BIAS) {
+            const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
+            const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
+            const float* t = tab + a.reach + kPad;
+            const float f = t[from > 0 ? a.reach : -a.reach];
+            t += from + (lane & 31) - 4 * h;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[kb][i] = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
+        } else {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) x[kb] *= scale;
+        }
+        if (edge) {
+            const int lim = last - j0 - 4 * h;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[kb][i] = 32 * kb + row_of(i) <= lim ? x[kb][i] : -kInf;
+        }
+        float mx = -kInf;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[kb][i]);
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (__any(mx > top + kSlack<IO>)) {
+            // (a row without scores so far has sums of 0, and none of its terms is counted against -infinity)
+            const float now = mx > top + kSlack<IO> ? mx : top;
+            const float c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+            top = now;
+            total *= c;
+#pragma unroll
+            for (int cb = 0; cb < DB; ++cb) acc[cb] *= c;
+        }
+        const float m = (top == -kInf ? 0.0f : top) - kShift<IO>;
+        float sum = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[kb][i] = __builtin_amdgcn_exp2f(x[kb][i] - m);
+                sum += x[kb][i];
+            }
+        total += sum;
+        uint32_t odd = 0;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int t = 0; t < C::NT; ++t) {
+                float w[C::E];
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) w[e] = x[kb][t * C::E + e];
+                const F p = O::pack(w);
+#pragma unroll
+                for (int cb = 0; cb < DB; ++cb) {
+                    F v[1] = {cols.get(0, kb, t, cb)};
+                    if (edge) {
+                        const uint32_t o = O::top(v);
+                        odd = o > odd ? o : odd;
+                        v[0] = O::finite(v[0]);
+                    }
+                    O::mma(acc[cb], v[0], p);
+                }
+            }
+        if (edge && __any(odd >= O::kInf)) add_odd_numbers<C, IO, 2>(acc, tv, x, 0, last - j0);
+    }
+    if (n_rows <= 0) return;
+    total += __shfl_xor(total, 32);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    store_rows<C, IO>(acc, a.o, s.q0 + w0, head, n_rows, a.D_v, inv, a.out_vec);
+    if (a.lse && h == 0 && (lane & 31) < n_rows)
+        a.lse[(int64_t)head * a.T + s.q0 + my] =
+            total == 0.0f ? -kInf : ((top == -kInf ? 0.0f : top) - kShift<IO> + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+
+// --- backward -------------------------------------------------------------------------
+// Per query and head, for the kernels below: lse in powers of two (+infinity for a row
+// that sees nothing, which makes its probabilities 0) and delta = d_o . o.  16 lanes a row.
+template <typename IO>
+__global__ __launch_bounds__(256) void row_kernel(AttentionArgs a, uint32_t base) {
+    const int tid = (int)threadIdx.x, l = tid & 15;
+    const int64_t row = ((int64_t)blockIdx.x + base) * 16 + (tid >> 4), n = a.T * a.heads;
+    if (row >= n) return;
+    const int64_t head = row / a.T, t = row - head * a.T;
+    const IO* o = (const IO*)a.o.p + t * a.o.ts + head * a.o.hs;
+    const IO* g = (const IO*)a.d_o.p + t * a.d_o.ts + head * a.d_o.hs;
+    float d = 0.0f;
+    for (int e = l; e < a.D_v; e += 16) d = __builtin_fmaf((float)o[e], (float)g[e], d);
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) d += __shfl_xor(d, m);
+    if (l == 0) {
+        const float s = a.lse[row];
+        a.row_lse[row] = s == -kInf ? kInf : s * kLog2e;
+        a.row_delta[row] = d;
+    }
+}
+
+// fp16: takes the lane's sums to a scale that holds its numbers x, and returns x's.
+template <typename IO, int N, int DB>
+__device__ __forceinline__ float hold(const f32x16 (&x)[N], float& f, f32x16 (&acc)[DB]) {
+    if constexpr (!std::is_same_v<IO, _Float16>) return 1.0f;
+    float m = 0.0f;
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[b][i]));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const bool over = m * f > 32768.0f && m < kInf;
+    if (__any(over)) {
+        const float now = over ? range_scale(m) : f;
+        const float c = now * inverse_of_power(f);
+        f = now;
+#pragma unroll
+        for (int cb = 0; cb < DB; ++cb) acc[cb] *= c;
+    }
+    return f;
+}
+
+// Gradients of q and, if wanted, of the biases: a wave owns 32 queries and passes over the
+// keys.  Of the biases, dS is summed by distance, each wave's halves in an array of their
+// own (the lanes of an instruction hold 32 distances apiece, all different, and a wave's
+// instructions come in order: the sums do not depend on timing); distances past the reach
+// share a bucket on either side and are summed in registers.  A workgroup writes the sums
+// of its buckets; reduce_kernel joins those of a head.
+template <typename IO, int DB, bool VEC, bool BIAS>
+__global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+    using C = Shape<IO, DB>;
+    using O = Op32<IO>;
+    using F = typename O::F;
+    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
+    __shared__ float tab[BIAS ? kTab : 1];
+    __shared__ float far_sums[BIAS ? 8 : 1];
+    extern __shared__ float sums[];  // [8][2 (reach + kPad) + 1] with gradients of the biases
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
+    const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
+    const uint32_t slot = id % a.slots;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    int64_t b, row0;
+    slot_of(a.offsets, a.batch, a.T, slot, b, row0);
+    Seq s;
+    tokens_of(a.offsets, a.batch, a.T, b, s.q0, s.n_q);
+    tokens_of(a.kv_offsets, a.batch, a.T_kv, b, s.k0, s.n_k);
+    const bool idle = row0 < 0 || row0 >= s.n_q;
+    if (idle && !(BIAS && a.dbias)) return;
+    if (idle) s.n_q = s.n_k = 0, row0 = 0;
+    const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
+    const int my = w0 + (lane & 31);
+    const int width = 2 * (a.reach + kPad) + 1;
+    if constexpr (BIAS) {
+        fill_biases<IO>(tab, a, map, head);
+        if (a.dbias)
+            for (int x = tid; x < 8 * width; x += 256) sums[x] = 0.0f;
+    }
+
+    F q[C::NS], d_o[C::NS];
+    load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
+    load_rows<C, IO, F, VEC>(d_o, a.d_o, s.q0 + w0, head, n_rows, a.D_v);
+    const bool real = (lane & 31) < n_rows;
+    const float lse = real ? a.row_lse[(int64_t)head * a.T + s.q0 + my] : kInf;
+    const float delta = real ? a.row_delta[(int64_t)head * a.T + s.q0 + my] : 0.0f;
+    f32x16 acc[DB];
+    clear(acc);
+    float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
+    const float scale = a.scale * kLog2e;
+    const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
+    const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
+    const int wave_all = a.causal && w0 + shift < s.n_k - 1 ? w0 + shift : s.n_k - 1;
+    const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
+
+    constexpr int NP = (C::P + 3) / 4;
+    const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
+    char *const tk = lds, *const tv = lds + C::TILE;
+    const RowFrags<C> krows(tk), vrows(tv);
+    const ColumnFrags<C, O> kcols(tk);
+    for (int j0 = 0; j0 < end; j0 += kTile) {
+        __syncthreads();
+        const int n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, tk);
+        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, tv);
+        wait_loads();
+        __syncthreads();
+        if (n_rows <= 0 || j0 >= wave_end) continue;
+        const bool edge = j0 + kTile - 1 > wave_all;
+        f32x16 x[2], dp[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            x[kb] = f32x16{}, dp[kb] = f32x16{};
+#pragma unroll
+            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], krows.template get<F>(0, kb, st), q[st]);
+#pragma unroll
+            for (int st = 0; st < C::NS; ++st) O::mma(dp[kb], vrows.template get<F>(0, kb, st), d_o[st]);
+        }
+        const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
+        const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
+        if constexpr (BIAS) {
+            const float* t = tab + a.reach + kPad;
+            const float f = t[from > 0 ? a.reach : -a.reach];
+            t += from + (lane & 31) - 4 * h;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[kb][i] = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
+        } else {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) x[kb] *= scale;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = __builtin_amdgcn_exp2f(x[kb][i] - lse);
+                x[kb][i] = p * (dp[kb][i] - delta);
+            }
+        if (edge) {
+            const int lim = last - j0 - 4 * h;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[kb][i] = 32 * kb + row_of(i) <= lim ? x[kb][i] : 0.0f;
+        }
+        if constexpr (BIAS) {
+            if (a.dbias && far) {
+                float t = 0.0f;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) t += x[kb][i];
+                if (from > 0) far_pos += t;
+                else far_neg += t;
+            } else if (a.dbias) {
+                float* const t = sums + (2 * wave + h) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        __hip_atomic_fetch_add(t - (32 * kb + row_of(i)), x[kb][i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+        }
+        const float f = hold<IO>(x, held, acc);
+        if constexpr (std::is_same_v<IO, _Float16>) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) x[kb] *= f;
+        }
+        uint32_t odd = 0;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int t = 0; t < C::NT; ++t) {
+                float w[C::E];
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) w[e] = x[kb][t * C::E + e];
+                const F p = O::pack(w);
+#pragma unroll
+                for (int cb = 0; cb < DB; ++cb) {
+                    F k[1] = {kcols.get(0, kb, t, cb)};
+                    if (edge) {
+                        const uint32_t o = O::top(k);
+                        odd = o > odd ? o : odd;
+                        k[0] = O::finite(k[0]);
+                    }
+                    O::mma(acc[cb], k[0], p);
+                }
+            }
+        if (edge && __any(odd >= O::kInf)) add_odd_numbers<C, IO, 2>(acc, tk, x, 0, last - j0);
+    }
+    if (n_rows > 0) {
+        const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
+        store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
+    }
+    if constexpr (BIAS) {
+        if (!a.dbias) return;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            far_pos += __shfl_xor(far_pos, m);
+            far_neg += __shfl_xor(far_neg, m);
+        }
+        if (lane == 0) far_sums[wave] = far_pos, far_sums[4 + wave] = far_neg;
+        __syncthreads();
+        for (int x = tid; x < width; x += 256) {
+            float t = sums[x];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) t += sums[k * width + x];
+            sums[x] = t;
+        }
+        __syncthreads();
+        const int side = a.causal ? a.buckets : a.buckets / 2;
+        if (tid < a.buckets) {
+            const bool before = tid < side;  // the key comes before the query (or is its own)
+            const int want = before ? tid : tid - side;
+            auto first = [&](int bucket) {  // least distance of a bucket, or one past the reach
+                int lo = 0, hi = a.reach + 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (map.of[mid] >= bucket) hi = mid;
+                    else lo = mid + 1;
+                }
+                return lo;
+            };
+            int x0 = first(want), x1 = want == side - 1 ? a.reach + kPad + 1 : first(want + 1);
+            if (!before && x0 == 0) x0 = 1;  // distance 0 is of the first side
+            float t = want == side - 1 ? (before ? far_sums[0] + far_sums[1] + far_sums[2] + far_sums[3]
+                                                 : far_sums[4] + far_sums[5] + far_sums[6] + far_sums[7])
+                                       : 0.0f;
+            for (int x = x0; x < x1; ++x) t += sums[a.reach + kPad + (before ? x : -x)];
+            a.parts[((int64_t)head * a.buckets + tid) * a.slots + slot] = t;
+        }
+    }
+}
+
+// Gradients of k and v: a wave owns 32 keys of a kv head and passes over the queries of
+// every head that shares it, in a fixed order.
+template <typename IO, int DB, bool VEC, bool BIAS>
+__global__ __launch_bounds__(256) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+    using C = Shape<IO, DB>;
+    using O = Op32<IO>;
+    using F = typename O::F;
+    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
+    __shared__ float tab[BIAS ? kTab : 1];
+    __shared__ __attribute__((aligned(16))) float stats[2][kTile];
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
+    const int kv = (int)(id / a.kv_slots), r = a.heads / a.kv_heads;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    int64_t b, row0;
+    slot_of(a.kv_offsets, a.batch, a.T_kv, id % a.kv_slots, b, row0);
+    Seq s;
+    tokens_of(a.offsets, a.batch, a.T, b, s.q0, s.n_q);
+    tokens_of(a.kv_offsets, a.batch, a.T_kv, b, s.k0, s.n_k);
+    if (row0 < 0 || row0 >= s.n_k) return;
+    const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_k - w0;
+    const int my = w0 + (lane & 31);
+
+    F k[C::NS], v[C::NS];
+    load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
+    load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
+    f32x16 dk[DB], dv[DB];
+    clear(dk), clear(dv);
+    float held = kTopScale;
+    const float scale = a.scale * kLog2e;
+    const int i_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile * kTile : 0;
+
+    constexpr int NP = (C::P + 3) / 4;
+    const Loader<IO, C::P, NP, true, VEC> lq(a.q, a.D_k, 0, wave, 4), lg(a.d_o, a.D_v, 0, wave, 4);
+    char *const tq = lds, *const tg = lds + C::TILE;
+    const RowFrags<C> qrows(tq), grows(tg);
+    const ColumnFrags<C, O> qcols(tq), gcols(tg);
+    for (int hh = 0; hh < r; ++hh) {
+        const int head = kv * r + hh;
+        if constexpr (BIAS) {
+            __syncthreads();
+            fill_biases<IO>(tab, a, map, head);
+        }
+        for (int i0 = i_first; i0 < s.n_q; i0 += kTile) {
+            __syncthreads();
+            const int n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
+            lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, tq);
+            lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, tg);
+            if (tid < 2 * kTile) {
+                const int i = tid % kTile;
+                const int64_t at = (int64_t)head * a.T + s.q0 + i0 + i;
+                stats[tid / kTile][i] = tid < kTile ? (i < n ? a.row_lse[at] : kInf) : (i < n ? a.row_delta[at] : 0.0f);
+            }
+            wait_loads();
+            __syncthreads();
+            if (n_rows <= 0 || (a.causal && i0 + kTile - 1 + shift < w0)) continue;
+            const bool edge = a.causal && i0 + shift < w0 + 31;
+            const int low = my - shift - i0;  // first row of the tile that sees the lane's key
+            const int from = i0 + shift - w0;  // distance of the tile's first row and the wave's first key
+            const bool far = from - 31 >= a.reach || from + 63 <= -a.reach;
+            const float* t = tab + a.reach + kPad;
+            const float f = BIAS ? t[from > 0 ? a.reach : -a.reach] : 0.0f;
+            t += from - (lane & 31) + 4 * h;
+            uint32_t odd = 0;
+            f32x16 p[2], ds[2];
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb) {
+                f32x16 x = {}, dp = {};
+#pragma unroll
+                for (int st = 0; st < C::NS; ++st) O::mma(x, qrows.template get<F>(0, qb, st), k[st]);
+#pragma unroll
+                for (int st = 0; st < C::NS; ++st) O::mma(dp, grows.template get<F>(0, qb, st), v[st]);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[0][32 * qb + 8 * g + 4 * h]);
+                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[1][32 * qb + 8 * g + 4 * h]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 4 * g + e, at = 32 * qb + row_of(i);
+                        float y = x[i] * scale;
+                        if constexpr (BIAS) y = __builtin_fmaf(x[i], scale, far ? f : t[at]);
+                        const float w = __builtin_amdgcn_exp2f(y - lse[e]);
+                        const bool seen = !edge || at + 4 * h >= low;
+                        p[qb][i] = seen ? w : 0.0f;
+                        ds[qb][i] = seen ? w * (dp[i] - delta[e]) : 0.0f;
+                    }
+                }
+            }
+            const float f16 = hold<IO>(ds, held, dk);
+            if constexpr (std::is_same_v<IO, _Float16>) {
+#pragma unroll
+                for (int qb = 0; qb < 2; ++qb) ds[qb] *= f16, p[qb] *= 4096.0f;
+            }
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb)
+#pragma unroll
+                for (int st = 0; st < C::NT; ++st) {
+                    float w[C::E], u[C::E];
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) w[e] = p[qb][st * C::E + e], u[e] = ds[qb][st * C::E + e];
+                    const F pf = O::pack(w), df = O::pack(u);
+#pragma unroll
+                    for (int cb = 0; cb < DB; ++cb) {
+                        F g[2] = {gcols.get(0, qb, st, cb), qcols.get(0, qb, st, cb)};
+                        if (edge) {
+                            const uint32_t o = O::top(g);
+                            odd = o > odd ? o : odd;
+                            g[0] = O::finite(g[0]), g[1] = O::finite(g[1]);
+                        }
+                        O::mma(dv[cb], g[0], pf);
+                        O::mma(dk[cb], g[1], df);
+                    }
+                }
+            if (edge && __any(odd >= O::kInf)) {
+                add_odd_numbers<C, IO, 2>(dv, tg, p, low, n - 1);
+                add_odd_numbers<C, IO, 2>(dk, tq, ds, low, n - 1);
+            }
+        }
+    }
+    if (n_rows <= 0) return;
+    const bool half = std::is_same_v<IO, _Float16>;
+    store_rows<C, IO>(dk, a.dk, s.k0 + w0, kv, n_rows, a.D_k, half ? a.scale * inverse_of_power(held) : a.scale, a.dk_vec);
+    store_rows<C, IO>(dv, a.dv, s.k0 + w0, kv, n_rows, a.D_v, half ? 1.0f / 4096.0f : 1.0f, a.dv_vec);
+}
+
+// --- host side ------------------------------------------------------------------------
+template <typename IO, int DB, bool VEC, bool BIAS>
+hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
+    in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
+    });
+    return hipGetLastError();
+}
+
+template <typename IO, int DB, bool VEC, bool BIAS>
+hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
+    in_pieces((int64_t)a.kv_slots * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
+    });
+    const size_t sums = BIAS && a.dbias ? (size_t)8 * (2 * (a.reach + kPad) + 1) * 4 : 0;
+    in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), sums, stream, a, map, base);
+    });
+    return hipGetLastError();
+}
+
+#define EQL_ATTENTION(WHAT)                                                                                        \
+    const int db = ((a.D_k > a.D_v ? a.D_k : a.D_v) + 31) / 32;                                                    \
+    const bool bias = a.bias != nullptr;                                                                           \
+    if (db == 1) return EQL_ATTENTION_DB(WHAT, 1);                                                                 \
+    if (db == 2) return EQL_ATTENTION_DB(WHAT, 2);                                                                 \
+    if (db == 3) return EQL_ATTENTION_DB(WHAT, 3);                                                                 \
+    return EQL_ATTENTION_DB(WHAT, 4);
+#define EQL_ATTENTION_DB(WHAT, DB)                                                                                 \
+    vec ? (bias ? WHAT<IO, DB, true, true>(a, map, stream) : WHAT<IO, DB, true, false>(a, map, stream))            \
+        : (bias ? WHAT<IO, DB, false, true>(a, map, stream) : WHAT<IO, DB, false, false>(a, map, stream))
+
+template <typename IO>
+hipError_t forward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {
+    const size_t es = sizeof(IO);
+    const bool vec = vec_ok(a.q, a.D_k, es, 16) && vec_ok(a.k, a.D_k, es, 16) && vec_ok(a.v, a.D_v, es, 16);
+    a.out_vec = vec_ok(a.o, a.D_v, es, 4 * es);
+    EQL_ATTENTION(forward_cfg)
+}
+
+template <typename IO>
+hipError_t backward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {
+    const size_t es = sizeof(IO);
+    const bool vec = vec_ok(a.q, a.D_k, es, 16) && vec_ok(a.k, a.D_k, es, 16) && vec_ok(a.v, a.D_v, es, 16) &&
+                     vec_ok(a.d_o, a.D_v, es, 16);
+    a.dq_vec = vec_ok(a.dq, a.D_k, es, 4 * es);
+    a.dk_vec = vec_ok(a.dk, a.D_k, es, 4 * es);
+    a.dv_vec = vec_ok(a.dv, a.D_v, es, 4 * es);
+    in_pieces((a.T * a.heads + 15) / 16, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((row_kernel<IO>), dim3(wgs), dim3(256), 0, stream, a, base);
+    });
+    EQL_ATTENTION(backward_cfg)
+}
+
+}  // namespace att
+}  // namespace eql

@@ -1,0 +1,77 @@
+// attention.hip -- softmax attention: what a launch takes besides its tensors, the kernels
+// by type (attention.h, instantiated in attention_{forward,backward}_{f32,bf16,f16}.hip),
+// and the join of the biases' gradients.
+#include "attention.h"
+
+namespace eql {
+
+namespace att {
+extern template hipError_t forward<float>(AttentionArgs, const BucketMap&, hipStream_t);
+extern template hipError_t forward<__bf16>(AttentionArgs, const BucketMap&, hipStream_t);
+extern template hipError_t forward<_Float16>(AttentionArgs, const BucketMap&, hipStream_t);
+extern template hipError_t backward<float>(AttentionArgs, const BucketMap&, hipStream_t);
+extern template hipError_t backward<__bf16>(AttentionArgs, const BucketMap&, hipStream_t);
+extern template hipError_t backward<_Float16>(AttentionArgs, const BucketMap&, hipStream_t);
+}  // namespace att
+
+namespace {
+
+using namespace att;
+
+// Gradient of one bias: the sums of every slot of its head, in a fixed order.
+__global__ __launch_bounds__(256) void reduce_kernel(const float* parts, float* dbias, int64_t n) {
+    __shared__ float sum[256];
+    const int tid = (int)threadIdx.x;
+    const float* p = parts + (int64_t)blockIdx.x * n;
+    float t = 0.0f;
+    for (int64_t i = tid; i < n; i += 256) t += p[i];
+    sum[tid] = t;
+    for (int w = 128; w > 0; w >>= 1) {
+        __syncthreads();
+        if (tid < w) sum[tid] += sum[tid + w];
+    }
+    if (tid == 0) dbias[blockIdx.x] = sum[0];
+}
+
+uint32_t slots_for(const int64_t* offsets, int64_t batch, int64_t T) {
+    if (batch <= 0) return 0;
+    return (uint32_t)(offsets ? T / kRows + batch : batch * ((T / batch + kRows - 1) / kRows));
+}
+
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// Rows' statistics, and the sums of each slot's buckets (packed sequences have the most slots).
+size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, bool backward) {
+    if (!backward || T <= 0) return 0;
+    return 2 * round_up((size_t)T * heads * 4) + (size_t)(T / kRows + batch) * heads * buckets * 4;
+}
+
+hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipStream_t stream) {
+    if (a.T <= 0) return hipSuccess;
+    a.slots = slots_for(a.offsets, a.batch, a.T);
+    if ((int64_t)a.slots * a.heads > 0x7fffffff) return hipErrorNotSupported;
+    return io == kIoF32 ? att::forward<float>(a, map, stream)
+                        : (io == kIoBF16 ? att::forward<__bf16>(a, map, stream) : att::forward<_Float16>(a, map, stream));
+}
+
+hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& map, void* ws, hipStream_t stream) {
+    const size_t n = round_up((size_t)a.T * a.heads * 4);
+    a.row_lse = static_cast<float*>(ws);
+    a.row_delta = reinterpret_cast<float*>(static_cast<char*>(ws) + n);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n);
+    a.slots = slots_for(a.offsets, a.batch, a.T);
+    a.kv_slots = slots_for(a.kv_offsets, a.batch, a.T_kv);
+    if ((int64_t)a.slots * a.heads > 0x7fffffff || (int64_t)a.kv_slots * a.kv_heads > 0x7fffffff) return hipErrorNotSupported;
+    const hipError_t e = io == kIoF32 ? att::backward<float>(a, map, stream)
+                         : io == kIoBF16 ? att::backward<__bf16>(a, map, stream)
+                                         : att::backward<_Float16>(a, map, stream);
+    if (e != hipSuccess) return e;
+    if (a.dbias)
+        hipLaunchKernelGGL(reduce_kernel, dim3((uint32_t)(a.heads * a.buckets)), dim3(256), 0, stream, a.parts, a.dbias,
+                           (int64_t)a.slots);
+    return hipGetLastError();
+}
+
+}  // namespace eql

@@ -173,4 +173,72 @@ hipError_t launch_linear_attention(int io, const MixArgs& a, void* ws, hipStream
 hipError_t launch_linear_attention_backward(int io, const MixArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_linear_attention_step(int io, const MixArgs& a, hipStream_t stream);
 
+// attention*.hip.  of: bucket of the distances 0 .. reach on one side.
+constexpr int kMaxBuckets = 256, kMaxReach = 1024;
+struct BucketMap {
+    uint8_t of[kMaxReach + 1];
+};
+struct AttentionArgs {
+    uint32_t slots, kv_slots;  // runs of rows of all sequences
+    int causal;
+    float scale;
+    int64_t batch, T, T_kv;
+    const int64_t *offsets, *kv_offsets;
+    int heads, kv_heads, D_k, D_v;  // D_k, D_v: numbers per head
+    Heads q, k, v, o;
+    const void* bias;  // [heads][buckets], or null
+    int buckets, reach;
+    float* lse;
+    Heads d_o, dq, dk, dv;  // backward
+    float* dbias;
+    float *row_lse, *row_delta, *parts;  // workspace
+    int out_vec, dq_vec, dk_vec, dv_vec;  // rows of an output in whole pieces of four
+};
+size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, bool backward);
+hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipStream_t stream);
+hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& map, void* ws, hipStream_t stream);
+
+// attention_step.hip: one query for each of batch sequences, keys and values through block tables.
+struct Pages {
+    const void* p;
+    int64_t bs, ts, hs;  // elements from block to block, token to token, head to head
+};
+struct StepArgs {
+    Heads q, o;
+    Pages k, v;
+    const int32_t *table, *lengths;
+    int64_t batch, blocks;
+    int max_blocks, block_size;
+    int heads, kv_heads, D_k, D_v;
+    float scale;
+    const void* bias;
+    int buckets, reach;
+    float* lse;
+};
+size_t attention_step_workspace(int heads, int kv_heads, int D_v, int64_t batch);
+hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream);
+
+// cache.hip: the tables of a paged cache, and the store of new tokens.
+struct TablesArgs {
+    const int32_t *lengths, *added, *free_blocks, *cursor;
+    int32_t* table;
+    int32_t *lengths_out, *cursor_out;
+    int64_t* slots;
+    int32_t* positions;
+    int64_t* offsets;
+    int64_t batch, n_free, T;
+    int max_blocks, block_size;
+};
+size_t cache_tables_workspace(int64_t batch);
+hipError_t launch_cache_tables(const TablesArgs& a, void* ws, hipStream_t stream);
+
+struct StoreArgs {
+    Heads k, v;
+    Pages k_cache, v_cache;
+    const int64_t* slots;
+    int64_t T, blocks;
+    int block_size, kv_heads, D_k, D_v;
+};
+hipError_t launch_cache_store(int io, const StoreArgs& a, hipStream_t stream);
+
 }  // namespace eql

@@ -9,8 +9,8 @@ struct eqlinear_plan_s {
     int kind;
     int dtype;
     int N;
-    int C_in, C_out;  // rotary and mixer plans: channels of all query heads in and out
-    // rotary and mixer plans
+    int C_in, C_out;  // rotary, mixer and attention plans: channels of all query heads in and out
+    // rotary, mixer and attention plans
     int heads = 0, kv_heads = 0;
     int d_k = 0, d_v = 0;  // channels per head (rotary: both d)
     // rotary plans
@@ -19,6 +19,9 @@ struct eqlinear_plan_s {
     // norm plans (C_in = C_out = C)
     int groups = 0, act = 0;
     float eps = 0.0f;
+    // attention plans
+    int causal = 0, buckets = 0, reach = 0;
+    eql::BucketMap map{};
 };
 
 namespace eql {

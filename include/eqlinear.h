@@ -68,7 +68,8 @@ typedef enum {
     EQL_KIND_D8 = 1,
     EQL_KIND_ROTARY = 2, /* eqlinear_rotary_plan */
     EQL_KIND_MIXER = 3,  /* eqlinear_mixer_plan */
-    EQL_KIND_NORM = 4    /* eqlinear_norm_plan */
+    EQL_KIND_NORM = 4,   /* eqlinear_norm_plan */
+    EQL_KIND_ATTENTION = 5 /* eqlinear_attention_plan */
 } eqlinear_kind;
 
 typedef struct eqlinear_plan_s* eqlinear_plan_t;
@@ -81,7 +82,8 @@ typedef struct {
     int32_t dtype;              /* eqlinear_dtype */
     int32_t N;                  /* group order (8 for D8) */
     int32_t C_in, C_out;        /* C_N: channels per group element; D8: full widths;
-                                   rotary, mixer: channels of all query heads; norm: C */
+                                   rotary, mixer, attention: channels of all query heads;
+                                   norm: C */
     int32_t bins;               /* C_N: floor(N/2)+1 kept frequencies; D8: 5 irrep blocks */
     int32_t planes;             /* C_N: real frequency planes (= N) */
     int32_t has_nyquist;        /* C_N: 1 when N is even */
@@ -593,6 +595,138 @@ eqlinear_status eqlinear_group_norm_backward(eqlinear_plan_t plan, const void* d
                                              const float* stats, const int64_t* offsets, int64_t batch, void* dx,
                                              int64_t dx_stride, float* dgamma, float* dbeta, int64_t T,
                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Plan of softmax attention: heads query heads that share kv_heads key and value heads
+ * (heads a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads)), d_k
+ * channels per query and key head and d_v per value head; d_k N and d_v N at most 128
+ * (EQL_ERR_UNSUPPORTED beyond).  causal != 0: a query sees no key after its own position.
+ * buckets > 0: calls may take a learned bias for every head and bucket of distances; else
+ * buckets = 0 and max_distance is ignored.
+ * Buckets.  A query at position p and a key at position j are p - j apart.  One side of
+ * distances n = 0, 1, ... has B buckets: causal plans one side, B = buckets >= 2; others
+ * two, B = buckets / 2 >= 2 (buckets even), keys after the query taking the second B.  With
+ * e = B / 2 and m = B - e, distances below e have a bucket each, and n >= e has bucket
+ * e + b for the largest b < m with n^m >= e^(m-b) max_distance^b: equal steps of the
+ * logarithm from e to max_distance, which is more than e; all from there on share the last.
+ * buckets at most 256 and max_distance at most 1024 (EQL_ERR_UNSUPPORTED beyond).
+ * Host metadata only. */
+eqlinear_status eqlinear_attention_plan(eqlinear_plan_t* out, int N, int heads, int kv_heads, int d_k, int d_v, int causal,
+                                        int buckets, int max_distance, eqlinear_dtype dt);
+
+/* Bucket of a distance (query's position less key's), -1 for plans of other kinds or
+ * without buckets and for distances that a causal query does not see. */
+int eqlinear_attention_bucket(eqlinear_plan_t plan, int64_t distance);
+
+/* Bytes of workspace of eqlinear_attention, or with backward != 0 of either call (0: none
+ * needed); 0 for other plans and for sizes that the calls refuse. */
+size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_kv, int64_t batch, int backward);
+
+/* Softmax attention for prompts and training.  A sequence has n_q queries and n_k keys;
+ * query i stands at position i + n_k - n_q (the last query beside the last key):
+ *   s_ij = scale q_i . k_j + bias[head][bucket],  P_ij = exp(s_ij) / sum over the keys
+ *   that query i sees of exp(s_ij),  o_i = sum P_ij v_j,  lse_i = log sum exp(s_ij)
+ *   q [T][heads][d_k][N], k [T_kv][kv_heads][d_k][N], v [T_kv][kv_heads][d_v][N],
+ *   o [T][heads][d_v][N]
+ *   scale     finite, not 0
+ *   bias      [heads][buckets], plan dtype, element-aligned, or NULL
+ *   offsets, kv_offsets  batch + 1 each, of the queries and of the keys (they may be the
+ *             same array); NULL: equal lengths T / batch, T_kv / batch
+ *   lse       fp32 [heads][T], for the backward or to join attention over several sets of
+ *             keys, or NULL
+ * A query that sees no key (or whose every score is -infinity) has o = 0 and lse =
+ * -infinity.  What a query does not see does not change its bits, NaN and infinities
+ * included.  Tokens that belong to no sequence are neither read for others nor written.
+ * 16-bit plans round the probabilities to the plan dtype before their product with v
+ * (fp16: times 2^12, so that one of 2^-36 of the largest counts); scores, sums and o's
+ * accumulation are fp32, o is rounded once.  T and T_kv at most 2^30 (EQL_ERR_UNSUPPORTED).
+ * Asynchronous on stream, no allocation; deterministic. */
+eqlinear_status eqlinear_attention(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
+                                   const eqlinear_heads* v, float scale, const void* bias, const int64_t* offsets,
+                                   const int64_t* kv_offsets, int64_t batch, const eqlinear_heads* o, float* lse, int64_t T,
+                                   int64_t T_kv, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients from o, its upstream gradient d_o and lse (all as the forward took and gave
+ * them), with probabilities made again from the scores: with delta_i = d_o_i . o_i,
+ *   dS_ij = P_ij (d_o_i . v_j - delta_i),  dq_i = scale sum_j dS_ij k_j,
+ *   dk_j = scale sum dS_ij q_i,  dv_j = sum P_ij d_o_i  (over the queries of every head
+ *   that shares the key),  d_bias[head][b] = sum of dS_ij over the pairs of bucket b
+ *   d_bias  fp32 [heads][buckets], or NULL; overwritten
+ * 16-bit plans round P and dS to the plan dtype before their products (fp16: times powers of
+ * two that keep them within its range, so that gradients may be smaller or larger than fp16's
+ * numbers as long as dq, dk and dv are not); d_bias sums dS in fp32.  Rows of k and v that no
+ * query sees get zeros.  Asynchronous on stream, no allocation; deterministic. */
+eqlinear_status eqlinear_attention_backward(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
+                                            const eqlinear_heads* v, const eqlinear_heads* o, const eqlinear_heads* d_o,
+                                            const float* lse, float scale, const void* bias, const int64_t* offsets,
+                                            const int64_t* kv_offsets, int64_t batch, const eqlinear_heads* dq,
+                                            const eqlinear_heads* dk, const eqlinear_heads* dv, float* d_bias, int64_t T,
+                                            int64_t T_kv, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keys or values of a paged cache, [blocks][block_size][kv_heads][d][N] with the last two
+ * axes contiguous; strides in elements.  Slot s is token s % block_size of block
+ * s / block_size.  Element alignment is enough; whole 16-byte rows run faster. */
+typedef struct {
+    void* ptr;
+    int64_t block_stride, token_stride, head_stride;
+} eqlinear_pages;
+
+/* Bytes of workspace of eqlinear_attention_step (0: none needed); 0 for other plans. */
+size_t eqlinear_attention_step_workspace(eqlinear_plan_t plan, int64_t batch);
+
+/* Attention of one new token for each of batch sequences (serving), over keys and values in
+ * a paged cache, the new token's own among them:
+ *   q [batch][heads][d_k][N], o [batch][heads][d_v][N]; the query stands at position
+ *             lengths[b] - 1 and sees the keys 0 .. lengths[b] - 1
+ *   table     int32 [batch][max_blocks], device: the blocks of each sequence in order
+ *   lengths   int32 [batch], device; at most max_blocks block_size count
+ *   lse       fp32 [heads][batch], or NULL
+ * Keys of a block that the cache does not have (negative, or blocks and above) count as not
+ * there; a sequence without keys has o = 0, lse = -infinity.  Entries past a sequence's
+ * last block are not read.  Roundings as in eqlinear_attention.  A long sequence is split
+ * over workgroups whose parts are joined in a fixed order.  max_blocks block_size at most
+ * 2^30 (EQL_ERR_UNSUPPORTED).  Asynchronous on stream, no allocation; deterministic. */
+eqlinear_status eqlinear_attention_step(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_pages* k_cache,
+                                        const eqlinear_pages* v_cache, int64_t blocks, int block_size, const int32_t* table,
+                                        int64_t max_blocks, const int32_t* lengths, float scale, const void* bias,
+                                        const eqlinear_heads* o, float* lse, int64_t batch, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of eqlinear_cache_tables. */
+size_t eqlinear_cache_tables_workspace(int64_t batch);
+
+/* The tables of a paged cache for the next step, from the requests' lengths, on the device
+ * alone.  All arrays are device arrays.  Request b holds lengths[b] tokens in the cache and
+ * gets added[b] more, which are packed one request after the other:
+ *   offsets     int64 [batch + 1]: first new token of each request (as the sequences of
+ *               eqlinear_attention)
+ *   positions   int32 [T]: each new token's position (as eqlinear_rotary takes them)
+ *   slots       int64 [T]: its place in the cache (as eqlinear_cache_store takes them)
+ *   lengths_out int32 [batch]: lengths + added; it may be lengths
+ *   table       int32 [batch][max_blocks]: entries of new blocks are written, in order of the
+ *               requests from free_blocks[cursor] on; all others are left as they were
+ *   free_blocks int32 [n_free]; cursor int32: its first entry not yet taken; cursor_out:
+ *               the first after this call (more than n_free: the list fell short); it may be
+ *               cursor
+ * A new block past the free list's end is -1 in the table.  Tokens without a block (so, or
+ * past max_blocks block_size, or in an entry below 0) have slot -1.  Entries of slots and
+ * positions past the last new token are set to -1 and 0; new tokens past T are dropped and
+ * not counted.  Negative lengths and additions count as 0.  max_blocks block_size, n_free
+ * and T at most 2^30 (EQL_ERR_UNSUPPORTED).  Outputs must not overlap inputs or each other
+ * except as said; workspace 256-byte aligned.  Asynchronous on stream, no allocation. */
+eqlinear_status eqlinear_cache_tables(const int32_t* lengths, const int32_t* added, const int32_t* free_blocks, int64_t n_free,
+                                      const int32_t* cursor, int32_t* table, int64_t max_blocks, int block_size,
+                                      int32_t* lengths_out, int32_t* cursor_out, int64_t* slots, int32_t* positions,
+                                      int64_t* offsets, int64_t batch, int64_t T, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/* New tokens' keys and values into the cache: row t of k [T][kv_heads][d_k][N] and
+ * v [T][kv_heads][d_v][N] to slot slots[t].  Slots below 0 or past the cache are skipped;
+ * two tokens of one call must not have the same slot (which of them is kept, number by
+ * number, is not defined).  k_cache and v_cache may be slices of one buffer whose blocks, or
+ * whose tokens, hold keys and values in turn.  Asynchronous on stream, no allocation. */
+eqlinear_status eqlinear_cache_store(eqlinear_plan_t plan, const eqlinear_heads* k, const eqlinear_heads* v,
+                                     const int64_t* slots, const eqlinear_pages* k_cache, const eqlinear_pages* v_cache,
+                                     int64_t blocks, int block_size, int64_t T, void* stream);
 
 #ifdef __cplusplus
 }
