@@ -411,27 +411,6 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
 
 
 // --- backward -------------------------------------------------------------------------
-// Per query and head, for the kernels below: lse in powers of two (+infinity for a row
-// that sees nothing, which makes its probabilities 0) and delta = d_o . o.  16 lanes a row.
-template <typename IO>
-__global__ __launch_bounds__(256) void row_kernel(AttentionArgs a, uint32_t base) {
-    const int tid = (int)threadIdx.x, l = tid & 15;
-    const int64_t row = ((int64_t)blockIdx.x + base) * 16 + (tid >> 4), n = a.T * a.heads;
-    if (row >= n) return;
-    const int64_t head = row / a.T, t = row - head * a.T;
-    const IO* o = (const IO*)a.o.p + t * a.o.ts + head * a.o.hs;
-    const IO* g = (const IO*)a.d_o.p + t * a.d_o.ts + head * a.d_o.hs;
-    float d = 0.0f;
-    for (int e = l; e < a.D_v; e += 16) d = __builtin_fmaf((float)o[e], (float)g[e], d);
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) d += __shfl_xor(d, m);
-    if (l == 0) {
-        const float s = a.lse[row];
-        a.row_lse[row] = s == -kInf ? kInf : s * kLog2e;
-        a.row_delta[row] = d;
-    }
-}
-
 // fp16: takes the lane's sums to a scale that holds its numbers x, and returns x's.
 template <typename IO, int N, int DB>
 __device__ __forceinline__ float hold(const f32x16 (&x)[N], float& f, f32x16 (&acc)[DB]) {
@@ -454,7 +433,11 @@ __device__ __forceinline__ float hold(const f32x16 (&x)[N], float& f, f32x16 (&a
 }
 
 // Gradients of q and, if wanted, of the biases: a wave owns 32 queries and passes over the
-// keys.  Of the biases, dS is summed by distance, each wave's halves in an array of their
+// keys twice.  The first pass makes delta = sum P dP, as what do . o leaves of it: o is
+// rounded to the plan's type, and delta from it alone is off by that rounding, which dS (a
+// difference) shows twofold and the biases' fp32 gradients by 1e-3 of their size.  It also
+// takes lse's own rounding out of P (sum P = 1), and leaves both for dkv_kernel.  The second
+// makes dS.  Of the biases, dS is summed by distance, each wave's halves in an array of their
 // own (the lanes of an instruction hold 32 distances apiece, all different, and a wave's
 // instructions come in order: the sums do not depend on timing); distances past the reach
 // share a bucket on either side and are summed in registers.  A workgroup writes the sums
@@ -493,8 +476,19 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
     load_rows<C, IO, F, VEC>(d_o, a.d_o, s.q0 + w0, head, n_rows, a.D_v);
     const bool real = (lane & 31) < n_rows;
-    const float lse = real ? a.row_lse[(int64_t)head * a.T + s.q0 + my] : kInf;
-    const float delta = real ? a.row_delta[(int64_t)head * a.T + s.q0 + my] : 0.0f;
+    const int64_t row = (int64_t)head * a.T + s.q0 + my;
+    // in powers of two; a row that sees nothing has probabilities of 0
+    float lse = real ? a.lse[row] * kLog2e : kInf, delta = 0.0f, left = 0.0f, ones = 0.0f;
+    lse = lse == -kInf ? kInf : lse;
+    {
+        F o[C::NS];
+        load_rows<C, IO, F, VEC>(o, a.o, s.q0 + w0, head, n_rows, a.D_v);
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st)
+#pragma unroll
+            for (int e = 0; e < C::E; ++e) delta = __builtin_fmaf(O::get(o[st], e), O::get(d_o[st], e), delta);
+        delta += __shfl_xor(delta, 32);
+    }
     f32x16 acc[DB];
     clear(acc);
     float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
@@ -509,16 +503,15 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     char *const tk = lds, *const tv = lds + C::TILE;
     const RowFrags<C> krows(tk), vrows(tv);
     const ColumnFrags<C, O> kcols(tk);
-    for (int j0 = 0; j0 < end; j0 += kTile) {
+    // One tile: probabilities and dP.  False: none of the wave's rows sees it.
+    auto scores = [&](int j0, f32x16 (&x)[2], f32x16 (&dp)[2], int from, bool far) {
         __syncthreads();
         const int n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
         lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, tk);
         lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, tv);
         wait_loads();
         __syncthreads();
-        if (n_rows <= 0 || j0 >= wave_end) continue;
-        const bool edge = j0 + kTile - 1 > wave_all;
-        f32x16 x[2], dp[2];
+        if (n_rows <= 0 || j0 >= wave_end) return false;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             x[kb] = f32x16{}, dp[kb] = f32x16{};
@@ -527,28 +520,51 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
 #pragma unroll
             for (int st = 0; st < C::NS; ++st) O::mma(dp[kb], vrows.template get<F>(0, kb, st), d_o[st]);
         }
-        const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
-        const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
-        if constexpr (BIAS) {
-            const float* t = tab + a.reach + kPad;
-            const float f = t[from > 0 ? a.reach : -a.reach];
-            t += from + (lane & 31) - 4 * h;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[kb][i] = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
-        } else {
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) x[kb] *= scale;
-        }
+        const float* t = tab + a.reach + kPad;
+        const float f = BIAS ? t[from > 0 ? a.reach : -a.reach] : 0.0f;
+        t += from + (lane & 31) - 4 * h;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(x[kb][i] - lse);
-                x[kb][i] = p * (dp[kb][i] - delta);
+                float y = x[kb][i] * scale;
+                if constexpr (BIAS) y = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
+                x[kb][i] = __builtin_amdgcn_exp2f(y - lse);
             }
+        return true;
+    };
+    for (int j0 = 0; j0 < end; j0 += kTile) {
+        f32x16 x[2], dp[2];
+        const int from = w0 + shift - j0;
+        if (!scores(j0, x, dp, from, from - 63 >= a.reach || from + 31 <= -a.reach)) continue;
+        const bool edge = j0 + kTile - 1 > wave_all;
+        const int lim = last - j0 - 4 * h;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool seen = !edge || 32 * kb + row_of(i) <= lim;
+                ones += seen ? x[kb][i] : 0.0f;
+                left += seen ? x[kb][i] * (dp[kb][i] - delta) : 0.0f;
+            }
+    }
+    ones += __shfl_xor(ones, 32);
+    left += __shfl_xor(left, 32);
+    if (ones != 0.0f) {
+        delta += left / ones;
+        lse += __builtin_amdgcn_logf(ones);
+    }
+    if (real && h == 0) a.row_lse[row] = lse, a.row_delta[row] = delta;
+    for (int j0 = 0; j0 < end; j0 += kTile) {
+        f32x16 x[2], dp[2];
+        const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
+        const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
+        if (!scores(j0, x, dp, from, far)) continue;
+        const bool edge = j0 + kTile - 1 > wave_all;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[kb][i] = x[kb][i] * (dp[kb][i] - delta);
         if (edge) {
             const int lim = last - j0 - 4 * h;
 #pragma unroll
@@ -645,7 +661,7 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     }
 }
 
-// Gradients of k and v: a wave owns 32 keys of a kv head and passes over the queries of
+// Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the queries of
 // every head that shares it, in a fixed order.
 template <typename IO, int DB, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
@@ -780,12 +796,12 @@ hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t
 
 template <typename IO, int DB, bool VEC, bool BIAS>
 hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
-    in_pieces((int64_t)a.kv_slots * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
-    });
     const size_t sums = BIAS && a.dbias ? (size_t)8 * (2 * (a.reach + kPad) + 1) * 4 : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), sums, stream, a, map, base);
+    });
+    in_pieces((int64_t)a.kv_slots * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
     });
     return hipGetLastError();
 }
@@ -813,13 +829,10 @@ template <typename IO>
 hipError_t backward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {
     const size_t es = sizeof(IO);
     const bool vec = vec_ok(a.q, a.D_k, es, 16) && vec_ok(a.k, a.D_k, es, 16) && vec_ok(a.v, a.D_v, es, 16) &&
-                     vec_ok(a.d_o, a.D_v, es, 16);
+                     vec_ok(a.o, a.D_v, es, 16) && vec_ok(a.d_o, a.D_v, es, 16);
     a.dq_vec = vec_ok(a.dq, a.D_k, es, 4 * es);
     a.dk_vec = vec_ok(a.dk, a.D_k, es, 4 * es);
     a.dv_vec = vec_ok(a.dv, a.D_v, es, 4 * es);
-    in_pieces((a.T * a.heads + 15) / 16, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((row_kernel<IO>), dim3(wgs), dim3(256), 0, stream, a, base);
-    });
     EQL_ATTENTION(backward_cfg)
 }
 
