@@ -12,42 +12,52 @@ using att::kInf;
 using att::kLn2;
 using att::kLog2e;
 
-constexpr int kQueries = 16;  // query heads of one workgroup: the columns of a matrix product
-constexpr int kKeys = 32;     // keys of a wave's tile
+constexpr int kQueries = 16;     // query heads of one workgroup: the columns of a matrix product
+constexpr int kKeys = 32;        // keys of a wave's tile
+constexpr int kUnit = 4 * kKeys;  // keys of a workgroup's pass
+constexpr int kMaxShared = 2048;  // sequences whose lengths a workgroup sums up
+constexpr int kWorkgroups = 768;
 
+// A sequence's keys are units of kUnit; an item is one (sequence, kv head, run of kQueries of
+// its query heads).  Up to kMaxShared sequences, the units of all items lie in one row that is
+// cut evenly: workgroup w of the W that have any (at most one a unit) takes units w n / W ..
+// (w + 1) n / W, whatever sequences they belong to, so that lengths need not be alike (or known
+// on the host).  An item inside one
+// workgroup is finished there; of one that spans several, each writes its part, at 2 w + 1 if
+// the item starts in w, else at 2 w, and join_kernel takes them in order.  With more sequences
+// each item is one workgroup's.
 struct Grid {
-    int groups, splits;  // of the query heads of a kv head; of a sequence
+    int groups, items;  // runs of the query heads of a kv head; items of a sequence
+    int shared;
+    uint32_t wgs;
 };
 Grid grid_for(int heads, int kv_heads, int64_t batch) {
     Grid g;
     g.groups = (heads / kv_heads + kQueries - 1) / kQueries;
-    const int64_t n = batch * kv_heads * g.groups;
-    g.splits = (int)(n >= 1024 ? 1 : (1024 + n - 1) / n);
-    g.splits = g.splits > 64 ? 64 : g.splits;
+    g.items = kv_heads * g.groups;
+    g.shared = batch <= kMaxShared;
+    g.wgs = g.shared ? kWorkgroups : (uint32_t)(batch * g.items);
     return g;
 }
+struct Cut {
+    int64_t units, W;
+    __device__ __forceinline__ Cut(int64_t n, uint32_t wgs) : units(n), W(n < wgs ? n : wgs) {}
+    __device__ __forceinline__ int64_t first(int64_t w) const { return w < W ? w * units / W : units; }
+    __device__ __forceinline__ int64_t owner(int64_t unit) const { return ((unit + 1) * W - 1) / units; }
+};
 
-// Keys of split `split` of a sequence of n: whole tiles of all four waves.
-__device__ __forceinline__ void keys_of(int n, int splits, int split, int& k0, int& k1) {
-    const int tiles = (n + 4 * kKeys - 1) / (4 * kKeys), per = (tiles + splits - 1) / splits * (4 * kKeys);
-    const int64_t a = (int64_t)split * per;
-    k0 = a < n ? (int)a : n;
-    k1 = a + per < n ? (int)(a + per) : n;
-}
 __device__ __forceinline__ int length_of(const StepArgs& a, int64_t b) {
     const int n = a.lengths[b];
     const int64_t most = (int64_t)a.max_blocks * a.block_size;
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
+// (an empty sequence has one unit, of no keys: its outputs are written too)
+__device__ __forceinline__ int units_of(int n) { return n > 0 ? (n + kUnit - 1) / kUnit : 1; }
 
-// Element offset of a key's row, or -1 where its block is none of the cache's.
-__device__ __forceinline__ int64_t row_of_key(const StepArgs& a, const Pages& x, int64_t b, int key, int kv) {
-    const int blk = key / a.block_size;
-    const int id = a.table[b * a.max_blocks + blk];
-    if (id < 0 || id >= a.blocks) return -1;
-    return id * x.bs + (int64_t)(key - blk * a.block_size) * x.ts + kv * x.hs;
-}
-
+// One wave takes 32 keys at a time: scores S^T = K Q^T with the keys as rows straight from
+// memory, the values through an LDS tile of its own (read back transposed), both for the next
+// keys while it works on these, and the blocks of the keys after those.  Its four waves'
+// sums are joined at the end of an item.
 template <typename IO, int DB, bool VEC>
 __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Grid g, float* ws, uint32_t base) {
     using O = Op<IO>;
@@ -56,206 +66,328 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
     constexpr int NL = kKeys * P / 64;  // loads of a tile of v
     __shared__ __attribute__((aligned(16))) char lds[4][kKeys * P * 16];
     __shared__ float ms[4][kQueries], ls[4][kQueries], all_top[kQueries], all_sum[kQueries];
+    __shared__ int wave_units[4];
+    extern __shared__ int shared[];  // units before each sequence; the biases of an item; the buckets of its distances
     const uint32_t wg = blockIdx.x + base;
-    const int split = (int)(wg % (uint32_t)g.splits);
-    uint32_t rest = wg / (uint32_t)g.splits;
-    const int group = (int)(rest % (uint32_t)g.groups);
-    rest /= (uint32_t)g.groups;
-    const int kv = (int)(rest % (uint32_t)a.kv_heads);
-    const int64_t b = rest / (uint32_t)a.kv_heads;
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, kg = lane >> 4, ln = lane & 15;
-    const int r = a.heads / a.kv_heads, nq = r - group * kQueries < kQueries ? r - group * kQueries : kQueries;
-    const int head0 = kv * r + group * kQueries;
-    const int n = length_of(a, b);
-    int k0, k1;
-    keys_of(n, g.splits, split, k0, k1);
-    if (k0 >= k1 && !(split == 0 && n == 0)) return;
-
-    F q[NM];
-    {
-        const IO* p = (const IO*)a.q.p + b * a.q.ts + (int64_t)(head0 + (ln < nq ? ln : 0)) * a.q.hs;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const u32x4 v = load_piece<IO>(p, (4 * m + kg) * E, ln < nq ? a.D_k : 0);
-            q[m] = __builtin_bit_cast(F, v);
-        }
-    }
-    f32x4 acc[NB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float top = -kInf, total = 0.0f;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4, ln = lane & 15;
+    const int r = a.heads / a.kv_heads, nr = r < kQueries ? r : kQueries;
     const float scale = a.scale * kLog2e;
-    char* const tv = lds[wave];
-    for (int j0 = k0 + wave * kKeys; j0 < k1; j0 += 4 * kKeys) {
-        f32x4 x[2];
-        bool ok[2][4];
+    float* const biases = reinterpret_cast<float*>(shared + (g.shared ? a.batch + 1 : 0));
+    uint8_t* const buckets = reinterpret_cast<uint8_t*>(biases + kQueries * a.buckets);
+
+    if (a.bias)
+        for (int i = tid; i <= a.reach; i += 256) buckets[i] = map.of[i];
+    int64_t u0, u1;
+    if (g.shared) {
+        constexpr int N = kMaxShared / 256;
+        const int B = (int)a.batch, per = (B + 255) / 256;
+        int n[N], sum = 0;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const int key = j0 + 16 * kb + ln;
-            const int64_t at = key < k1 ? row_of_key(a, a.k, b, key, kv) : -1;
-            const IO* p = (const IO*)a.k.p + (at < 0 ? 0 : at);
-            x[kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < N; ++i) {
+            const int b = tid * per + i;
+            n[i] = i < per && b < B ? units_of(length_of(a, b)) : 0;
+            sum += n[i];
+        }
+        int at = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int w = __shfl_up(at, o);
+            if (lane >= o) at += w;
+        }
+        if (lane == 63) wave_units[wave] = at;
+        __syncthreads();
+        at -= sum;
+        for (int w = 0; w < wave; ++w) at += wave_units[w];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int b = tid * per + i;
+            if (i < per && b <= B) shared[b] = at;
+            at += n[i];
+        }
+        if (tid == 255 && per * 256 <= B) shared[B] = at;
+        __syncthreads();
+        if (wg == 0)  // for join_kernel
+            for (int b = tid; b <= B; b += 256) reinterpret_cast<int*>(ws)[b] = shared[b];
+        const Cut cut((int64_t)shared[B] * g.items, g.wgs);
+        u0 = cut.first(wg), u1 = cut.first(wg + 1);
+    } else {
+        u0 = 0, u1 = 1;
+    }
+    float* const parts = ws + (g.shared ? (a.batch + 1 + 63) / 64 * 64 : 0);
+
+    while (u0 < u1) {
+        int64_t b;
+        int item, unit, n, count;
+        bool starts = true, ends = true;
+        if (g.shared) {
+            int lo = 0, hi = (int)a.batch - 1;  // last sequence whose units start at u0 or before
+            const int64_t target = u0 / g.items;
+            // units of sequence b are shared[b] g.items .. shared[b + 1] g.items
+            while (lo < hi) {
+                const int mid = lo + (hi - lo + 1) / 2;
+                if (shared[mid] <= target) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            n = length_of(a, b);
+            const int of = units_of(n);
+            const int64_t in = u0 - (int64_t)shared[lo] * g.items;
+            item = (int)(in / of);
+            unit = (int)(in - (int64_t)item * of);
+            count = u1 - u0 < of - unit ? (int)(u1 - u0) : of - unit;
+            starts = unit == 0, ends = unit + count == of;
+        } else {
+            b = wg / (uint32_t)g.items;
+            item = (int)(wg - (uint32_t)b * (uint32_t)g.items);
+            n = length_of(a, b);
+            unit = 0, count = units_of(n);
+        }
+        u0 += g.shared ? count : 1;
+        const int kv = item / g.groups, group = item - kv * g.groups;
+        const int nq = r - group * kQueries < kQueries ? r - group * kQueries : kQueries, head0 = kv * r + group * kQueries;
+        const int k0 = unit * kUnit, k1 = n - k0 < count * kUnit ? n : k0 + count * kUnit;
+
+        // Row offsets of a tile's keys, in lanes 0 .. 31 (and again 32 .. 63): -1 where there is none.
+        auto block_of = [&](int j0) {
+            const int key = j0 + (lane & 31);
+            return key < k1 ? a.table[b * a.max_blocks + (uint32_t)key / (uint32_t)a.block_size] : -1;
+        };
+        struct Tile {
+            u32x4 k[2][NM], v[NL];
+            uint32_t there;  // keys of the tile, a bit each
+        };
+        auto load = [&](Tile& t, int j0, int id) {
+            const int key = j0 + (lane & 31);
+            const bool ok = id >= 0 && id < a.blocks;
+            t.there = (uint32_t)__ballot(ok);
+            const int64_t in = (uint32_t)key % (uint32_t)a.block_size, blk = ok ? id : 0;
+            const int64_t kat = ok ? blk * a.k.bs + in * a.k.ts : 0, vat = ok ? blk * a.v.bs + in * a.v.ts : 0;
+            const IO* const kp = (const IO*)a.k.p + kv * a.k.hs;
+            const IO* const vp = (const IO*)a.v.p + kv * a.v.hs;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const IO* p = kp + __shfl(kat, 16 * kb + ln);
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    const int col = (4 * m + kg) * E;
+                    if constexpr (VEC) t.k[kb][m] = *reinterpret_cast<const u32x4*>(p + (col < a.D_k ? col : 0));
+                    else t.k[kb][m] = load_piece<IO>(p, col, a.D_k);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int s = 64 * i + lane, col = s % P * E;
+                const IO* p = vp + __shfl(vat, s / P);
+                if constexpr (VEC) t.v[i] = *reinterpret_cast<const u32x4*>(p + (col < a.D_v ? col : 0));
+                else t.v[i] = load_piece<IO>(p, col, a.D_v);
+            }
+        };
+
+        const int j_first = k0 + wave * kKeys;
+        int id = block_of(j_first);
+        Tile tile;
+        load(tile, j_first, id);
+        id = block_of(j_first + kUnit);
+
+        F q[NM];
+        {
+            const IO* p = (const IO*)a.q.p + b * a.q.ts + (int64_t)(head0 + (ln < nq ? ln : 0)) * a.q.hs;
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                u32x4 v = {0u, 0u, 0u, 0u};
                 const int col = (4 * m + kg) * E;
-                if (at >= 0) {
-                    if constexpr (VEC) {
-                        if (col < a.D_k) v = *reinterpret_cast<const u32x4*>(p + col);
-                    } else {
-                        v = load_piece<IO>(p, col, a.D_k);
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (VEC && a.q_vec) {
+                    if (ln < nq && col < a.D_k) v = *reinterpret_cast<const u32x4*>(p + col);
+                } else {
+                    v = load_piece<IO>(p, col, ln < nq ? a.D_k : 0);
+                }
+                q[m] = __builtin_bit_cast(F, v);
+            }
+        }
+        if (a.bias)
+            for (int i = tid; i < nq * a.buckets; i += 256)
+                biases[i] = kLog2e * (float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i];
+        __syncthreads();
+
+        f32x4 acc[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float top = -kInf, total = 0.0f;
+        char* const tv = lds[wave];
+        const float far = a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.buckets_last] : 0.0f;
+        for (int j0 = j_first; j0 < k1; j0 += kUnit) {
+            const int after = block_of(j0 + 2 * kUnit);
+            Tile next;
+            load(next, j0 + kUnit, id);
+            id = after;
+            const uint32_t there = tile.there;
+            f32x4 x[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                x[kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    u32x4 v = tile.k[kb][m];
+                    // (numbers past the row are others': zeros)
+                    if (VEC && D != a.D_k && (4 * m + kg) * E >= a.D_k) v = u32x4{0u, 0u, 0u, 0u};
+                    O::mma(x[kb], __builtin_bit_cast(F, v), q[m]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int s = 64 * i + lane, row = s / P, piece = s % P;
+                u32x4 v = tile.v[i];
+                if (VEC && D != a.D_v && piece * E >= a.D_v) v = u32x4{0u, 0u, 0u, 0u};
+                if (there != 0xffffffffu && !(there >> row & 1)) v = u32x4{0u, 0u, 0u, 0u};
+                *reinterpret_cast<u32x4*>(tv + place<ES, P>(row, piece)) = v;
+            }
+            if (a.bias && n - 1 - (j0 + kKeys - 1) < a.reach) {  // the tile's last key
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        int far_by = n - 1 - (j0 + 16 * kb + 4 * kg + i);
+                        far_by = far_by < 0 ? 0 : (far_by < a.reach ? far_by : a.reach);
+                        x[kb][i] = __builtin_fmaf(x[kb][i], scale, biases[(ln < nq ? ln : 0) * a.buckets + buckets[far_by]]);
                     }
-                }
-                O::mma(x[kb], __builtin_bit_cast(F, v), q[m]);
+            } else {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, far);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ok[kb][i] = __shfl((int)(at >= 0), 4 * kg + i) != 0;
-        }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int s = 64 * i + lane, row = s / P, piece = s % P, key = j0 + row, col = piece * E;
-            const int64_t at = key < k1 && col < a.D_v ? row_of_key(a, a.v, b, key, kv) : -1;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (at >= 0) {
-                const IO* p = (const IO*)a.v.p + at;
-                if constexpr (VEC) v = *reinterpret_cast<const u32x4*>(p + col);
-                else v = load_piece<IO>(p, col, a.D_v);
-            }
-            *reinterpret_cast<u32x4*>(tv + place<ES, P>(row, piece)) = v;
-        }
-        float mx = -kInf;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y = x[kb][i] * scale;
-                if (a.bias) {
-                    const int far = n - 1 - (j0 + 16 * kb + 4 * kg + i);
-                    const int at = map.of[far < 0 ? 0 : (far < a.reach ? far : a.reach)];
-                    y += kLog2e * (ln < nq ? (float)((const IO*)a.bias)[(int64_t)(head0 + ln) * a.buckets + at] : 0.0f);
-                }
-                x[kb][i] = ok[kb][i] ? y : -kInf;
-                mx = fmaxf(mx, x[kb][i]);
-            }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (__any(mx > top + att::kSlack<IO>)) {
-            const float now = mx > top + att::kSlack<IO> ? mx : top;
-            const float c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
-            top = now;
-            total *= c;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) acc[i] *= c;
-        }
-        const float m = (top == -kInf ? 0.0f : top) - att::kShift<IO>;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[kb][i] = __builtin_amdgcn_exp2f(x[kb][i] - m);
-                total += x[kb][i];
-            }
-        // (the wave's own tile: its writes are there once they are waited for)
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if constexpr (ES == 2) {
-            const u32x4 u = {Half<IO>::pack2(x[0][0], x[0][1]), Half<IO>::pack2(x[0][2], x[0][3]),
-                             Half<IO>::pack2(x[1][0], x[1][1]), Half<IO>::pack2(x[1][2], x[1][3])};
-            const F p = __builtin_bit_cast(F, u);
-            const int row = 4 * kg + (ln >> 2);
-#pragma unroll
-            for (int cb = 0; cb < NB; ++cb) {
-                const int piece = 2 * cb + ((lane & 3) >> 1), in = (lane & 1) * 8;
-                O::mma(acc[cb], O::column(tv + place<ES, P>(row, piece) + in, tv + place<ES, P>(row + 16, piece) + in), p);
-            }
-        } else {
+            float mx = -kInf;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int cb = 0; cb < NB; ++cb) {
-                    F v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = *reinterpret_cast<const float*>(tv + place<ES, P>(16 * kb + 4 * kg + e, 4 * cb + (ln >> 2)) + (ln & 3) * 4);
-                    O::mma(acc[cb], v, x[kb]);
+                for (int i = 0; i < 4; ++i) {
+                    if (there != 0xffffffffu && !(there >> (16 * kb + 4 * kg + i) & 1)) x[kb][i] = -kInf;
+                    mx = fmaxf(mx, x[kb][i]);
                 }
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            if (__any(mx > top + att::kSlack<IO>)) {
+                const float now = mx > top + att::kSlack<IO> ? mx : top;
+                const float c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+                top = now;
+                total *= c;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) acc[i] *= c;
+            }
+            const float m = (top == -kInf ? 0.0f : top) - att::kShift<IO>;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[kb][i] = __builtin_amdgcn_exp2f(x[kb][i] - m);
+                    total += x[kb][i];
+                }
+            // (the wave's own tile: its LDS instructions come in order)
+            asm volatile("" ::: "memory");
+            if constexpr (ES == 2) {
+                const u32x4 u = {Half<IO>::pack2(x[0][0], x[0][1]), Half<IO>::pack2(x[0][2], x[0][3]),
+                                 Half<IO>::pack2(x[1][0], x[1][1]), Half<IO>::pack2(x[1][2], x[1][3])};
+                const F p = __builtin_bit_cast(F, u);
+                const int row = 4 * kg + (ln >> 2);
+#pragma unroll
+                for (int cb = 0; cb < NB; ++cb) {
+                    const int piece = 2 * cb + ((lane & 3) >> 1), in = (lane & 1) * 8;
+                    O::mma(acc[cb], O::column(tv + place<ES, P>(row, piece) + in, tv + place<ES, P>(row + 16, piece) + in), p);
+                }
+            } else {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int cb = 0; cb < NB; ++cb) {
+                        F v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = *reinterpret_cast<const float*>(tv + place<ES, P>(16 * kb + 4 * kg + e, 4 * cb + (ln >> 2)) +
+                                                                   (ln & 3) * 4);
+                        O::mma(acc[cb], v, x[kb]);
+                    }
+            }
+            asm volatile("" ::: "memory");
+            tile = next;
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
-    total += __shfl_xor(total, 16);
-    total += __shfl_xor(total, 32);
-    if (kg == 0) ms[wave][ln] = top, ls[wave][ln] = total;
-    __syncthreads();
-    float all = -kInf;
+        total += __shfl_xor(total, 16);
+        total += __shfl_xor(total, 32);
+        if (kg == 0) ms[wave][ln] = top, ls[wave][ln] = total;
+        __syncthreads();
+        float all = -kInf;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) all = fmaxf(all, ms[w][ln]);
-    float sum = 0.0f;
+        for (int w = 0; w < 4; ++w) all = fmaxf(all, ms[w][ln]);
+        float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float t = ms[w][ln];
-        // (a wave whose scores were all NaN has no maximum but a sum)
-        sum += ls[w][ln] * (t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all));
-    }
-    const float c = top == all || top == -kInf ? 1.0f : __builtin_amdgcn_exp2f(top - all);
-    // each wave's sums to LDS (its own tile, which nobody else reads), then joined in order
-    float* const mine = reinterpret_cast<float*>(lds[wave]);
-    constexpr int kRow = kKeys * P * 16 / 4 / kQueries;  // floats of a query's row: D (16 bit) or 2 D
-    static_assert(kRow >= D, "a wave's tile holds its sums");
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mine[ln * kRow + 16 * i + 4 * kg + e] = c * acc[i][e];
-    if (tid < kQueries) all_top[tid] = all, all_sum[tid] = sum;  // (lane ln of wave 0)
-    __syncthreads();
-    const int nr = r < kQueries ? r : kQueries;
-    for (int e = tid; e < nq * a.D_v; e += 256) {
-        const int h = e / a.D_v, d = e - h * a.D_v;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) v += reinterpret_cast<const float*>(lds[w])[h * kRow + d];
-        if (g.splits == 1) {
-            const float s = all_sum[h];
-            ((IO*)const_cast<void*>(a.o.p))[b * a.o.ts + (int64_t)(head0 + h) * a.o.hs + d] = (IO)(s == 0.0f ? 0.0f : v / s);
-        } else {
-            ws[((int64_t)wg * nr + h) * (a.D_v + 2) + 2 + d] = v;
+        for (int w = 0; w < 4; ++w) {
+            const float t = ms[w][ln];
+            // (a wave whose scores were all NaN has no maximum but a sum)
+            sum += ls[w][ln] * (t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all));
         }
-    }
-    if (tid < nq) {
-        const float s = all_sum[tid], t = all_top[tid];
-        if (g.splits > 1) {
-            float* p = ws + ((int64_t)wg * nr + tid) * (a.D_v + 2);
-            p[0] = t, p[1] = s;
-        } else if (a.lse) {
-            a.lse[(int64_t)(head0 + tid) * a.batch + b] =
-                s == 0.0f ? -kInf : ((t == -kInf ? 0.0f : t) - att::kShift<IO> + __builtin_amdgcn_logf(s)) * kLn2;
+        const float c = top == all || top == -kInf ? 1.0f : __builtin_amdgcn_exp2f(top - all);
+        // each wave's sums to LDS (its own tile, which nobody else reads), then joined in order
+        float* const mine = reinterpret_cast<float*>(lds[wave]);
+        constexpr int kRow = kKeys * P * 16 / 4 / kQueries;  // floats of a query's row: D (16 bit) or 2 D
+        static_assert(kRow >= D, "a wave's tile holds its sums");
+#pragma unroll
+        for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(mine + ln * kRow + 16 * i + 4 * kg) = acc[i] * c;
+        if (tid < kQueries) all_top[tid] = all, all_sum[tid] = sum;  // (lane ln of wave 0)
+        __syncthreads();
+        const bool whole = starts && ends;
+        float* const part = parts + (int64_t)(2 * wg + (starts ? 1 : 0)) * nr * (a.D_v + 2);
+        for (int e = tid; e < nq * a.D_v; e += 256) {
+            const int h = e / a.D_v, d = e - h * a.D_v;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v += reinterpret_cast<const float*>(lds[w])[h * kRow + d];
+            if (whole) {
+                const float s = all_sum[h];
+                ((IO*)const_cast<void*>(a.o.p))[b * a.o.ts + (int64_t)(head0 + h) * a.o.hs + d] = (IO)(s == 0.0f ? 0.0f : v / s);
+            } else {
+                part[h * (a.D_v + 2) + 2 + d] = v;
+            }
         }
+        if (tid < nq) {
+            const float s = all_sum[tid], t = all_top[tid];
+            if (!whole) part[tid * (a.D_v + 2)] = t, part[tid * (a.D_v + 2) + 1] = s;
+            else if (a.lse)
+                a.lse[(int64_t)(head0 + tid) * a.batch + b] =
+                    s == 0.0f ? -kInf : ((t == -kInf ? 0.0f : t) - att::kShift<IO> + __builtin_amdgcn_logf(s)) * kLn2;
+        }
+        __syncthreads();
     }
 }
 
-// Joins the splits of one (sequence, head): a wave each.
+// Joins the parts of one (sequence, head): a wave each.
 template <typename IO>
-__global__ __launch_bounds__(256) void join_kernel(StepArgs a, Grid g, const float* ws, uint32_t base) {
+__global__ __launch_bounds__(256) void join_kernel(StepArgs a, Grid g, const float* ws) {
     const int lane = (int)threadIdx.x & 63;
-    const int64_t id = ((int64_t)blockIdx.x + base) * 4 + (threadIdx.x >> 6);
+    const int id = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
     if (id >= a.batch * a.heads) return;
-    const int64_t b = id / a.heads;
-    const int head = (int)(id - b * a.heads), r = a.heads / a.kv_heads, kv = head / r, group = (head - kv * r) / kQueries;
-    const int h = head - kv * r - group * kQueries, nr = r < kQueries ? r : kQueries;
-    const int n = length_of(a, b);
-    const float* p = ws + (((b * a.kv_heads + kv) * g.groups + group) * g.splits * nr + h) * (a.D_v + 2);
+    const int b = id / a.heads, head = id - b * a.heads, r = a.heads / a.kv_heads, kv = head / r;
+    const int group = (head - kv * r) / kQueries, h = head - kv * r - group * kQueries, nr = r < kQueries ? r : kQueries;
+    const int* const before = reinterpret_cast<const int*>(ws);
+    const Cut cut((int64_t)before[a.batch] * g.items, g.wgs);
+    const int64_t of = before[b + 1] - before[b];
+    const int64_t u = (int64_t)before[b] * g.items + (kv * g.groups + group) * of;
+    const int64_t w0 = cut.owner(u), w1 = cut.owner(u + of - 1);
+    if (w0 == w1) return;  // finished there
+    const float* const parts = ws + (a.batch + 1 + 63) / 64 * 64;
     const int64_t step = (int64_t)nr * (a.D_v + 2);
-    int used = 0;
-    for (int s = 0, k0, k1; s < g.splits; ++s) {
-        keys_of(n, g.splits, s, k0, k1);
-        if (k0 < k1 || (s == 0 && n == 0)) used = s + 1;
-    }
+    const float* p = parts + h * (a.D_v + 2);
+    auto at = [&](int64_t w) { return p + (2 * w + (w == w0 ? 1 : 0)) * step; };
     float all = -kInf, sum = 0.0f;
-    for (int s = 0; s < used; ++s) all = fmaxf(all, p[s * step]);
+    for (int64_t w = w0 + lane; w <= w1; w += 64) all = fmaxf(all, at(w)[0]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) all = fmaxf(all, __shfl_xor(all, o));
     float v0 = 0.0f, v1 = 0.0f;
-    for (int s = 0; s < used; ++s) {
-        const float t = p[s * step], c = t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all);
-        sum += c * p[s * step + 1];
-        if (lane < a.D_v) v0 += c * p[s * step + 2 + lane];
-        if (lane + 64 < a.D_v) v1 += c * p[s * step + 2 + lane + 64];
+#pragma unroll 4
+    for (int64_t w = w0; w <= w1; ++w) {
+        const float* const x = at(w);
+        const float t = x[0], c = t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all);
+        sum += c * x[1];
+        v0 += c * (lane < a.D_v ? x[2 + lane] : 0.0f);
+        v1 += c * (lane + 64 < a.D_v ? x[2 + lane + 64] : 0.0f);
     }
     IO* o = (IO*)const_cast<void*>(a.o.p) + b * a.o.ts + (int64_t)head * a.o.hs;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -269,19 +401,20 @@ __global__ __launch_bounds__(256) void join_kernel(StepArgs a, Grid g, const flo
 template <typename IO, int DB, bool VEC>
 hipError_t run_cfg(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t stream) {
     const Grid g = grid_for(a.heads, a.kv_heads, a.batch);
-    in_pieces(a.batch * a.kv_heads * g.groups * g.splits, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((step_kernel<IO, DB, VEC>), dim3(wgs), dim3(256), 0, stream, a, map, g, ws, base);
+    const size_t lds = (g.shared ? (size_t)(a.batch + 1) * 4 : 0) + (a.bias ? (size_t)kQueries * a.buckets * 4 + a.reach + 1 : 0);
+    in_pieces(g.wgs, 256, [&](uint32_t base, uint32_t wgs) {
+        hipLaunchKernelGGL((step_kernel<IO, DB, VEC>), dim3(wgs), dim3(256), lds, stream, a, map, g, ws, base);
     });
-    if (g.splits > 1)
-        in_pieces((a.batch * a.heads + 3) / 4, 256, [&](uint32_t base, uint32_t wgs) {
-            hipLaunchKernelGGL((join_kernel<IO>), dim3(wgs), dim3(256), 0, stream, a, g, ws, base);
-        });
+    if (g.shared)
+        hipLaunchKernelGGL((join_kernel<IO>), dim3((uint32_t)((a.batch * a.heads + 3) / 4)), dim3(256), 0, stream, a, g, ws);
     return hipGetLastError();
 }
 
 template <typename IO>
-hipError_t run(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t stream) {
+hipError_t run(StepArgs a, const BucketMap& map, float* ws, hipStream_t stream) {
     const size_t es = sizeof(IO);
+    a.q_vec = vec_ok(a.q, a.D_k, es, 16);
+    a.buckets_last = a.buckets ? map.of[a.reach] : 0;
     auto vec = [&](const Pages& x, int D) {
         return (uintptr_t)x.p % 16 == 0 && x.bs * es % 16 == 0 && x.ts * es % 16 == 0 && x.hs * es % 16 == 0 && D * es % 16 == 0;
     };
@@ -297,11 +430,12 @@ hipError_t run(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t s
 
 }  // namespace
 
+// Units before each sequence, and two parts of every workgroup.
 size_t attention_step_workspace(int heads, int kv_heads, int D_v, int64_t batch) {
     if (batch <= 0) return 0;
     const Grid g = grid_for(heads, kv_heads, batch);
     const int r = heads / kv_heads, nr = r < kQueries ? r : kQueries;
-    return g.splits == 1 ? 0 : (size_t)batch * kv_heads * g.groups * g.splits * nr * (D_v + 2) * 4;
+    return g.shared ? ((size_t)(batch + 1 + 63) / 64 * 64 + (size_t)2 * g.wgs * nr * (D_v + 2)) * 4 : 0;
 }
 
 hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream) {
