@@ -22,6 +22,7 @@ namespace att {
 using namespace tile;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) float lds_float;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;  // rows that a workgroup's four waves own
@@ -114,39 +115,44 @@ struct ColumnFrags {
     }
 };
 
-// Number (row, d) of a tile.
-template <class C, typename IO>
-__device__ __forceinline__ float element(const char* tile, int row, int d) {
-    return (float)*reinterpret_cast<const IO*>(tile + place<C::ES, C::P>(row, d / C::E) + d % C::E * C::ES);
-}
-
-// What the products with finite operands left out: acc[d] += p_row x[row][d] for the
-// infinities and NaN of a tile of 64 rows, for those rows lo .. hi that the lane's own
-// row sees (and those alone: their p of 0 is no probability).
-template <class C, typename IO, int NB>
-__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, const f32x16 (&p)[NB], int lo, int hi) {
+// What the products with finite operands left out of acc: the infinities and NaN of a tile's
+// `rows` rows.  (A product would spread those in unseen rows as well: 0 times infinity.)  A
+// lane's row sees rows 0 .. lim, or (SUFFIX) lim and later, so a column's first (last) such
+// number decides: +infinity or NaN in `found`, -infinity or NaN behind it.  nan: any is a NaN at
+// once (it multiplies factors that may be 0).  Rare, and held to few registers.
+template <class C, typename IO, bool SUFFIX>
+__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, int rows, int lim, bool nan, int* found) {
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
-    for (int row = 0; row < 32 * NB; ++row) {
-        bool odd = false;
-        for (int d = lane; d < C::D; d += 64) odd |= !(fabsf(element<C, IO>(tile, row, d)) < kInf);
-        if (!__any(odd)) continue;
-        const int at = (row >> 5) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
-        float mine = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mine = at == 16 * b + i ? p[b][i] : mine;
-        const float other = __shfl_xor(mine, 32);
-        const float w = h == ((row >> 2) & 1) ? mine : other;
-        if (row < lo || row > hi) continue;
-#pragma unroll
-        for (int cb = 0; cb < C::DB; ++cb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = element<C, IO>(tile, row, 32 * cb + row_of(i) + 4 * h);
-                if (!(fabsf(x) < kInf)) acc[cb][i] += w * x;
-            }
+    constexpr int none = SUFFIX ? -0x7fffffff : 0x7fffffff;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll 1
+    for (int d = lane; d < C::D; d += 64) {
+        int pos = none, neg = none;
+#pragma unroll 1
+        for (int k = 0; k < rows; ++k) {
+            const int row = SUFFIX ? k : rows - 1 - k;
+            const float x = (float)*reinterpret_cast<const IO*>(tile + place<C::ES, C::P>(row, d / C::E) + d % C::E * C::ES);
+            if (fabsf(x) < kInf) continue;
+            if (nan || !(x < 0.0f)) pos = row;
+            if (nan || !(x > 0.0f)) neg = row;
+        }
+        found[d] = pos, found[C::D + d] = neg;
     }
+    // (the wave's own numbers: its LDS instructions come in order)
+#pragma unroll
+    for (int cb = 0; cb < C::DB; ++cb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            asm volatile("" ::: "memory");
+            const i32x4 p = *reinterpret_cast<const i32x4*>(found + 32 * cb + 8 * g + 4 * h);
+            const i32x4 n = *reinterpret_cast<const i32x4*>(found + C::D + 32 * cb + 8 * g + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[cb][4 * g + e] += (SUFFIX ? p[e] >= lim : p[e] <= lim) ? kInf : 0.0f;
+                acc[cb][4 * g + e] += (SUFFIX ? n[e] >= lim : n[e] <= lim) ? -kInf : 0.0f;
+            }
+        }
+    asm volatile("" ::: "memory");
 }
 
 template <int N>
@@ -209,7 +215,7 @@ __device__ __forceinline__ void fill_biases(float* tab, const AttentionArgs& a, 
     const int off = a.reach + kPad;
     for (int x = (int)threadIdx.x; x <= 2 * off; x += 256) tab[x] = kLog2e * bias_of<IO>(a, map, head, x - off);
 }
-constexpr int kTab = 2 * (kMaxReach + kPad) + 1;
+__host__ __device__ constexpr int tab_width(int reach) { return 2 * (reach + kPad) + 1; }
 
 // Fragments of 32 rows from memory, the operand of the products over the head's numbers.
 template <class C, typename IO, typename F, bool VEC>
@@ -278,14 +284,73 @@ constexpr float kSlack = std::is_same_v<IO, _Float16> ? 3.0f : 8.0f;
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// 64 numbers of 4 bytes, one from each lane's offset in the resource, to LDS from `to` on.
+__device__ __forceinline__ void load_words_to_lds(const u32x4& rsrc, uint32_t offset, const float* to) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(offset), "s"(rsrc), "s"(at)
+                 : "memory");
+}
+
+// Two tiles, 64 rows each, pass through LDS; where both fit twice into half of it, the next
+// pair's loads are in flight behind the products of this one.
+template <class C>
+constexpr int kStages = 4 * C::TILE <= 80 * 1024 ? 2 : 1;
+
+// Visits n_a + n_b pairs of tiles: load(v, stage) of visit v, then, when its tiles are there,
+// a(v, stage) for the first n_a visits and b(v, stage) for the others.  Every wave calls it, and
+// a() and b() have no barrier.  (Two loops: work with and without masks in one, by a branch,
+// costs half as many registers again.)
+template <class C, typename L, typename A, typename B>
+__device__ __forceinline__ void pass_over(int n_a, int n_b, L&& load, A&& a, B&& b) {
+    const int n = n_a + n_b;
+    int stage = 0;
+    auto next = [&](int v) {
+        if constexpr (kStages<C> == 2) {
+            wait_loads();
+            __syncthreads();
+            if (v + 1 < n) load(v + 1, stage ^ 1);
+        } else {
+            __syncthreads();
+            load(v, 0);
+            wait_loads();
+            __syncthreads();
+        }
+    };
+    if constexpr (kStages<C> == 2) {
+        __syncthreads();
+        if (n > 0) load(0, 0);
+    }
+    int v = 0;
+    for (; v < n_a; ++v, stage ^= kStages<C> - 1) {
+        next(v);
+        a(v, stage);
+    }
+    for (; v < n; ++v, stage ^= kStages<C> - 1) {
+        next(v);
+        b(v, stage);
+    }
+}
+__device__ __forceinline__ int tiles(int rows) { return rows > 0 ? (rows + kTile - 1) / kTile : 0; }
+
+// Waves per SIMD that the registers are held to.
+constexpr int forward_waves(int es, int db) { return es == 4 ? (db <= 2 ? 2 : 1) : (db == 1 ? 4 : (db == 2 ? 3 : 2)); }
+constexpr int dq_waves(int es, int db) { return es == 4 ? (db <= 2 ? 2 : 1) : (db == 1 ? 4 : (db == 2 ? 3 : 2)); }
+constexpr int dkv_waves(int es, int db) { return es == 4 ? 2 : (db == 1 ? 3 : 2); }
+// Whether dk and dv are two launches, each with its own accumulators and the scores made twice:
+// both at once hold more numbers than 256 registers.
+constexpr bool dkv_apart(int es, int db) { return es == 4 ? db >= 2 : db >= 4; }
+
 // --- forward --------------------------------------------------------------------------
 template <typename IO, int DB, bool VEC, bool BIAS>
-__global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+__global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
-    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
-    __shared__ float tab[BIAS ? kTab : 1];
+    __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
+    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
+    extern __shared__ float tab[];  // [tab_width(reach)] with biases
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
     const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
@@ -297,56 +362,55 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
     if (row0 < 0 || row0 >= s.n_q) return;
     const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
     const int my = w0 + (lane & 31);
-    if constexpr (BIAS) fill_biases<IO>(tab, a, map, head);
 
     F q[C::NS];
     load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
+    if constexpr (BIAS) fill_biases<IO>(tab, a, map, head);
     f32x16 acc[DB];
     clear(acc);
     float top = -kInf, total = 0.0f;
     const float scale = a.scale * kLog2e;
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;  // last key that it sees
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
-    const int wave_all = a.causal && w0 + shift < s.n_k - 1 ? w0 + shift : s.n_k - 1;          // all its rows see
+    // keys that some of the workgroup's rows see; tiles that all of them do
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
+    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
-    char *const tk = lds, *const tv = lds + C::TILE;
-    const RowFrags<C> rows(tk);
-    const ColumnFrags<C, O> cols(tv);
-    for (int j0 = 0; j0 < end; j0 += kTile) {
-        __syncthreads();
-        const int n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
-        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, tk);
-        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, tv);
-        wait_loads();
-        __syncthreads();
-        if (n_rows <= 0 || j0 >= wave_end) continue;
-        const bool edge = j0 + kTile - 1 > wave_all;
+    const RowFrags<C> rows(lds[0]);
+    const ColumnFrags<C, O> cols(lds[0] + C::TILE);
+    // Keys j0 .. of the tiles at `by`.  EDGE: some that not every row sees.
+    auto tile = [&](auto edge, int j0, int by) __attribute__((always_inline)) {
+        constexpr bool EDGE = decltype(edge)::value;
         f32x16 x[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             x[kb] = f32x16{};
 #pragma unroll
-            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], rows.template get<F>(0, kb, st), q[st]);
+            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], rows.template get<F>(by, kb, st), q[st]);
         }
         if constexpr (BIAS) {
             const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
-            const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
             const float* t = tab + a.reach + kPad;
-            const float f = t[from > 0 ? a.reach : -a.reach];
-            t += from + (lane & 31) - 4 * h;
+            if (from - 63 >= a.reach || from + 31 <= -a.reach) {
+                const float f = t[from > 0 ? a.reach : -a.reach];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+                for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[kb][i] = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
+                    for (int i = 0; i < 16; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, f);
+            } else {
+                t += from + (lane & 31) - 4 * h;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, t[-(32 * kb + row_of(i))]);
+            }
         } else {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) x[kb] *= scale;
         }
-        if (edge) {
+        if constexpr (EDGE) {
             const int lim = last - j0 - 4 * h;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -369,15 +433,13 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
             for (int cb = 0; cb < DB; ++cb) acc[cb] *= c;
         }
         const float m = (top == -kInf ? 0.0f : top) - kShift<IO>;
-        float sum = 0.0f;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 x[kb][i] = __builtin_amdgcn_exp2f(x[kb][i] - m);
-                sum += x[kb][i];
+                total += x[kb][i];
             }
-        total += sum;
         uint32_t odd = 0;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -389,8 +451,8 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
                 const F p = O::pack(w);
 #pragma unroll
                 for (int cb = 0; cb < DB; ++cb) {
-                    F v[1] = {cols.get(0, kb, t, cb)};
-                    if (edge) {
+                    F v[1] = {cols.get(by, kb, t, cb)};
+                    if constexpr (EDGE) {
                         const uint32_t o = O::top(v);
                         odd = o > odd ? o : odd;
                         v[0] = O::finite(v[0]);
@@ -398,8 +460,21 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
                     O::mma(acc[cb], v[0], p);
                 }
             }
-        if (edge && __any(odd >= O::kInf)) add_odd_numbers<C, IO, 2>(acc, tv, x, 0, last - j0);
-    }
+        if (EDGE && __any(odd >= O::kInf)) add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by, kTile, last - j0, false, found[wave]);
+    };
+    pass_over<C>(
+        whole, tiles(end) - whole,
+        [&](int t, int stage) {
+            const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+            lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[stage]);
+            lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
+        },
+        [&](int t, int stage) {
+            if (n_rows > 0) tile(std::false_type{}, t * kTile, stage * 2 * C::TILE);
+        },
+        [&](int t, int stage) {
+            if (n_rows > 0 && t * kTile < wave_end) tile(std::true_type{}, t * kTile, stage * 2 * C::TILE);
+        });
     if (n_rows <= 0) return;
     total += __shfl_xor(total, 32);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
@@ -408,7 +483,6 @@ __global__ __launch_bounds__(256) void forward_kernel(AttentionArgs a, BucketMap
         a.lse[(int64_t)head * a.T + s.q0 + my] =
             total == 0.0f ? -kInf : ((top == -kInf ? 0.0f : top) - kShift<IO> + __builtin_amdgcn_logf(total)) * kLn2;
 }
-
 
 // --- backward -------------------------------------------------------------------------
 // fp16: takes the lane's sums to a scale that holds its numbers x, and returns x's.
@@ -432,25 +506,46 @@ __device__ __forceinline__ float hold(const f32x16 (&x)[N], float& f, f32x16 (&a
     return f;
 }
 
+// Sums of a block of 32 x 32 along its diagonals.  Accumulator i holds row r = row_of(i) (+ 4 h)
+// of all 32 columns; turned by r lanes, column c comes to lane c - r, or c - r + 32: the first
+// are added to `near` (distance: lane), the others to `wrap` (distance: lane - 32).
+__device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, float& wrap) {
+    const int lane = (int)threadIdx.x & 31;
+    static_for<0, 16>([&](auto ic) {
+        constexpr int i = decltype(ic)::value, r = row_of(i);
+        float v = x[i];
+        if constexpr (r != 0) {
+            // swizzle, rotate mode: lane l of each 32 reads lane (l + r) % 32
+            v = __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0xc000 | r << 5));
+            near += lane < 32 - r ? v : 0.0f;
+            wrap += lane < 32 - r ? 0.0f : v;
+        } else {
+            near += v;
+        }
+    });
+}
+
 // Gradients of q and, if wanted, of the biases: a wave owns 32 queries and passes over the
-// keys twice.  The first pass makes delta = sum P dP, as what do . o leaves of it: o is
+// keys twice.  The first pass makes delta = sum P dP, as what d_o . o leaves of it: o is
 // rounded to the plan's type, and delta from it alone is off by that rounding, which dS (a
 // difference) shows twofold and the biases' fp32 gradients by 1e-3 of their size.  It also
 // takes lse's own rounding out of P (sum P = 1), and leaves both for dkv_kernel.  The second
-// makes dS.  Of the biases, dS is summed by distance, each wave's halves in an array of their
-// own (the lanes of an instruction hold 32 distances apiece, all different, and a wave's
-// instructions come in order: the sums do not depend on timing); distances past the reach
-// share a bucket on either side and are summed in registers.  A workgroup writes the sums
+// makes dS.  Of the biases, dS is summed by distance: along the diagonals of a block in
+// registers, then into an array for each half of each wave (the lanes of an instruction hold 32
+// distances apiece, all different, and a wave's instructions come in order: the sums do not
+// depend on timing); distances past the reach share a bucket on either side and are summed
+// in registers.  (One LDS addition for each of a block's 16 accumulators instead of its diagonals
+// took the kernel from 140 to 370 us in packed training on images.)  A workgroup writes the sums
 // of its buckets; reduce_kernel joins those of a head.
 template <typename IO, int DB, bool VEC, bool BIAS>
-__global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+__global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
-    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
-    __shared__ float tab[BIAS ? kTab : 1];
+    __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
+    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
     __shared__ float far_sums[BIAS ? 8 : 1];
-    extern __shared__ float sums[];  // [8][2 (reach + kPad) + 1] with gradients of the biases
+    extern __shared__ float tab[];  // [width] with biases, [8][width] with their gradients
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
     const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
     const uint32_t slot = id % a.slots;
@@ -465,7 +560,8 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     if (idle) s.n_q = s.n_k = 0, row0 = 0;
     const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
     const int my = w0 + (lane & 31);
-    const int width = 2 * (a.reach + kPad) + 1;
+    const int width = tab_width(a.reach);
+    float* const sums = tab + width;
     if constexpr (BIAS) {
         fill_biases<IO>(tab, a, map, head);
         if (a.dbias)
@@ -495,59 +591,67 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     const float scale = a.scale * kLog2e;
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
-    const int wave_all = a.causal && w0 + shift < s.n_k - 1 ? w0 + shift : s.n_k - 1;
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
+    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
-    char *const tk = lds, *const tv = lds + C::TILE;
-    const RowFrags<C> krows(tk), vrows(tv);
-    const ColumnFrags<C, O> kcols(tk);
-    // One tile: probabilities and dP.  False: none of the wave's rows sees it.
-    auto scores = [&](int j0, f32x16 (&x)[2], f32x16 (&dp)[2], int from, bool far) {
-        __syncthreads();
-        const int n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
-        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, tk);
-        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, tv);
-        wait_loads();
-        __syncthreads();
-        if (n_rows <= 0 || j0 >= wave_end) return false;
+    const RowFrags<C> krows(lds[0]);  // (v's tile lies C::TILE behind k's)
+    const ColumnFrags<C, O> kcols(lds[0]);
+    auto load = [&](int t, int stage) {
+        const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[stage]);
+        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
+    };
+    // Probabilities and dP of 32 keys from j on, at block kb of the tiles at `by`.
+    auto scores = [&](f32x16& x, f32x16& dp, int j, int kb, int by) __attribute__((always_inline)) {
+        x = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st) O::mma(x, krows.template get<F>(by, kb, st), q[st]);
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st) O::mma(dp, krows.template get<F>(by + C::TILE, kb, st), d_o[st]);
+        if constexpr (BIAS) {
+            const int from = w0 + shift - j;  // distance of the wave's first row and the block's first key
+            const float* t = tab + a.reach + kPad;
+            if (from - 31 >= a.reach || from + 31 <= -a.reach) {
+                const float f = t[from > 0 ? a.reach : -a.reach];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, f);
+            } else {
+                t += from + (lane & 31) - 4 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[-row_of(i)]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(x[i] - lse);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -lse));
+        }
+    };
+    auto first = [&](bool edge, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            x[kb] = f32x16{}, dp[kb] = f32x16{};
+            const int j = t * kTile + 32 * kb;
+            if (n_rows <= 0 || j >= wave_end) return;
+            f32x16 x, dp;
+            scores(x, dp, j, kb, stage * 2 * C::TILE);
+            if (edge) {
+                const int lim = last - j - 4 * h;
 #pragma unroll
-            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], krows.template get<F>(0, kb, st), q[st]);
+                for (int i = 0; i < 16; ++i) {
+                    ones += row_of(i) <= lim ? x[i] : 0.0f;
+                    left += row_of(i) <= lim ? x[i] * (dp[i] - delta) : 0.0f;
+                }
+            } else {
 #pragma unroll
-            for (int st = 0; st < C::NS; ++st) O::mma(dp[kb], vrows.template get<F>(0, kb, st), d_o[st]);
+                for (int i = 0; i < 16; ++i) ones += x[i], left = __builtin_fmaf(x[i], dp[i] - delta, left);
+            }
         }
-        const float* t = tab + a.reach + kPad;
-        const float f = BIAS ? t[from > 0 ? a.reach : -a.reach] : 0.0f;
-        t += from + (lane & 31) - 4 * h;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float y = x[kb][i] * scale;
-                if constexpr (BIAS) y = __builtin_fmaf(x[kb][i], scale, far ? f : t[-(32 * kb + row_of(i))]);
-                x[kb][i] = __builtin_amdgcn_exp2f(y - lse);
-            }
-        return true;
     };
-    for (int j0 = 0; j0 < end; j0 += kTile) {
-        f32x16 x[2], dp[2];
-        const int from = w0 + shift - j0;
-        if (!scores(j0, x, dp, from, from - 63 >= a.reach || from + 31 <= -a.reach)) continue;
-        const bool edge = j0 + kTile - 1 > wave_all;
-        const int lim = last - j0 - 4 * h;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool seen = !edge || 32 * kb + row_of(i) <= lim;
-                ones += seen ? x[kb][i] : 0.0f;
-                left += seen ? x[kb][i] * (dp[kb][i] - delta) : 0.0f;
-            }
-    }
+    pass_over<C>(
+        whole, tiles(end) - whole, load, [&](int t, int stage) { first(false, t, stage); },
+        [&](int t, int stage) { first(true, t, stage); });
     ones += __shfl_xor(ones, 32);
     left += __shfl_xor(left, 32);
     if (ones != 0.0f) {
@@ -555,68 +659,64 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
         lse += __builtin_amdgcn_logf(ones);
     }
     if (real && h == 0) a.row_lse[row] = lse, a.row_delta[row] = delta;
-    for (int j0 = 0; j0 < end; j0 += kTile) {
-        f32x16 x[2], dp[2];
-        const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
-        const bool far = from - 63 >= a.reach || from + 31 <= -a.reach;
-        if (!scores(j0, x, dp, from, far)) continue;
-        const bool edge = j0 + kTile - 1 > wave_all;
+
+    auto block = [&](auto edge, int j, int kb, int by) __attribute__((always_inline)) {
+        constexpr bool EDGE = decltype(edge)::value;
+        f32x16 x[1], dp;
+        scores(x[0], dp, j, kb, by);
+        const int lim = last - j - 4 * h;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[kb][i] = x[kb][i] * (dp[kb][i] - delta);
-        if (edge) {
-            const int lim = last - j0 - 4 * h;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[kb][i] = 32 * kb + row_of(i) <= lim ? x[kb][i] : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            x[0][i] *= dp[i] - delta;
+            if constexpr (EDGE) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
         }
         if constexpr (BIAS) {
-            if (a.dbias && far) {
+            const int from = w0 + shift - j;
+            if (a.dbias && (from - 31 >= a.reach || from + 31 <= -a.reach)) {
                 float t = 0.0f;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) t += x[kb][i];
+                for (int i = 0; i < 16; ++i) t += x[0][i];
                 if (from > 0) far_pos += t;
                 else far_neg += t;
             } else if (a.dbias) {
-                float* const t = sums + (2 * wave + h) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        __hip_atomic_fetch_add(t - (32 * kb + row_of(i)), x[kb][i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                float near = 0.0f, wrap = 0.0f;
+                add_diagonals(x[0], near, wrap);
+                lds_float* const t = (lds_float*)tab + (2 * wave + h + 1) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
+                __hip_atomic_fetch_add(t, near, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                __hip_atomic_fetch_add(t - 32, wrap, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
             }
         }
         const float f = hold<IO>(x, held, acc);
-        if constexpr (std::is_same_v<IO, _Float16>) {
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) x[kb] *= f;
-        }
+        if constexpr (std::is_same_v<IO, _Float16>) x[0] *= f;
         uint32_t odd = 0;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int t = 0; t < C::NT; ++t) {
+            float w[C::E];
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t) {
-                float w[C::E];
+            for (int e = 0; e < C::E; ++e) w[e] = x[0][t * C::E + e];
+            const F p = O::pack(w);
 #pragma unroll
-                for (int e = 0; e < C::E; ++e) w[e] = x[kb][t * C::E + e];
-                const F p = O::pack(w);
-#pragma unroll
-                for (int cb = 0; cb < DB; ++cb) {
-                    F k[1] = {kcols.get(0, kb, t, cb)};
-                    if (edge) {
-                        const uint32_t o = O::top(k);
-                        odd = o > odd ? o : odd;
-                        k[0] = O::finite(k[0]);
-                    }
-                    O::mma(acc[cb], k[0], p);
+            for (int cb = 0; cb < DB; ++cb) {
+                F k[1] = {kcols.get(by, kb, t, cb)};
+                if constexpr (EDGE) {
+                    const uint32_t o = O::top(k);
+                    odd = o > odd ? o : odd;
+                    k[0] = O::finite(k[0]);
                 }
+                O::mma(acc[cb], k[0], p);
             }
-        if (edge && __any(odd >= O::kInf)) add_odd_numbers<C, IO, 2>(acc, tk, x, 0, last - j0);
-    }
+        }
+        if (EDGE && __any(odd >= O::kInf)) 
+            add_odd_numbers<C, IO, false>(acc, lds[0] + by + kb * (32 * C::P * 16), 32, last - j, true, found[wave]);
+    };
+    auto second = [&](auto edge, int t, int stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (n_rows > 0 && t * kTile + 32 * kb < wave_end) block(edge, t * kTile + 32 * kb, kb, stage * 2 * C::TILE);
+    };
+    pass_over<C>(
+        whole, tiles(end) - whole, load, [&](int t, int stage) { second(std::false_type{}, t, stage); },
+        [&](int t, int stage) { second(std::true_type{}, t, stage); });
     if (n_rows > 0) {
         const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
         store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
@@ -661,16 +761,17 @@ __global__ __launch_bounds__(256) void dq_kernel(AttentionArgs a, BucketMap map,
     }
 }
 
-// Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the queries of
-// every head that shares it, in a fixed order.
-template <typename IO, int DB, bool VEC, bool BIAS>
-__global__ __launch_bounds__(256) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+// Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the
+// queries of every head that shares it, in a fixed order; DK and DV: which of the two.
+template <typename IO, int DB, bool VEC, bool BIAS, bool DK, bool DV>
+__global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
-    __shared__ __attribute__((aligned(16))) char lds[2 * C::TILE];
-    __shared__ float tab[BIAS ? kTab : 1];
-    __shared__ __attribute__((aligned(16))) float stats[2][kTile];
+    __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
+    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
+    __shared__ __attribute__((aligned(16))) float stats[kStages<C>][2][kTile];  // lse, delta
+    extern __shared__ float tab[];
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
     const int kv = (int)(id / a.kv_slots), r = a.heads / a.kv_heads;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
@@ -685,123 +786,157 @@ __global__ __launch_bounds__(256) void dkv_kernel(AttentionArgs a, BucketMap map
 
     F k[C::NS], v[C::NS];
     load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
-    load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
+    if constexpr (DK) load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
     f32x16 dk[DB], dv[DB];
     clear(dk), clear(dv);
     float held = kTopScale;
     const float scale = a.scale * kLog2e;
-    const int i_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile * kTile : 0;
+    // Tiles of queries from the first that sees one of the workgroup's keys; visited first are
+    // the last, if it is not whole, and those that do not see all its keys.
+    const int t_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile : 0;
+    const int t_all = a.causal && (int)row0 + kRows - 1 - shift > 0 ? tiles((int)row0 + kRows - 1 - shift) : 0;
+    const int t_whole = s.n_q / kTile, tail = s.n_q % kTile && t_first <= t_whole ? 1 : 0;
+    const int t_edge = t_all < t_whole ? (t_all > t_first ? t_all : t_first) : t_whole;  // edge tiles: t_first .. t_edge - 1
+    const int n_edge = tail + (t_edge > t_first ? t_edge - t_first : 0), n_whole = t_whole > t_edge ? t_whole - t_edge : 0;
+    auto row_at = [&](int t) { return (tail && t == 0 ? t_whole : t_first + t - tail) * kTile; };
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lq(a.q, a.D_k, 0, wave, 4), lg(a.d_o, a.D_v, 0, wave, 4);
-    char *const tq = lds, *const tg = lds + C::TILE;
-    const RowFrags<C> qrows(tq), grows(tg);
-    const ColumnFrags<C, O> qcols(tq), gcols(tg);
+    const RowFrags<C> qrows(lds[0]);  // (d_o's tile lies C::TILE behind q's)
+    const ColumnFrags<C, O> qcols(lds[0]);
+    // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  EDGE: not all of them see all keys, or
+    // fewer than 32 are left.
+    auto block = [&](auto edge, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
+        constexpr bool EDGE = decltype(edge)::value;
+        const int low = a.causal ? my - shift - q0 : 0, high = s.n_q - 1 - q0;  // rows of the block that see the lane's key
+        f32x16 x = {}, dp = {}, p[1], ds[1];
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st) O::mma(x, qrows.template get<F>(by, qb, st), k[st]);
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st)
+            if constexpr (DK) O::mma(dp, qrows.template get<F>(by + C::TILE, qb, st), v[st]);
+        if constexpr (BIAS) {
+            const int from = q0 + shift - w0;  // distance of the block's first row and the wave's first key
+            const float* t = tab + a.reach + kPad;
+            if (from - 31 >= a.reach || from + 31 <= -a.reach) {
+                const float f = t[from > 0 ? a.reach : -a.reach];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, f);
+            } else {
+                t += from - (lane & 31) + 4 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[row_of(i)]);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[0][32 * qb + 8 * g + 4 * h]);
+            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * g + e, at = row_of(i) + 4 * h;
+                const float y = BIAS ? x[i] - lse[e] : __builtin_fmaf(x[i], scale, -lse[e]);
+                p[0][i] = __builtin_amdgcn_exp2f(y);
+                if constexpr (DK) ds[0][i] = p[0][i] * (dp[i] - delta[e]);
+                if constexpr (EDGE) {
+                    const bool seen = at >= low && at <= high;
+                    p[0][i] = seen ? p[0][i] : 0.0f;
+                    if constexpr (DK) ds[0][i] = seen ? ds[0][i] : 0.0f;
+                }
+            }
+        }
+        if constexpr (DK && std::is_same_v<IO, _Float16>) ds[0] *= hold<IO>(ds, held, dk);
+        if constexpr (DV && std::is_same_v<IO, _Float16>) p[0] *= 4096.0f;
+        uint32_t odd = 0;
+        // column frags of the tile at `at` (finite, where it matters) times numbers w
+        auto product = [&](f32x16 (&acc)[DB], int at, const f32x16& w) __attribute__((always_inline)) {
+#pragma unroll
+            for (int st = 0; st < C::NT; ++st) {
+                float u[C::E];
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) u[e] = w[st * C::E + e];
+                const F f = O::pack(u);
+#pragma unroll
+                for (int cb = 0; cb < DB; ++cb) {
+                    F g[1] = {qcols.get(at, qb, st, cb)};
+                    if constexpr (EDGE) {
+                        const uint32_t o = O::top(g);
+                        odd = o > odd ? o : odd;
+                        g[0] = O::finite(g[0]);
+                    }
+                    O::mma(acc[cb], g[0], f);
+                }
+            }
+        };
+        if constexpr (DV) product(dv, by + C::TILE, p[0]);
+        if constexpr (DK) product(dk, by, ds[0]);
+        if (EDGE && __any(odd >= O::kInf)) {
+            const char* t = lds[0] + by + qb * (32 * C::P * 16);
+            if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave]);
+            if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave]);
+        }
+    };
     for (int hh = 0; hh < r; ++hh) {
         const int head = kv * r + hh;
         if constexpr (BIAS) {
             __syncthreads();
             fill_biases<IO>(tab, a, map, head);
         }
-        for (int i0 = i_first; i0 < s.n_q; i0 += kTile) {
-            __syncthreads();
-            const int n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
-            lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, tq);
-            lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, tg);
-            if (tid < 2 * kTile) {
-                const int i = tid % kTile;
-                const int64_t at = (int64_t)head * a.T + s.q0 + i0 + i;
-                stats[tid / kTile][i] = tid < kTile ? (i < n ? a.row_lse[at] : kInf) : (i < n ? a.row_delta[at] : 0.0f);
-            }
-            wait_loads();
-            __syncthreads();
-            if (n_rows <= 0 || (a.causal && i0 + kTile - 1 + shift < w0)) continue;
-            const bool edge = a.causal && i0 + shift < w0 + 31;
-            const int low = my - shift - i0;  // first row of the tile that sees the lane's key
-            const int from = i0 + shift - w0;  // distance of the tile's first row and the wave's first key
-            const bool far = from - 31 >= a.reach || from + 63 <= -a.reach;
-            const float* t = tab + a.reach + kPad;
-            const float f = BIAS ? t[from > 0 ? a.reach : -a.reach] : 0.0f;
-            t += from - (lane & 31) + 4 * h;
-            uint32_t odd = 0;
-            f32x16 p[2], ds[2];
-#pragma unroll
-            for (int qb = 0; qb < 2; ++qb) {
-                f32x16 x = {}, dp = {};
-#pragma unroll
-                for (int st = 0; st < C::NS; ++st) O::mma(x, qrows.template get<F>(0, qb, st), k[st]);
-#pragma unroll
-                for (int st = 0; st < C::NS; ++st) O::mma(dp, grows.template get<F>(0, qb, st), v[st]);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[0][32 * qb + 8 * g + 4 * h]);
-                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[1][32 * qb + 8 * g + 4 * h]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 4 * g + e, at = 32 * qb + row_of(i);
-                        float y = x[i] * scale;
-                        if constexpr (BIAS) y = __builtin_fmaf(x[i], scale, far ? f : t[at]);
-                        const float w = __builtin_amdgcn_exp2f(y - lse[e]);
-                        const bool seen = !edge || at + 4 * h >= low;
-                        p[qb][i] = seen ? w : 0.0f;
-                        ds[qb][i] = seen ? w * (dp[i] - delta[e]) : 0.0f;
-                    }
+        pass_over<C>(
+            n_edge, n_whole,
+            [&](int t, int stage) {
+                const int i0 = row_at(t), n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
+                lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
+                lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
+                if (wave < 2) {
+                    const float* from = (wave ? a.row_delta : a.row_lse) + (int64_t)head * a.T + s.q0 + i0;
+                    load_words_to_lds(resource(from, (uint32_t)n * 4), (uint32_t)lane * 4, stats[stage][wave]);
                 }
-            }
-            const float f16 = hold<IO>(ds, held, dk);
-            if constexpr (std::is_same_v<IO, _Float16>) {
+            },
+            [&](int t, int stage) {
 #pragma unroll
-                for (int qb = 0; qb < 2; ++qb) ds[qb] *= f16, p[qb] *= 4096.0f;
-            }
-#pragma unroll
-            for (int qb = 0; qb < 2; ++qb)
-#pragma unroll
-                for (int st = 0; st < C::NT; ++st) {
-                    float w[C::E], u[C::E];
-#pragma unroll
-                    for (int e = 0; e < C::E; ++e) w[e] = p[qb][st * C::E + e], u[e] = ds[qb][st * C::E + e];
-                    const F pf = O::pack(w), df = O::pack(u);
-#pragma unroll
-                    for (int cb = 0; cb < DB; ++cb) {
-                        F g[2] = {gcols.get(0, qb, st, cb), qcols.get(0, qb, st, cb)};
-                        if (edge) {
-                            const uint32_t o = O::top(g);
-                            odd = o > odd ? o : odd;
-                            g[0] = O::finite(g[0]), g[1] = O::finite(g[1]);
-                        }
-                        O::mma(dv[cb], g[0], pf);
-                        O::mma(dk[cb], g[1], df);
-                    }
+                for (int qb = 0; qb < 2; ++qb) {
+                    const int q0 = row_at(t) + 32 * qb;
+                    if (n_rows > 0 && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
+                        block(std::true_type{}, q0, qb, stage * 2 * C::TILE, stats[stage]);
                 }
-            if (edge && __any(odd >= O::kInf)) {
-                add_odd_numbers<C, IO, 2>(dv, tg, p, low, n - 1);
-                add_odd_numbers<C, IO, 2>(dk, tq, ds, low, n - 1);
-            }
-        }
+            },
+            [&](int t, int stage) {
+#pragma unroll
+                for (int qb = 0; qb < 2; ++qb)
+                    if (n_rows > 0) block(std::false_type{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
+            });
     }
     if (n_rows <= 0) return;
     const bool half = std::is_same_v<IO, _Float16>;
-    store_rows<C, IO>(dk, a.dk, s.k0 + w0, kv, n_rows, a.D_k, half ? a.scale * inverse_of_power(held) : a.scale, a.dk_vec);
-    store_rows<C, IO>(dv, a.dv, s.k0 + w0, kv, n_rows, a.D_v, half ? 1.0f / 4096.0f : 1.0f, a.dv_vec);
+    if constexpr (DK)
+        store_rows<C, IO>(dk, a.dk, s.k0 + w0, kv, n_rows, a.D_k, half ? a.scale * inverse_of_power(held) : a.scale, a.dk_vec);
+    if constexpr (DV) store_rows<C, IO>(dv, a.dv, s.k0 + w0, kv, n_rows, a.D_v, half ? 1.0f / 4096.0f : 1.0f, a.dv_vec);
 }
 
 // --- host side ------------------------------------------------------------------------
 template <typename IO, int DB, bool VEC, bool BIAS>
 hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
+    const size_t table = BIAS ? tab_width(a.reach) * 4 : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
+        hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), table, stream, a, map, base);
     });
     return hipGetLastError();
 }
 
 template <typename IO, int DB, bool VEC, bool BIAS>
 hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
-    const size_t sums = BIAS && a.dbias ? (size_t)8 * (2 * (a.reach + kPad) + 1) * 4 : 0;
+    const size_t table = BIAS ? tab_width(a.reach) * 4 : 0, sums = a.dbias ? 8 * table : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), sums, stream, a, map, base);
+        hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
     });
     in_pieces((int64_t)a.kv_slots * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), 0, stream, a, map, base);
+        if constexpr (dkv_apart(sizeof(IO), DB)) {
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, true, false>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, false, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+        } else {
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, true, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+        }
     });
     return hipGetLastError();
 }

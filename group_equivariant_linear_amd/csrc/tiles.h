@@ -184,8 +184,8 @@ __device__ __forceinline__ void lds_barrier() {
 
 // 64 pieces of 16 bytes, one from each lane's offset in the resource, to LDS from `to` on.
 __device__ __forceinline__ void load_to_lds(const u32x4& rsrc, uint32_t offset, const char* to) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to);
+    // (the low half of a generic LDS address is the address in LDS)
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(offset), "s"(rsrc), "s"(at)
