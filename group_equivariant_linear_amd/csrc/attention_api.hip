@@ -226,7 +226,7 @@ eqlinear_status eqlinear_attention_backward(eqlinear_plan_t p, const eqlinear_he
 
 size_t eqlinear_attention_step_workspace(eqlinear_plan_t p, int64_t batch) {
     if (!p || p->kind != EQL_KIND_ATTENTION || batch < 0 || batch > 0x7fffffff) return 0;
-    return attention_step_workspace(p->heads, p->kv_heads, p->d_v * p->N, batch);
+    return attention_step_workspace(p->dtype, p->heads, p->kv_heads, p->d_k * p->N, p->d_v * p->N, batch);
 }
 
 eqlinear_status eqlinear_attention_step(eqlinear_plan_t p, const eqlinear_heads* q, const eqlinear_pages* k_cache,

@@ -16,7 +16,7 @@ constexpr int kQueries = 16;     // query heads of one workgroup: the columns of
 constexpr int kKeys = 32;        // keys of a wave's tile
 constexpr int kUnit = 4 * kKeys;  // keys of a workgroup's pass
 constexpr int kMaxShared = 2048;  // sequences whose lengths a workgroup sums up
-constexpr int kWorkgroups = 768;
+constexpr int kWorkgroups = 1024;  // at most
 
 // A sequence's keys are units of kUnit; an item is one (sequence, kv head, run of kQueries of
 // its query heads).  Up to kMaxShared sequences, the units of all items lie in one row that is
@@ -31,12 +31,14 @@ struct Grid {
     int shared;
     uint32_t wgs;
 };
-Grid grid_for(int heads, int kv_heads, int64_t batch) {
+// Waves per SIMD that the registers are held to: workgroups a CU, all of which run at once.
+constexpr int step_waves(int es, int db) { return es == 4 ? (db == 1 ? 3 : (db == 2 ? 2 : 1)) : (db == 1 ? 4 : (db == 2 ? 3 : 2)); }
+Grid grid_for(int es, int heads, int kv_heads, int D_k, int D_v, int64_t batch) {
     Grid g;
     g.groups = (heads / kv_heads + kQueries - 1) / kQueries;
     g.items = kv_heads * g.groups;
     g.shared = batch <= kMaxShared;
-    g.wgs = g.shared ? kWorkgroups : (uint32_t)(batch * g.items);
+    g.wgs = g.shared ? 256 * step_waves(es, ((D_k > D_v ? D_k : D_v) + 31) / 32) : (uint32_t)(batch * g.items);
     return g;
 }
 struct Cut {
@@ -51,15 +53,18 @@ __device__ __forceinline__ int length_of(const StepArgs& a, int64_t b) {
     const int64_t most = (int64_t)a.max_blocks * a.block_size;
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
+// Floats of a part's row of values: whole pieces of four.
+__host__ __device__ constexpr int row_floats(int D) { return (D + 3) / 4 * 4; }
 // (an empty sequence has one unit, of no keys: its outputs are written too)
 __device__ __forceinline__ int units_of(int n) { return n > 0 ? (n + kUnit - 1) / kUnit : 1; }
 
 // One wave takes 32 keys at a time: scores S^T = K Q^T with the keys as rows straight from
-// memory, the values through an LDS tile of its own (read back transposed), both for the next
-// keys while it works on these, and the blocks of the keys after those.  Its four waves'
+// memory, the values through an LDS tile of its own (read back transposed).  The next keys'
+// loads go out as soon as these have left their registers, and the blocks of the keys after
+// those with them.  Its four waves'
 // sums are joined at the end of an item.
 template <typename IO, int DB, bool VEC>
-__global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Grid g, float* ws, uint32_t base) {
+__global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(StepArgs a, BucketMap map, Grid g, float* ws, uint32_t base) {
     using O = Op<IO>;
     using F = typename O::F;
     constexpr int ES = O::ES, E = 16 / ES, D = 32 * DB, P = D / E, NB = D / 16, NM = D / O::KS;
@@ -152,41 +157,44 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
             const int key = j0 + (lane & 31);
             return key < k1 ? a.table[b * a.max_blocks + (uint32_t)key / (uint32_t)a.block_size] : -1;
         };
-        struct Tile {
-            u32x4 k[2][NM], v[NL];
-            uint32_t there;  // keys of the tile, a bit each
+        u32x4 kreg[2][NM], vreg[NL];
+        uint32_t there = 0;  // the tile's keys that are there, a bit each
+        const IO* const kp = (const IO*)a.k.p + kv * a.k.hs;
+        const IO* const vp = (const IO*)a.v.p + kv * a.v.hs;
+        // (a key that is not there reads the cache's first row, and counts for nothing)
+        auto at = [&](const Pages& x, int j0, int id) {
+            const int64_t in = (uint32_t)(j0 + (lane & 31)) % (uint32_t)a.block_size;
+            return id >= 0 && id < a.blocks ? id * x.bs + in * x.ts : (int64_t)0;
         };
-        auto load = [&](Tile& t, int j0, int id) {
-            const int key = j0 + (lane & 31);
-            const bool ok = id >= 0 && id < a.blocks;
-            t.there = (uint32_t)__ballot(ok);
-            const int64_t in = (uint32_t)key % (uint32_t)a.block_size, blk = ok ? id : 0;
-            const int64_t kat = ok ? blk * a.k.bs + in * a.k.ts : 0, vat = ok ? blk * a.v.bs + in * a.v.ts : 0;
-            const IO* const kp = (const IO*)a.k.p + kv * a.k.hs;
-            const IO* const vp = (const IO*)a.v.p + kv * a.v.hs;
+        auto load_k = [&](int64_t rows) __attribute__((always_inline)) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                const IO* p = kp + __shfl(kat, 16 * kb + ln);
+                const IO* p = kp + __shfl(rows, 16 * kb + ln);
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
                     const int col = (4 * m + kg) * E;
-                    if constexpr (VEC) t.k[kb][m] = *reinterpret_cast<const u32x4*>(p + (col < a.D_k ? col : 0));
-                    else t.k[kb][m] = load_piece<IO>(p, col, a.D_k);
+                    if constexpr (VEC) kreg[kb][m] = *reinterpret_cast<const u32x4*>(p + (col < a.D_k ? col : 0));
+                    else kreg[kb][m] = load_piece<IO>(p, col, a.D_k);
                 }
             }
+        };
+        auto load_v = [&](int64_t rows) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int s = 64 * i + lane, col = s % P * E;
-                const IO* p = vp + __shfl(vat, s / P);
-                if constexpr (VEC) t.v[i] = *reinterpret_cast<const u32x4*>(p + (col < a.D_v ? col : 0));
-                else t.v[i] = load_piece<IO>(p, col, a.D_v);
+                const IO* p = vp + __shfl(rows, s / P);
+                if constexpr (VEC) vreg[i] = *reinterpret_cast<const u32x4*>(p + (col < a.D_v ? col : 0));
+                else vreg[i] = load_piece<IO>(p, col, a.D_v);
             }
         };
 
         const int j_first = k0 + wave * kKeys;
         int id = block_of(j_first);
-        Tile tile;
-        load(tile, j_first, id);
+        if (k0 < k1) {  // (else there may be no cache)
+            load_k(at(a.k, j_first, id));
+            load_v(at(a.v, j_first, id));
+        }
+        there = (uint32_t)__ballot(id >= 0 && id < a.blocks);
         id = block_of(j_first + kUnit);
 
         F q[NM];
@@ -216,31 +224,30 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
         char* const tv = lds[wave];
         const float far = a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.buckets_last] : 0.0f;
         for (int j0 = j_first; j0 < k1; j0 += kUnit) {
-            const int after = block_of(j0 + 2 * kUnit);
-            Tile next;
-            load(next, j0 + kUnit, id);
-            id = after;
-            const uint32_t there = tile.there;
             f32x4 x[2];
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 x[kb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    u32x4 v = tile.k[kb][m];
+                    u32x4 v = kreg[kb][m];
                     // (numbers past the row are others': zeros)
                     if (VEC && D != a.D_k && (4 * m + kg) * E >= a.D_k) v = u32x4{0u, 0u, 0u, 0u};
                     O::mma(x[kb], __builtin_bit_cast(F, v), q[m]);
                 }
             }
+            load_k(at(a.k, j0 + kUnit, id));
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int s = 64 * i + lane, row = s / P, piece = s % P;
-                u32x4 v = tile.v[i];
+                u32x4 v = vreg[i];
                 if (VEC && D != a.D_v && piece * E >= a.D_v) v = u32x4{0u, 0u, 0u, 0u};
                 if (there != 0xffffffffu && !(there >> row & 1)) v = u32x4{0u, 0u, 0u, 0u};
                 *reinterpret_cast<u32x4*>(tv + place<ES, P>(row, piece)) = v;
             }
+            load_v(at(a.v, j0 + kUnit, id));
+            const uint32_t next = (uint32_t)__ballot(id >= 0 && id < a.blocks);
+            id = block_of(j0 + 2 * kUnit);
             if (a.bias && n - 1 - (j0 + kKeys - 1) < a.reach) {  // the tile's last key
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
                     }
             }
             asm volatile("" ::: "memory");
-            tile = next;
+            there = next;
         }
         total += __shfl_xor(total, 16);
         total += __shfl_xor(total, 32);
@@ -334,7 +341,8 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
         if (tid < kQueries) all_top[tid] = all, all_sum[tid] = sum;  // (lane ln of wave 0)
         __syncthreads();
         const bool whole = starts && ends;
-        float* const part = parts + (int64_t)(2 * wg + (starts ? 1 : 0)) * nr * (a.D_v + 2);
+        const int64_t at_part = (int64_t)(2 * wg + (starts ? 1 : 0)) * nr;
+        float* const part = parts + 4 * (int64_t)g.wgs * nr + at_part * row_floats(a.D_v);
         for (int e = tid; e < nq * a.D_v; e += 256) {
             const int h = e / a.D_v, d = e - h * a.D_v;
             float v = 0.0f;
@@ -344,12 +352,12 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
                 const float s = all_sum[h];
                 ((IO*)const_cast<void*>(a.o.p))[b * a.o.ts + (int64_t)(head0 + h) * a.o.hs + d] = (IO)(s == 0.0f ? 0.0f : v / s);
             } else {
-                part[h * (a.D_v + 2) + 2 + d] = v;
+                part[h * row_floats(a.D_v) + d] = v;
             }
         }
         if (tid < nq) {
             const float s = all_sum[tid], t = all_top[tid];
-            if (!whole) part[tid * (a.D_v + 2)] = t, part[tid * (a.D_v + 2) + 1] = s;
+            if (!whole) reinterpret_cast<float2*>(parts)[at_part + tid] = float2{t, s};
             else if (a.lse)
                 a.lse[(int64_t)(head0 + tid) * a.batch + b] =
                     s == 0.0f ? -kInf : ((t == -kInf ? 0.0f : t) - att::kShift<IO> + __builtin_amdgcn_logf(s)) * kLn2;
@@ -358,55 +366,87 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, BucketMap map, Gr
     }
 }
 
-// Joins the parts of one (sequence, head): a wave each.
-template <typename IO>
-__global__ __launch_bounds__(256) void join_kernel(StepArgs a, Grid g, const float* ws) {
-    const int lane = (int)threadIdx.x & 63;
-    const int id = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
-    if (id >= a.batch * a.heads) return;
+// Joins the parts of one (sequence, head): a workgroup of kJoin threads, 32 to a part, several
+// parts in flight from each.  One sequence of 131072 tokens had 384 parts a head: 7 us on 512
+// threads, 71 with a wave that takes one part after the other; 3072 rows of two parts or so
+// took 13.7 us on 512 threads, whose waves come in three rounds.
+template <typename IO, int kJoin>
+__global__ __launch_bounds__(kJoin) void join_kernel(StepArgs a, Grid g, const float* ws) {
+    constexpr int G = kJoin / 32;
+    __shared__ float tops[kWorkgroups + 1], sums[G][att::Shape<float, 4>::D], red[kJoin / 64];
+    const int tid = (int)threadIdx.x, id = (int)blockIdx.x;
     const int b = id / a.heads, head = id - b * a.heads, r = a.heads / a.kv_heads, kv = head / r;
     const int group = (head - kv * r) / kQueries, h = head - kv * r - group * kQueries, nr = r < kQueries ? r : kQueries;
     const int* const before = reinterpret_cast<const int*>(ws);
     const Cut cut((int64_t)before[a.batch] * g.items, g.wgs);
     const int64_t of = before[b + 1] - before[b];
     const int64_t u = (int64_t)before[b] * g.items + (kv * g.groups + group) * of;
-    const int64_t w0 = cut.owner(u), w1 = cut.owner(u + of - 1);
-    if (w0 == w1) return;  // finished there
+    const int w0 = (int)cut.owner(u), n = (int)cut.owner(u + of - 1) - w0 + 1;
+    if (n == 1) return;  // finished there
     const float* const parts = ws + (a.batch + 1 + 63) / 64 * 64;
-    const int64_t step = (int64_t)nr * (a.D_v + 2);
-    const float* p = parts + h * (a.D_v + 2);
-    auto at = [&](int64_t w) { return p + (2 * w + (w == w0 ? 1 : 0)) * step; };
-    float all = -kInf, sum = 0.0f;
-    for (int64_t w = w0 + lane; w <= w1; w += 64) all = fmaxf(all, at(w)[0]);
+    auto row = [&](int i) { return (int64_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * nr + h; };
+    float all = -kInf;
+    float2 mine[(kWorkgroups + kJoin - 1) / kJoin];
+#pragma unroll
+    for (int k = 0; k < (kWorkgroups + kJoin - 1) / kJoin; ++k) {
+        const int i = tid + k * kJoin;
+        mine[k] = i < n ? reinterpret_cast<const float2*>(parts)[row(i)] : float2{-kInf, 0.0f};
+        all = fmaxf(all, mine[k].x);
+    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) all = fmaxf(all, __shfl_xor(all, o));
-    float v0 = 0.0f, v1 = 0.0f;
-#pragma unroll 4
-    for (int64_t w = w0; w <= w1; ++w) {
-        const float* const x = at(w);
-        const float t = x[0], c = t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all);
-        sum += c * x[1];
-        v0 += c * (lane < a.D_v ? x[2 + lane] : 0.0f);
-        v1 += c * (lane + 64 < a.D_v ? x[2 + lane + 64] : 0.0f);
+    if ((tid & 63) == 0) red[tid >> 6] = all;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoin / 64; ++k) all = fmaxf(all, red[k]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < (kWorkgroups + kJoin - 1) / kJoin; ++k) {
+        const float t = mine[k].x, c = t == all || t == -kInf ? 1.0f : __builtin_amdgcn_exp2f(t - all);
+        if (tid + k * kJoin < n) tops[tid + k * kJoin] = c;
+        sum += c * mine[k].y;
     }
-    IO* o = (IO*)const_cast<void*>(a.o.p) + b * a.o.ts + (int64_t)head * a.o.hs;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (lane < a.D_v) o[lane] = (IO)(v0 * inv);
-    if (lane + 64 < a.D_v) o[lane + 64] = (IO)(v1 * inv);
-    if (lane == 0 && a.lse)
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+    __syncthreads();
+    if ((tid & 63) == 0) red[tid >> 6] = sum;
+    const float* const values = parts + 4 * (int64_t)g.wgs * nr;
+    const int gr = tid / 32, d = (tid & 31) * 4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    if (d < a.D_v) {
+#pragma unroll 8
+        for (int i = gr; i < n; i += G) v += *reinterpret_cast<const f32x4*>(values + row(i) * row_floats(a.D_v) + d) * tops[i];
+        *reinterpret_cast<f32x4*>(&sums[gr][d]) = v;
+    }
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoin / 64; ++k) sum += red[k];
+    if (tid < a.D_v) {
+        float o = 0.0f;
+        const int used = n < G ? n : G;
+        for (int k = 0; k < used; ++k) o += sums[k][tid];
+        ((IO*)const_cast<void*>(a.o.p))[b * a.o.ts + (int64_t)head * a.o.hs + tid] = (IO)(sum == 0.0f ? 0.0f : o / sum);
+    }
+    if (tid == 0 && a.lse)
         a.lse[(int64_t)head * a.batch + b] =
             sum == 0.0f ? -kInf : ((all == -kInf ? 0.0f : all) - att::kShift<IO> + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 template <typename IO, int DB, bool VEC>
 hipError_t run_cfg(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t stream) {
-    const Grid g = grid_for(a.heads, a.kv_heads, a.batch);
+    const Grid g = grid_for(sizeof(IO), a.heads, a.kv_heads, a.D_k, a.D_v, a.batch);
     const size_t lds = (g.shared ? (size_t)(a.batch + 1) * 4 : 0) + (a.bias ? (size_t)kQueries * a.buckets * 4 + a.reach + 1 : 0);
     in_pieces(g.wgs, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((step_kernel<IO, DB, VEC>), dim3(wgs), dim3(256), lds, stream, a, map, g, ws, base);
     });
-    if (g.shared)
-        hipLaunchKernelGGL((join_kernel<IO>), dim3((uint32_t)((a.batch * a.heads + 3) / 4)), dim3(256), 0, stream, a, g, ws);
+    if (g.shared) {
+        // many rows: few parts each (on average); few: many
+        const dim3 rows((uint32_t)(a.batch * a.heads));
+        if (a.batch * g.items >= g.wgs / 8) hipLaunchKernelGGL((join_kernel<IO, 128>), rows, dim3(128), 0, stream, a, g, ws);
+        else hipLaunchKernelGGL((join_kernel<IO, 512>), rows, dim3(512), 0, stream, a, g, ws);
+    }
     return hipGetLastError();
 }
 
@@ -431,11 +471,11 @@ hipError_t run(StepArgs a, const BucketMap& map, float* ws, hipStream_t stream) 
 }  // namespace
 
 // Units before each sequence, and two parts of every workgroup.
-size_t attention_step_workspace(int heads, int kv_heads, int D_v, int64_t batch) {
+size_t attention_step_workspace(int io, int heads, int kv_heads, int D_k, int D_v, int64_t batch) {
     if (batch <= 0) return 0;
-    const Grid g = grid_for(heads, kv_heads, batch);
+    const Grid g = grid_for(io == kIoF32 ? 4 : 2, heads, kv_heads, D_k, D_v, batch);
     const int r = heads / kv_heads, nr = r < kQueries ? r : kQueries;
-    return g.shared ? ((size_t)(batch + 1 + 63) / 64 * 64 + (size_t)2 * g.wgs * nr * (D_v + 2)) * 4 : 0;
+    return g.shared ? ((size_t)(batch + 1 + 63) / 64 * 64 + (size_t)2 * g.wgs * nr * (row_floats(D_v) + 2)) * 4 : 0;
 }
 
 hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream) {

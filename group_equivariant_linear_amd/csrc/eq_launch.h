@@ -216,7 +216,7 @@ struct StepArgs {
     float* lse;
     int q_vec, buckets_last;  // rows of q in whole pieces; the bucket of all distances past the reach
 };
-size_t attention_step_workspace(int heads, int kv_heads, int D_v, int64_t batch);
+size_t attention_step_workspace(int io, int heads, int kv_heads, int D_k, int D_v, int64_t batch);
 hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream);
 
 // cache.hip: the tables of a paged cache, and the store of new tokens.

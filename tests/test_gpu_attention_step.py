@@ -153,6 +153,22 @@ def test_blocks_that_are_not_there(eq, dt):
 
 
 @pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("empty", ["blocks", "table", "lengths"])
+def test_no_cache(eq, dt, empty):
+    """A cache of no blocks, a table of no entries, sequences of no keys."""
+    import torch
+    s = Step(eq, dt, 8, 2, 1, 8, 8, [3, 0, 1], 16)
+    if empty == "blocks":
+        s.kc, s.vc = s.kc[:0], s.vc[:0]
+    elif empty == "table":
+        s.table = s.table[:, :0].contiguous()
+    else:
+        s.lengths.zero_()
+    s.run()
+    assert (s.o == 0).all() and (s.lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("dt", TYPES)
 def test_nan_behind_the_last_key(eq, dt):
     """Values and keys past a sequence's length, in its own last block too, and in blocks of no sequence."""
     import torch
