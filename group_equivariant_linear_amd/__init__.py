@@ -861,19 +861,31 @@ def eqlinear_cache_tables(lengths, added, free_blocks, cursor, table, block_size
     max_blocks]), lengths_out, cursor_out, and for the packed new tokens slots (int64 [T]), positions (int32 [T]) and
     offsets (int64 [batch + 1]).  lengths_out may be lengths and cursor_out cursor."""
     torch = _torch()
-    for t in (lengths, added, free_blocks, cursor, table, lengths_out, cursor_out, slots, positions, offsets):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("eqlinear_cache_tables: expected torch tensors (their sizes are checked)")
-    i32, B, T = torch.int32, lengths.numel(), slots.numel()
+    i32, i64 = torch.int32, torch.int64
+    try:
+        B, T, F, rows = lengths.numel(), slots.numel(), free_blocks.numel(), table.shape
+    except AttributeError:
+        raise TypeError("eqlinear_cache_tables: expected torch tensors (their sizes are checked)") from None
+    if rows != (B, rows[-1]):
+        raise ValueError(f"table: expected shape {(B, rows[-1])}, got {tuple(rows)}")
     ws, nb = _workspace(workspace)
-    max_blocks = table.shape[-1]
     _check(load_library().eqlinear_cache_tables(
-        _dense(lengths, "lengths", i32, (B,)), _dense(added, "added", i32, (B,)),
-        _dense(free_blocks, "free_blocks", i32, (free_blocks.numel(),)), free_blocks.numel(),
-        _dense(cursor, "cursor", i32, (1,)), _dense(table, "table", i32, (B, max_blocks)), max_blocks, int(block_size),
-        _dense(lengths_out, "lengths_out", i32, (B,)), _dense(cursor_out, "cursor_out", i32, (1,)),
-        _dense(slots, "slots", torch.int64, (T,)), _dense(positions, "positions", i32, (T,)),
-        _dense(offsets, "offsets", torch.int64, (B + 1,)), B, T, ws, nb, _raw_stream(stream)), "eqlinear_cache_tables")
+        _flat(lengths, "lengths", i32, B), _flat(added, "added", i32, B), _flat(free_blocks, "free_blocks", i32, F), F,
+        _flat(cursor, "cursor", i32, 1), _flat(table, "table", i32, B * rows[1]), rows[1], block_size,
+        _flat(lengths_out, "lengths_out", i32, B), _flat(cursor_out, "cursor_out", i32, 1), _flat(slots, "slots", i64, T),
+        _flat(positions, "positions", i32, T), _flat(offsets, "offsets", i64, B + 1), B, T, ws, nb, _raw_stream(stream)),
+        "eqlinear_cache_tables")
+
+
+def _flat(t, name: str, dtype, numel: int):
+    """Address of a contiguous GPU tensor of the given dtype and number of elements (whose shape is a single axis, or
+    has been checked: half of _dense's cost)."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dense(t, name, dtype, (numel,))
 
 
 def eqlinear_cache_store(plan: Plan, k, v, slots, k_cache, v_cache, T: int | None = None, blocks: int | None = None,

@@ -20,8 +20,7 @@ constexpr int kWorkgroups = 1024;  // at most
 
 // A sequence's keys are units of kUnit; an item is one (sequence, kv head, run of kQueries of
 // its query heads).  Up to kMaxShared sequences, the units of all items lie in one row that is
-// cut evenly: workgroup w of the W that have any (at most one a unit) takes units w n / W ..
-// (w + 1) n / W, whatever sequences they belong to, so that lengths need not be alike (or known
+// cut evenly over the workgroups (as many as have any), whatever sequences they belong to, so that lengths need not be alike (or known
 // on the host).  An item inside one
 // workgroup is finished there; of one that spans several, each writes its part, at 2 w + 1 if
 // the item starts in w, else at 2 w, and join_kernel takes them in order.  With more sequences
@@ -41,11 +40,21 @@ Grid grid_for(int es, int heads, int kv_heads, int D_k, int D_v, int64_t batch) 
     g.wgs = g.shared ? 256 * step_waves(es, ((D_k > D_v ? D_k : D_v) + 31) / 32) : (uint32_t)(batch * g.items);
     return g;
 }
+// (64-bit divisions take 150 instructions in a row: 32-bit ones where they do)
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 struct Cut {
-    int64_t units, W;
-    __device__ __forceinline__ Cut(int64_t n, uint32_t wgs) : units(n), W(n < wgs ? n : wgs) {}
-    __device__ __forceinline__ int64_t first(int64_t w) const { return w < W ? w * units / W : units; }
-    __device__ __forceinline__ int64_t owner(int64_t unit) const { return ((unit + 1) * W - 1) / units; }
+    int64_t W, each, more;  // workgroups; units of each; the first `more` take one more
+    __device__ __forceinline__ Cut(int64_t units, uint32_t wgs) : W(units < wgs ? units : wgs) {
+        each = divided(units, W);
+        more = units - each * W;
+    }
+    __device__ __forceinline__ int64_t first(int64_t w) const { return (w < W ? w : W) * each + (w < more ? w : more); }
+    __device__ __forceinline__ int64_t owner(int64_t unit) const {
+        const int64_t big = more * (each + 1);
+        return unit < big ? divided(unit, each + 1) : more + divided(unit - big, each);
+    }
 };
 
 __device__ __forceinline__ int length_of(const StepArgs& a, int64_t b) {
@@ -72,12 +81,13 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
     __shared__ __attribute__((aligned(16))) char lds[4][kKeys * P * 16];
     __shared__ float ms[4][kQueries], ls[4][kQueries], all_top[kQueries], all_sum[kQueries];
     __shared__ int wave_units[4];
-    extern __shared__ int shared[];  // units before each sequence; the biases of an item; the buckets of its distances
+    extern __shared__ int shared[];  // units before each sequence, lengths; an item's biases; the buckets of distances
     const uint32_t wg = blockIdx.x + base;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4, ln = lane & 15;
     const int r = a.heads / a.kv_heads, nr = r < kQueries ? r : kQueries;
     const float scale = a.scale * kLog2e;
-    float* const biases = reinterpret_cast<float*>(shared + (g.shared ? a.batch + 1 : 0));
+    int* const lengths = shared + a.batch + 1;
+    float* const biases = reinterpret_cast<float*>(shared + (g.shared ? 2 * a.batch + 1 : 0));
     uint8_t* const buckets = reinterpret_cast<uint8_t*>(biases + kQueries * a.buckets);
 
     if (a.bias)
@@ -90,7 +100,9 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int b = tid * per + i;
-            n[i] = i < per && b < B ? units_of(length_of(a, b)) : 0;
+            const int len = i < per && b < B ? length_of(a, b) : 0;
+            if (i < per && b < B) lengths[b] = len;
+            n[i] = i < per && b < B ? units_of(len) : 0;
             sum += n[i];
         }
         int at = sum;
@@ -126,7 +138,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
         bool starts = true, ends = true;
         if (g.shared) {
             int lo = 0, hi = (int)a.batch - 1;  // last sequence whose units start at u0 or before
-            const int64_t target = u0 / g.items;
+            const int64_t target = divided(u0, g.items);
             // units of sequence b are shared[b] g.items .. shared[b + 1] g.items
             while (lo < hi) {
                 const int mid = lo + (hi - lo + 1) / 2;
@@ -134,10 +146,10 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                 else hi = mid - 1;
             }
             b = lo;
-            n = length_of(a, b);
+            n = lengths[lo];
             const int of = units_of(n);
             const int64_t in = u0 - (int64_t)shared[lo] * g.items;
-            item = (int)(in / of);
+            item = (int)divided(in, of);
             unit = (int)(in - (int64_t)item * of);
             count = u1 - u0 < of - unit ? (int)(u1 - u0) : of - unit;
             starts = unit == 0, ends = unit + count == of;
@@ -190,13 +202,6 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
 
         const int j_first = k0 + wave * kKeys;
         int id = block_of(j_first);
-        if (k0 < k1) {  // (else there may be no cache)
-            load_k(at(a.k, j_first, id));
-            load_v(at(a.v, j_first, id));
-        }
-        there = (uint32_t)__ballot(id >= 0 && id < a.blocks);
-        id = block_of(j_first + kUnit);
-
         F q[NM];
         {
             const IO* p = (const IO*)a.q.p + b * a.q.ts + (int64_t)(head0 + (ln < nq ? ln : 0)) * a.q.hs;
@@ -212,6 +217,13 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                 q[m] = __builtin_bit_cast(F, v);
             }
         }
+        if (k0 < k1) {  // (else there may be no cache)
+            load_k(at(a.k, j_first, id));
+            load_v(at(a.v, j_first, id));
+        }
+        there = (uint32_t)__ballot(id >= 0 && id < a.blocks);
+        id = block_of(j_first + kUnit);
+
         if (a.bias)
             for (int i = tid; i < nq * a.buckets; i += 256)
                 biases[i] = kLog2e * (float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i];
@@ -437,7 +449,7 @@ __global__ __launch_bounds__(kJoin) void join_kernel(StepArgs a, Grid g, const f
 template <typename IO, int DB, bool VEC>
 hipError_t run_cfg(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t stream) {
     const Grid g = grid_for(sizeof(IO), a.heads, a.kv_heads, a.D_k, a.D_v, a.batch);
-    const size_t lds = (g.shared ? (size_t)(a.batch + 1) * 4 : 0) + (a.bias ? (size_t)kQueries * a.buckets * 4 + a.reach + 1 : 0);
+    const size_t lds = (g.shared ? (size_t)(2 * a.batch + 1) * 4 : 0) + (a.bias ? (size_t)kQueries * a.buckets * 4 + a.reach + 1 : 0);
     in_pieces(g.wgs, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((step_kernel<IO, DB, VEC>), dim3(wgs), dim3(256), lds, stream, a, map, g, ws, base);
     });

@@ -16,8 +16,8 @@ struct Request {
     int32_t held_tokens, held_blocks;
 };
 
-__device__ __forceinline__ int64_t blocks_for(int64_t tokens, const TablesArgs& a) {
-    const int64_t n = (tokens + a.block_size - 1) / a.block_size;
+__device__ __forceinline__ int64_t blocks_for(int64_t tokens, const TablesArgs& a) {  // (tokens < 2^31)
+    const int64_t n = ((uint32_t)tokens + (uint32_t)a.block_size - 1u) / (uint32_t)a.block_size;
     return n < a.max_blocks ? n : a.max_blocks;
 }
 
@@ -42,10 +42,47 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t& all) {
     return v + before;
 }
 
+// New token t: its slot and position, and its request's next block if it is the block's first.
+__device__ __forceinline__ void place_token(const TablesArgs& a, const Request* requests, const int64_t* offsets, int64_t t) {
+    if (t >= offsets[a.batch]) {
+        a.slots[t] = -1;
+        a.positions[t] = 0;
+        return;
+    }
+    int lo = 0, hi = (int)a.batch - 1;  // first request whose tokens end after t
+    while (lo < hi) {
+        const int mid = (int)(((int64_t)lo + hi) / 2);
+        if (offsets[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    const Request q = requests[lo];
+    const uint32_t pos = (uint32_t)(q.held_tokens + (t - offsets[lo])), at = pos / (uint32_t)a.block_size;
+    const uint32_t in = pos - at * (uint32_t)a.block_size;
+    int64_t id = -1;
+    if (at < (uint32_t)a.max_blocks) {
+        int32_t* const entry = a.table + (int64_t)lo * a.max_blocks + at;
+        if ((int)at < q.held_blocks) {
+            id = *entry;
+        } else {
+            const int64_t f = q.first + at - q.held_blocks;
+            if (f >= 0 && f < a.n_free) id = a.free_blocks[f];
+            if (in == 0) *entry = (int32_t)id;
+        }
+    }
+    a.slots[t] = id < 0 ? -1 : id * a.block_size + in;
+    a.positions[t] = (int32_t)pos;
+}
+
 // One workgroup walks the requests: offsets of their new tokens, lengths, and where in the
-// free list their new blocks start.
-__global__ __launch_bounds__(kScan) void requests_kernel(TablesArgs a, Request* out) {
+// free list their new blocks start.  Few requests and tokens (ALONE) are all its own: one launch
+// of 5 us instead of two of 4.5 and 2.5.
+constexpr int kAloneRequests = 2048, kAloneTokens = 2 * kScan;
+template <bool ALONE>
+__global__ __launch_bounds__(kScan) void requests_kernel(TablesArgs a, Request* ws) {
     __shared__ int64_t start;  // (read by the thread that overwrites it)
+    extern __shared__ int64_t mine[];  // ALONE: [batch + 1] offsets, [batch] requests
+    int64_t* const offsets = ALONE ? mine : a.offsets;
+    Request* const out = ALONE ? reinterpret_cast<Request*>(mine + a.batch + 1) : ws;
     if (threadIdx.x == 0) start = a.cursor[0];
     __syncthreads();
     const int64_t cursor = start;
@@ -66,44 +103,24 @@ __global__ __launch_bounds__(kScan) void requests_kernel(TablesArgs a, Request* 
         const int64_t last = scan(fresh, all) + blocks;
         if (b < a.batch) {
             if (b == 0) a.offsets[0] = 0;
+            if (b == 0 && ALONE) offsets[0] = 0;
             a.offsets[b + 1] = t1;
+            if (ALONE) offsets[b + 1] = t1;
             a.lengths_out[b] = (int32_t)(n + t1 - t0);
             out[b] = Request{cursor + last - fresh, (int32_t)n, (int32_t)held};
         }
         blocks += all;
     }
     if (threadIdx.x == 0) a.cursor_out[0] = (int32_t)(cursor + blocks);
+    if constexpr (ALONE) {
+        __syncthreads();
+        for (int64_t t = threadIdx.x; t < a.T; t += kScan) place_token(a, out, offsets, t);
+    }
 }
 
 __global__ __launch_bounds__(256) void tokens_kernel(TablesArgs a, const Request* requests, uint32_t base) {
     const int64_t t = ((int64_t)blockIdx.x + base) * 256 + threadIdx.x;
-    if (t >= a.T) return;
-    if (t >= a.offsets[a.batch]) {
-        a.slots[t] = -1;
-        a.positions[t] = 0;
-        return;
-    }
-    int64_t lo = 0, hi = a.batch - 1;  // first request whose tokens end after t
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.offsets[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    const Request q = requests[lo];
-    const int64_t pos = q.held_tokens + (t - a.offsets[lo]), at = pos / a.block_size;
-    int64_t id = -1;
-    if (at < a.max_blocks) {
-        int32_t* const entry = a.table + lo * a.max_blocks + at;
-        if (at < q.held_blocks) {
-            id = *entry;
-        } else {
-            const int64_t f = q.first + at - q.held_blocks;
-            if (f >= 0 && f < a.n_free) id = a.free_blocks[f];
-            if (pos % a.block_size == 0) *entry = (int32_t)id;  // (a new block's first token)
-        }
-    }
-    a.slots[t] = id < 0 ? -1 : id * a.block_size + pos % a.block_size;
-    a.positions[t] = (int32_t)pos;
+    if (t < a.T) place_token(a, requests, a.offsets, t);
 }
 
 // W numbers a thread: 16 bytes, or one.
@@ -133,7 +150,12 @@ size_t cache_tables_workspace(int64_t batch) { return (size_t)batch * sizeof(Req
 
 hipError_t launch_cache_tables(const TablesArgs& a, void* ws, hipStream_t stream) {
     Request* const r = static_cast<Request*>(ws);
-    hipLaunchKernelGGL(requests_kernel, dim3(1), dim3(kScan), 0, stream, a, r);
+    if (a.batch <= kAloneRequests && a.T <= kAloneTokens) {
+        const size_t lds = (size_t)(a.batch + 1) * 8 + (size_t)a.batch * sizeof(Request);
+        hipLaunchKernelGGL((requests_kernel<true>), dim3(1), dim3(kScan), lds, stream, a, r);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((requests_kernel<false>), dim3(1), dim3(kScan), 0, stream, a, r);
     in_pieces((a.T + 255) / 256, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL(tokens_kernel, dim3(wgs), dim3(256), 0, stream, a, (const Request*)r, base);
     });
