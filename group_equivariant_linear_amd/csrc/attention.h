@@ -213,7 +213,7 @@ __device__ __forceinline__ float bias_of(const AttentionArgs& a, const BucketMap
 template <typename IO>
 __device__ __forceinline__ void fill_biases(float* tab, const AttentionArgs& a, const BucketMap& map, int head) {
     const int off = a.reach + kPad;
-    for (int x = (int)threadIdx.x; x <= 2 * off; x += 256) tab[x] = kLog2e * bias_of<IO>(a, map, head, x - off);
+    for (int x = (int)threadIdx.x; x <= 2 * off; x += 256) tab[x] = a.bias ? kLog2e * bias_of<IO>(a, map, head, x - off) : 0.0f;
 }
 __host__ __device__ constexpr int tab_width(int reach) { return 2 * (reach + kPad) + 1; }
 
@@ -238,6 +238,14 @@ __device__ __forceinline__ void load_rows(F (&f)[C::NS], const Heads& x, int64_t
             f[s] = __builtin_bit_cast(F, v);
         }
     }
+}
+
+// The numbers of fragments with their signs turned.
+template <typename F, int N>
+__device__ __forceinline__ void negate(F (&f)[N]) {
+    constexpr uint32_t sign = sizeof(f[0][0]) == 2 ? 0x80008000u : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __builtin_bit_cast(F, __builtin_bit_cast(u32x4, f[i]) ^ sign);
 }
 
 // Accumulators of 32 rows to memory, times m, rounded once.
@@ -298,10 +306,18 @@ __device__ __forceinline__ void load_words_to_lds(const u32x4& rsrc, uint32_t of
 template <class C>
 constexpr int kStages = 4 * C::TILE <= 80 * 1024 ? 2 : 1;
 
+// What work on a tile has to look at: every row sees all of it; some of its rows are not
+// there (zeros); some are there and not seen, so that no infinity of theirs may be multiplied.
+// (UNSEEN kernels look for those: causal ones, and those for rows off 16 bytes, which are one
+// for all calls.)
+constexpr int kWhole = 0, kPartial = 1, kUnseen = 2;
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
 // Visits n_a + n_b pairs of tiles: load(v, stage) of visit v, then, when its tiles are there,
 // a(v, stage) for the first n_a visits and b(v, stage) for the others.  Every wave calls it, and
-// a() and b() have no barrier.  (Two loops: work with and without masks in one, by a branch,
-// costs half as many registers again.)
+// a() and b() have no barrier.  (Loops of their own: work with and without masks in one, by a
+// branch, costs half as many registers again.)
 template <class C, typename L, typename A, typename B>
 __device__ __forceinline__ void pass_over(int n_a, int n_b, L&& load, A&& a, B&& b) {
     const int n = n_a + n_b;
@@ -343,7 +359,7 @@ constexpr int dkv_waves(int es, int db) { return es == 4 ? 2 : (db == 1 ? 3 : 2)
 constexpr bool dkv_apart(int es, int db) { return es == 4 ? db >= 2 : db >= 4; }
 
 // --- forward --------------------------------------------------------------------------
-template <typename IO, int DB, bool VEC, bool BIAS>
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
@@ -368,8 +384,9 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     if constexpr (BIAS) fill_biases<IO>(tab, a, map, head);
     f32x16 acc[DB];
     clear(acc);
-    float top = -kInf, total = 0.0f;
-    const float scale = a.scale * kLog2e;
+    float top = -kInf, total = 0.0f, ref = -kShift<IO>;
+    const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
+    if (a.scale < 0.0f) negate(q);
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;  // last key that it sees
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
     // keys that some of the workgroup's rows see; tiles that all of them do
@@ -380,9 +397,9 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
     const RowFrags<C> rows(lds[0]);
     const ColumnFrags<C, O> cols(lds[0] + C::TILE);
-    // Keys j0 .. of the tiles at `by`.  EDGE: some that not every row sees.
-    auto tile = [&](auto edge, int j0, int by) __attribute__((always_inline)) {
-        constexpr bool EDGE = decltype(edge)::value;
+    // Keys j0 .. of the tiles at `by`.  Scores come relative to `ref`, in powers of two.
+    auto tile = [&](auto kind, int j0, int by) __attribute__((always_inline)) {
+        constexpr int K = decltype(kind)::value;
         f32x16 x[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -406,11 +423,8 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, t[-(32 * kb + row_of(i))]);
             }
-        } else {
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) x[kb] *= scale;
         }
-        if constexpr (EDGE) {
+        if constexpr (K != kWhole) {
             const int lim = last - j0 - 4 * h;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -423,21 +437,23 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[kb][i]);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if constexpr (!BIAS) mx *= scale;
         if (__any(mx > top + kSlack<IO>)) {
             // (a row without scores so far has sums of 0, and none of its terms is counted against -infinity)
             const float now = mx > top + kSlack<IO> ? mx : top;
             const float c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
             top = now;
+            ref = (top == -kInf ? 0.0f : top) - kShift<IO>;
             total *= c;
+            asm volatile("");  // (rare: not to be computed beside the other way)
 #pragma unroll
             for (int cb = 0; cb < DB; ++cb) acc[cb] *= c;
         }
-        const float m = (top == -kInf ? 0.0f : top) - kShift<IO>;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                x[kb][i] = __builtin_amdgcn_exp2f(x[kb][i] - m);
+                x[kb][i] = __builtin_amdgcn_exp2f(BIAS ? x[kb][i] - ref : __builtin_fmaf(x[kb][i], scale, -ref));
                 total += x[kb][i];
             }
         uint32_t odd = 0;
@@ -452,7 +468,7 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
 #pragma unroll
                 for (int cb = 0; cb < DB; ++cb) {
                     F v[1] = {cols.get(by, kb, t, cb)};
-                    if constexpr (EDGE) {
+                    if constexpr (K == kUnseen) {
                         const uint32_t o = O::top(v);
                         odd = o > odd ? o : odd;
                         v[0] = O::finite(v[0]);
@@ -460,7 +476,11 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
                     O::mma(acc[cb], v[0], p);
                 }
             }
-        if (EDGE && __any(odd >= O::kInf)) add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by, kTile, last - j0, false, found[wave]);
+        if (K == kUnseen && __any(odd >= O::kInf))
+            add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by, kTile, last - j0, false, found[wave]);
+    };
+    auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
+        if (n_rows > 0 && t * kTile < wave_end) tile(kind, t * kTile, stage * 2 * C::TILE);
     };
     pass_over<C>(
         whole, tiles(end) - whole,
@@ -470,18 +490,16 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
             lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
         },
         [&](int t, int stage) {
-            if (n_rows > 0) tile(std::false_type{}, t * kTile, stage * 2 * C::TILE);
+            if (n_rows > 0) tile(Kind<kWhole>{}, t * kTile, stage * 2 * C::TILE);
         },
-        [&](int t, int stage) {
-            if (n_rows > 0 && t * kTile < wave_end) tile(std::true_type{}, t * kTile, stage * 2 * C::TILE);
-        });
+        [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
     if (n_rows <= 0) return;
     total += __shfl_xor(total, 32);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     store_rows<C, IO>(acc, a.o, s.q0 + w0, head, n_rows, a.D_v, inv, a.out_vec);
     if (a.lse && h == 0 && (lane & 31) < n_rows)
         a.lse[(int64_t)head * a.T + s.q0 + my] =
-            total == 0.0f ? -kInf : ((top == -kInf ? 0.0f : top) - kShift<IO> + __builtin_amdgcn_logf(total)) * kLn2;
+            total == 0.0f ? -kInf : (ref + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // --- backward -------------------------------------------------------------------------
@@ -537,7 +555,7 @@ __device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, floa
 // in registers.  (One LDS addition for each of a block's 16 accumulators instead of its diagonals
 // took the kernel from 140 to 370 us in packed training on images.)  A workgroup writes the sums
 // of its buckets; reduce_kernel joins those of a head.
-template <typename IO, int DB, bool VEC, bool BIAS>
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
@@ -588,7 +606,8 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     f32x16 acc[DB];
     clear(acc);
     float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
-    const float scale = a.scale * kLog2e;
+    const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
+    if (a.scale < 0.0f) negate(q);
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
@@ -658,17 +677,17 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         delta += left / ones;
         lse += __builtin_amdgcn_logf(ones);
     }
-    if (real && h == 0) a.row_lse[row] = lse, a.row_delta[row] = delta;
+    if (real && h == 0) a.row_lse[row] = -lse / scale, a.row_delta[row] = -delta;  // (as dkv_kernel takes them)
 
-    auto block = [&](auto edge, int j, int kb, int by) __attribute__((always_inline)) {
-        constexpr bool EDGE = decltype(edge)::value;
+    auto block = [&](auto kind, int j, int kb, int by) __attribute__((always_inline)) {
+        constexpr int K = decltype(kind)::value;
         f32x16 x[1], dp;
         scores(x[0], dp, j, kb, by);
         const int lim = last - j - 4 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             x[0][i] *= dp[i] - delta;
-            if constexpr (EDGE) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
+            if constexpr (K != kWhole) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
         }
         if constexpr (BIAS) {
             const int from = w0 + shift - j;
@@ -698,7 +717,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
 #pragma unroll
             for (int cb = 0; cb < DB; ++cb) {
                 F k[1] = {kcols.get(by, kb, t, cb)};
-                if constexpr (EDGE) {
+                if constexpr (K == kUnseen) {
                     const uint32_t o = O::top(k);
                     odd = o > odd ? o : odd;
                     k[0] = O::finite(k[0]);
@@ -706,17 +725,17 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
                 O::mma(acc[cb], k[0], p);
             }
         }
-        if (EDGE && __any(odd >= O::kInf)) 
+        if (K == kUnseen && __any(odd >= O::kInf)) 
             add_odd_numbers<C, IO, false>(acc, lds[0] + by + kb * (32 * C::P * 16), 32, last - j, true, found[wave]);
     };
-    auto second = [&](auto edge, int t, int stage) __attribute__((always_inline)) {
+    auto second = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
-            if (n_rows > 0 && t * kTile + 32 * kb < wave_end) block(edge, t * kTile + 32 * kb, kb, stage * 2 * C::TILE);
+            if (n_rows > 0 && t * kTile + 32 * kb < wave_end) block(kind, t * kTile + 32 * kb, kb, stage * 2 * C::TILE);
     };
     pass_over<C>(
-        whole, tiles(end) - whole, load, [&](int t, int stage) { second(std::false_type{}, t, stage); },
-        [&](int t, int stage) { second(std::true_type{}, t, stage); });
+        whole, tiles(end) - whole, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
+        [&](int t, int stage) { second(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
     if (n_rows > 0) {
         const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
         store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
@@ -763,7 +782,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
 
 // Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the
 // queries of every head that shares it, in a fixed order; DK and DV: which of the two.
-template <typename IO, int DB, bool VEC, bool BIAS, bool DK, bool DV>
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN, bool DK, bool DV>
 __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
@@ -790,26 +809,37 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     f32x16 dk[DB], dv[DB];
     clear(dk), clear(dv);
     float held = kTopScale;
-    const float scale = a.scale * kLog2e;
-    // Tiles of queries from the first that sees one of the workgroup's keys; visited first are
-    // the last, if it is not whole, and those that do not see all its keys.
+    const float scale = fabsf(a.scale) * kLog2e;  // the keys take its sign
+    if (a.scale < 0.0f) negate(k);
+    // Tiles of queries from the first that sees one of the workgroup's keys: t_edge .. t_whole - 1
+    // see all of them and are visited first, then those before, then the last, if it is not whole.
     const int t_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile : 0;
     const int t_all = a.causal && (int)row0 + kRows - 1 - shift > 0 ? tiles((int)row0 + kRows - 1 - shift) : 0;
     const int t_whole = s.n_q / kTile, tail = s.n_q % kTile && t_first <= t_whole ? 1 : 0;
     const int t_edge = t_all < t_whole ? (t_all > t_first ? t_all : t_first) : t_whole;  // edge tiles: t_first .. t_edge - 1
-    const int n_edge = tail + (t_edge > t_first ? t_edge - t_first : 0), n_whole = t_whole > t_edge ? t_whole - t_edge : 0;
-    auto row_at = [&](int t) { return (tail && t == 0 ? t_whole : t_first + t - tail) * kTile; };
+    const int n_whole = t_whole > t_edge ? t_whole - t_edge : 0, n_early = t_edge > t_first ? t_edge - t_first : 0;
+    auto row_at = [&](int t) {
+        t -= n_whole;
+        return (t < 0 ? t + n_whole + t_edge : (t < n_early ? t_first + t : t_whole)) * kTile;
+    };
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lq(a.q, a.D_k, 0, wave, 4), lg(a.d_o, a.D_v, 0, wave, 4);
     const RowFrags<C> qrows(lds[0]);  // (d_o's tile lies C::TILE behind q's)
     const ColumnFrags<C, O> qcols(lds[0]);
-    // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  EDGE: not all of them see all keys, or
-    // fewer than 32 are left.
-    auto block = [&](auto edge, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
-        constexpr bool EDGE = decltype(edge)::value;
+    // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  Their statistics are what the
+    // accumulators start from: the products end in (score - lse) / scale and dP - delta.
+    auto block = [&](auto kind, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
+        constexpr int K = decltype(kind)::value;
         const int low = a.causal ? my - shift - q0 : 0, high = s.n_q - 1 - q0;  // rows of the block that see the lane's key
-        f32x16 x = {}, dp = {}, p[1], ds[1];
+        f32x16 x, dp, p[1], ds[1];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[0][32 * qb + 8 * g + 4 * h]);
+            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * g + e] = lse[e], dp[4 * g + e] = DK ? delta[e] : 0.0f;
+        }
 #pragma unroll
         for (int st = 0; st < C::NS; ++st) O::mma(x, qrows.template get<F>(by, qb, st), k[st]);
 #pragma unroll
@@ -829,20 +859,14 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
             }
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[0][32 * qb + 8 * g + 4 * h]);
-            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * g + e, at = row_of(i) + 4 * h;
-                const float y = BIAS ? x[i] - lse[e] : __builtin_fmaf(x[i], scale, -lse[e]);
-                p[0][i] = __builtin_amdgcn_exp2f(y);
-                if constexpr (DK) ds[0][i] = p[0][i] * (dp[i] - delta[e]);
-                if constexpr (EDGE) {
-                    const bool seen = at >= low && at <= high;
-                    p[0][i] = seen ? p[0][i] : 0.0f;
-                    if constexpr (DK) ds[0][i] = seen ? ds[0][i] : 0.0f;
-                }
+        for (int i = 0; i < 16; ++i) {
+            p[0][i] = __builtin_amdgcn_exp2f(BIAS ? x[i] : x[i] * scale);
+            if constexpr (DK) ds[0][i] = p[0][i] * dp[i];
+            if constexpr (K != kWhole) {
+                const int at = row_of(i) + 4 * h;
+                const bool seen = at >= low && at <= high;
+                p[0][i] = seen ? p[0][i] : 0.0f;
+                if constexpr (DK) ds[0][i] = seen ? ds[0][i] : 0.0f;
             }
         }
         if constexpr (DK && std::is_same_v<IO, _Float16>) ds[0] *= hold<IO>(ds, held, dk);
@@ -859,7 +883,7 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
 #pragma unroll
                 for (int cb = 0; cb < DB; ++cb) {
                     F g[1] = {qcols.get(at, qb, st, cb)};
-                    if constexpr (EDGE) {
+                    if constexpr (K == kUnseen) {
                         const uint32_t o = O::top(g);
                         odd = o > odd ? o : odd;
                         g[0] = O::finite(g[0]);
@@ -870,7 +894,7 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
         };
         if constexpr (DV) product(dv, by + C::TILE, p[0]);
         if constexpr (DK) product(dk, by, ds[0]);
-        if (EDGE && __any(odd >= O::kInf)) {
+        if (K == kUnseen && __any(odd >= O::kInf)) {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
             if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave]);
             if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave]);
@@ -882,8 +906,16 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
             __syncthreads();
             fill_biases<IO>(tab, a, map, head);
         }
+        auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb) {
+                const int q0 = row_at(t) + 32 * qb;
+                if (n_rows > 0 && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
+                    block(kind, q0, qb, stage * 2 * C::TILE, stats[stage]);
+            }
+        };
         pass_over<C>(
-            n_edge, n_whole,
+            n_whole, n_early + tail,
             [&](int t, int stage) {
                 const int i0 = row_at(t), n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
                 lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
@@ -895,17 +927,10 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
             },
             [&](int t, int stage) {
 #pragma unroll
-                for (int qb = 0; qb < 2; ++qb) {
-                    const int q0 = row_at(t) + 32 * qb;
-                    if (n_rows > 0 && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
-                        block(std::true_type{}, q0, qb, stage * 2 * C::TILE, stats[stage]);
-                }
-            },
-            [&](int t, int stage) {
-#pragma unroll
                 for (int qb = 0; qb < 2; ++qb)
-                    if (n_rows > 0) block(std::false_type{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
-            });
+                    if (n_rows > 0) block(Kind<kWhole>{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
+            },
+            [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
     }
     if (n_rows <= 0) return;
     const bool half = std::is_same_v<IO, _Float16>;
@@ -915,42 +940,44 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
 }
 
 // --- host side ------------------------------------------------------------------------
-template <typename IO, int DB, bool VEC, bool BIAS>
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
     const size_t table = BIAS ? tab_width(a.reach) * 4 : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), table, stream, a, map, base);
+        hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table, stream, a, map, base);
     });
     return hipGetLastError();
 }
 
-template <typename IO, int DB, bool VEC, bool BIAS>
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
     const size_t table = BIAS ? tab_width(a.reach) * 4 : 0, sums = a.dbias ? 8 * table : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
+        hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
     });
     in_pieces((int64_t)a.kv_slots * a.kv_heads, 256, [&](uint32_t base, uint32_t wgs) {
         if constexpr (dkv_apart(sizeof(IO), DB)) {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, true, false>), dim3(wgs), dim3(256), table, stream, a, map, base);
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, false, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, false>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, false, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
         } else {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, true, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
         }
     });
     return hipGetLastError();
 }
 
-#define EQL_ATTENTION(WHAT)                                                                                        \
-    const int db = ((a.D_k > a.D_v ? a.D_k : a.D_v) + 31) / 32;                                                    \
-    const bool bias = a.bias != nullptr;                                                                           \
-    if (db == 1) return EQL_ATTENTION_DB(WHAT, 1);                                                                 \
-    if (db == 2) return EQL_ATTENTION_DB(WHAT, 2);                                                                 \
-    if (db == 3) return EQL_ATTENTION_DB(WHAT, 3);                                                                 \
+// Rows off 16 bytes go number by number into the kernels with everything.
+#define EQL_ATTENTION(WHAT)                                       \
+    const int db = ((a.D_k > a.D_v ? a.D_k : a.D_v) + 31) / 32;   \
+    const bool bias = a.bias != nullptr;                          \
+    if (db == 1) return EQL_ATTENTION_DB(WHAT, 1);                \
+    if (db == 2) return EQL_ATTENTION_DB(WHAT, 2);                \
+    if (db == 3) return EQL_ATTENTION_DB(WHAT, 3);                \
     return EQL_ATTENTION_DB(WHAT, 4);
-#define EQL_ATTENTION_DB(WHAT, DB)                                                                                 \
-    vec ? (bias ? WHAT<IO, DB, true, true>(a, map, stream) : WHAT<IO, DB, true, false>(a, map, stream))            \
-        : (bias ? WHAT<IO, DB, false, true>(a, map, stream) : WHAT<IO, DB, false, false>(a, map, stream))
+#define EQL_ATTENTION_DB(WHAT, DB)                                                                                            \
+    !vec       ? WHAT<IO, DB, false, true, true>(a, map, stream)                                                              \
+    : a.causal ? (bias ? WHAT<IO, DB, true, true, true>(a, map, stream) : WHAT<IO, DB, true, false, true>(a, map, stream))    \
+               : (bias ? WHAT<IO, DB, true, true, false>(a, map, stream) : WHAT<IO, DB, true, false, false>(a, map, stream))
 
 template <typename IO>
 hipError_t forward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {

@@ -191,7 +191,7 @@ struct AttentionArgs {
     float* lse;
     Heads d_o, dq, dk, dv;  // backward
     float* dbias;
-    float *row_lse, *row_delta, *parts;  // workspace
+    float *row_lse, *row_delta, *parts;  // workspace: -lse / |scale| and -delta of each row, sums of the biases' gradients
     int out_vec, dq_vec, dk_vec, dv_vec;  // rows of an output in whole pieces of four
 };
 size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, bool backward);
