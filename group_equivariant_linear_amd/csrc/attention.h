@@ -192,30 +192,44 @@ __device__ __forceinline__ void slot_of(const int64_t* offsets, int64_t batch, i
         row = (int64_t)(slot - (uint32_t)b * per) * kRows;
         return;
     }
-    int64_t lo = 0, hi = batch - 1;  // last b whose first slot is at most `slot`
-    while (lo < hi) {
-        const int64_t mid = lo + (hi - lo + 1) / 2;
-        if (clamped(offsets, mid, T) / kRows + mid <= slot) lo = mid;
-        else hi = mid - 1;
+    // last b whose first slot is at most `slot`: 64 of them looked at in one load
+    const int lane = (int)threadIdx.x & 63;
+    int64_t lo = 0, n = batch;
+    while (n > 1) {
+        const int64_t step = (n + 63) / 64, at = lane * step;
+        const bool yes = at < n && clamped(offsets, lo + at, T) / kRows + lo + at <= slot;
+        const int last = __popcll(__ballot(yes)) - 1;  // (first slots ascend)
+        const int64_t from = (last < 0 ? 0 : last) * step;
+        lo += from;
+        n = n - from < step ? n - from : step;
     }
     b = lo;
     row = ((int64_t)slot - clamped(offsets, lo, T) / kRows - lo) * kRows;
 }
 
-// Biases (times log2 e) of the distances -(reach + kPad) .. reach + kPad, at distance +
-// reach + kPad of `tab`.
-template <typename IO>
-__device__ __forceinline__ float bias_of(const AttentionArgs& a, const BucketMap& map, int head, int distance) {
-    const int n = distance < 0 ? -distance : distance;
-    const int b = map.of[n < a.reach ? n : a.reach] + (distance < 0 && !a.causal ? a.buckets / 2 : 0);
-    return (float)((const IO*)a.bias)[(int64_t)head * a.buckets + b];
-}
-template <typename IO>
-__device__ __forceinline__ void fill_biases(float* tab, const AttentionArgs& a, const BucketMap& map, int head) {
-    const int off = a.reach + kPad;
-    for (int x = (int)threadIdx.x; x <= 2 * off; x += 256) tab[x] = a.bias ? kLog2e * bias_of<IO>(a, map, head, x - off) : 0.0f;
-}
+// Biases (times log2 e) of the distances -(reach + kPad) .. reach + kPad, at distance + reach +
+// kPad of `tab`; behind them the least distance of each bucket of one side, and one past the
+// reach.  scratch: LDS for the head's biases.  Ends with its writes not waited for.
 __host__ __device__ constexpr int tab_width(int reach) { return 2 * (reach + kPad) + 1; }
+__host__ __device__ constexpr int table_words(int reach, int buckets) { return tab_width(reach) + buckets + 1; }
+template <typename IO>
+__device__ __forceinline__ void fill_biases(float* tab, float* scratch, const AttentionArgs& a, const BucketMap& map, int head) {
+    const int tid = (int)threadIdx.x, off = a.reach + kPad, side = a.causal ? a.buckets : a.buckets / 2;
+    int* const starts = reinterpret_cast<int*>(tab + tab_width(a.reach));
+    if (tid < a.buckets) scratch[tid] = a.bias ? kLog2e * (float)((const IO*)a.bias)[(int64_t)head * a.buckets + tid] : 0.0f;
+    for (int i = tid; i <= side; i += 256) starts[i] = map.start[i];
+    __syncthreads();
+    for (int x = tid; x <= 2 * off; x += 256) {
+        const int d = x - off, m = d < 0 ? -d : d, n = m < a.reach ? m : a.reach;
+        int lo = 0, hi = side - 1;  // last bucket that starts at n or before
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (starts[mid] <= n) lo = mid;
+            else hi = mid - 1;
+        }
+        tab[x] = a.bias ? scratch[lo + (d < 0 && !a.causal ? side : 0)] : 0.0f;
+    }
+}
 
 // Fragments of 32 rows from memory, the operand of the products over the head's numbers.
 template <class C, typename IO, typename F, bool VEC>
@@ -366,7 +380,7 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     using F = typename O::F;
     __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
     __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
-    extern __shared__ float tab[];  // [tab_width(reach)] with biases
+    extern __shared__ float tab[];  // with biases: fill_biases'
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
     const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
@@ -381,7 +395,7 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
 
     F q[C::NS];
     load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
-    if constexpr (BIAS) fill_biases<IO>(tab, a, map, head);
+    if constexpr (BIAS) fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
     f32x16 acc[DB];
     clear(acc);
     float top = -kInf, total = 0.0f, ref = -kShift<IO>;
@@ -563,7 +577,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
     __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
     __shared__ float far_sums[BIAS ? 8 : 1];
-    extern __shared__ float tab[];  // [width] with biases, [8][width] with their gradients
+    extern __shared__ float tab[];  // with biases: fill_biases', then [8][width] with their gradients
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x) + base;
     const int head = (int)(id / a.slots), kv = head / (a.heads / a.kv_heads);
     const uint32_t slot = id % a.slots;
@@ -579,9 +593,9 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
     const int my = w0 + (lane & 31);
     const int width = tab_width(a.reach);
-    float* const sums = tab + width;
+    float* const sums = tab + table_words(a.reach, a.buckets);
     if constexpr (BIAS) {
-        fill_biases<IO>(tab, a, map, head);
+        fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
         if (a.dbias)
             for (int x = tid; x < 8 * width; x += 256) sums[x] = 0.0f;
     }
@@ -700,7 +714,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             } else if (a.dbias) {
                 float near = 0.0f, wrap = 0.0f;
                 add_diagonals(x[0], near, wrap);
-                lds_float* const t = (lds_float*)tab + (2 * wave + h + 1) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
+                lds_float* const t = (lds_float*)tab + table_words(a.reach, a.buckets) + (2 * wave + h) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
                 __hip_atomic_fetch_add(t, near, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
                 __hip_atomic_fetch_add(t - 32, wrap, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
             }
@@ -756,26 +770,23 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             sums[x] = t;
         }
         __syncthreads();
+        // a bucket's distances are added up by the lanes of a wave
         const int side = a.causal ? a.buckets : a.buckets / 2;
-        if (tid < a.buckets) {
-            const bool before = tid < side;  // the key comes before the query (or is its own)
-            const int want = before ? tid : tid - side;
-            auto first = [&](int bucket) {  // least distance of a bucket, or one past the reach
-                int lo = 0, hi = a.reach + 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi) / 2;
-                    if (map.of[mid] >= bucket) hi = mid;
-                    else lo = mid + 1;
-                }
-                return lo;
-            };
-            int x0 = first(want), x1 = want == side - 1 ? a.reach + kPad + 1 : first(want + 1);
+        const int* const starts = reinterpret_cast<const int*>(tab + width);
+        for (int bucket = wave; bucket < a.buckets; bucket += 4) {
+            const bool before = bucket < side;  // the key comes before the query (or is its own)
+            const int want = before ? bucket : bucket - side;
+            int x0 = starts[want];
+            const int x1 = want == side - 1 ? a.reach + kPad + 1 : starts[want + 1];
             if (!before && x0 == 0) x0 = 1;  // distance 0 is of the first side
-            float t = want == side - 1 ? (before ? far_sums[0] + far_sums[1] + far_sums[2] + far_sums[3]
-                                                 : far_sums[4] + far_sums[5] + far_sums[6] + far_sums[7])
-                                       : 0.0f;
-            for (int x = x0; x < x1; ++x) t += sums[a.reach + kPad + (before ? x : -x)];
-            a.parts[((int64_t)head * a.buckets + tid) * a.slots + slot] = t;
+            float t = 0.0f;
+            for (int x = x0 + lane; x < x1; x += 64) t += sums[a.reach + kPad + (before ? x : -x)];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) t += __shfl_xor(t, m);
+            if (want == side - 1)
+                t += before ? far_sums[0] + far_sums[1] + far_sums[2] + far_sums[3]
+                            : far_sums[4] + far_sums[5] + far_sums[6] + far_sums[7];
+            if (lane == 0) a.parts[((int64_t)head * a.buckets + bucket) * a.slots + slot] = t;
         }
     }
 }
@@ -904,7 +915,7 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
         const int head = kv * r + hh;
         if constexpr (BIAS) {
             __syncthreads();
-            fill_biases<IO>(tab, a, map, head);
+            fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
         }
         auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
@@ -942,7 +953,7 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
 // --- host side ------------------------------------------------------------------------
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
-    const size_t table = BIAS ? tab_width(a.reach) * 4 : 0;
+    const size_t table = BIAS ? table_words(a.reach, a.buckets) * 4 : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((forward_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table, stream, a, map, base);
     });
@@ -951,7 +962,7 @@ hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t
 
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
-    const size_t table = BIAS ? tab_width(a.reach) * 4 : 0, sums = a.dbias ? 8 * table : 0;
+    const size_t table = BIAS ? table_words(a.reach, a.buckets) * 4 : 0, sums = a.dbias ? 8 * tab_width(a.reach) * 4 : 0;
     in_pieces((int64_t)a.slots * a.heads, 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
     });

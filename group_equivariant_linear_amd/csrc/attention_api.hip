@@ -18,16 +18,19 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions are ints in the k
 void fill_buckets(BucketMap& map, int side, int reach) {
     const int exact = side / 2, m = side - exact;
     const long double le = std::log((long double)exact), lr = std::log((long double)reach);
-    int j = 0;
-    for (int n = 0; n <= reach; ++n) {
-        if (n < exact) {
-            map.of[n] = (uint8_t)n;
-            continue;
-        }
+    for (int b = 0; b <= exact; ++b) map.start[b] = (uint16_t)b;
+    for (int n = exact, j = 0; n <= reach; ++n) {
         const long double ln = m * std::log((long double)n);
-        while (j + 1 < m && ln >= (m - j - 1) * le + (j + 1) * lr - 1e-13L) ++j;
-        map.of[n] = (uint8_t)(exact + j);
+        while (j + 1 < m && ln >= (m - j - 1) * le + (j + 1) * lr - 1e-13L) map.start[exact + ++j] = (uint16_t)n;
     }
+    map.start[side] = (uint16_t)(reach + 1);
+}
+
+// Bucket of distance n <= reach on one side: the last that starts there or before.
+int bucket_of(const BucketMap& map, int side, int n) {
+    int b = side - 1;
+    while (map.start[b] > n) --b;
+    return b;
 }
 
 // A cache tensor [blocks][block_size][kv_heads][D]: extents that stay far from the end of
@@ -138,8 +141,9 @@ eqlinear_status eqlinear_attention_plan(eqlinear_plan_t* out, int N, int heads, 
 int eqlinear_attention_bucket(eqlinear_plan_t p, int64_t distance) {
     if (!p || p->kind != EQL_KIND_ATTENTION || !p->buckets) return -1;
     if (distance < 0 && p->causal) return -1;
-    if (distance < 0) return p->map.of[distance > -p->reach ? -distance : p->reach] + p->buckets / 2;
-    return p->map.of[distance < p->reach ? distance : p->reach];
+    const int side = p->causal ? p->buckets : p->buckets / 2;
+    if (distance < 0) return bucket_of(p->map, side, distance > -p->reach ? (int)-distance : p->reach) + side;
+    return bucket_of(p->map, side, distance < p->reach ? (int)distance : p->reach);
 }
 
 size_t eqlinear_attention_workspace(eqlinear_plan_t p, int64_t T, int64_t T_kv, int64_t batch, int backward) {
@@ -270,6 +274,7 @@ eqlinear_status eqlinear_attention_step(eqlinear_plan_t p, const eqlinear_heads*
     a.scale = scale;
     a.bias = bias;
     a.buckets = p->buckets, a.reach = p->reach;
+    a.side = p->causal ? p->buckets : p->buckets / 2;
     a.lse = lse;
     return status_of(launch_attention_step(p->dtype, a, p->map, workspace, (hipStream_t)stream));
 }

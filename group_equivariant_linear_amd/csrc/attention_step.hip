@@ -90,8 +90,9 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
     float* const biases = reinterpret_cast<float*>(shared + (g.shared ? 2 * a.batch + 1 : 0));
     uint8_t* const buckets = reinterpret_cast<uint8_t*>(biases + kQueries * a.buckets);
 
-    if (a.bias)
-        for (int i = tid; i <= a.reach; i += 256) buckets[i] = map.of[i];
+    if (a.bias)  // each bucket marks its distances (the step is causal: all past ones are on the first side)
+        for (int i = tid; i < a.side; i += 256)
+            for (int x = map.start[i]; x < map.start[i + 1]; ++x) buckets[x] = (uint8_t)i;
     int64_t u0, u1;
     if (g.shared) {
         constexpr int N = kMaxShared / 256;
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
         for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         float top = -kInf, total = 0.0f;
         char* const tv = lds[wave];
-        const float far = a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.buckets_last] : 0.0f;
+        const float far = a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.side - 1] : 0.0f;
         for (int j0 = j_first; j0 < k1; j0 += kUnit) {
             f32x4 x[2];
 #pragma unroll
@@ -466,7 +467,7 @@ template <typename IO>
 hipError_t run(StepArgs a, const BucketMap& map, float* ws, hipStream_t stream) {
     const size_t es = sizeof(IO);
     a.q_vec = vec_ok(a.q, a.D_k, es, 16);
-    a.buckets_last = a.buckets ? map.of[a.reach] : 0;
+    
     auto vec = [&](const Pages& x, int D) {
         return (uintptr_t)x.p % 16 == 0 && x.bs * es % 16 == 0 && x.ts * es % 16 == 0 && x.hs * es % 16 == 0 && D * es % 16 == 0;
     };

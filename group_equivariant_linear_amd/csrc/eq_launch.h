@@ -173,10 +173,11 @@ hipError_t launch_linear_attention(int io, const MixArgs& a, void* ws, hipStream
 hipError_t launch_linear_attention_backward(int io, const MixArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_linear_attention_step(int io, const MixArgs& a, hipStream_t stream);
 
-// attention*.hip.  of: bucket of the distances 0 .. reach on one side.
+// attention*.hip.  start: the least distance of each bucket of one side, and one past the reach
+// (a bucket without distances starts where the next one does).
 constexpr int kMaxBuckets = 256, kMaxReach = 1024;
 struct BucketMap {
-    uint8_t of[kMaxReach + 1];
+    uint16_t start[kMaxBuckets + 1];
 };
 struct AttentionArgs {
     uint32_t slots, kv_slots;  // runs of rows of all sequences
@@ -214,7 +215,8 @@ struct StepArgs {
     const void* bias;
     int buckets, reach;
     float* lse;
-    int q_vec, buckets_last;  // rows of q in whole pieces; the bucket of all distances past the reach
+    int side;   // buckets of past distances
+    int q_vec;  // rows of q in whole pieces
 };
 size_t attention_step_workspace(int io, int heads, int kv_heads, int D_k, int D_v, int64_t batch);
 hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream);
