@@ -254,12 +254,26 @@ __device__ __forceinline__ void load_rows(F (&f)[C::NS], const Heads& x, int64_t
     }
 }
 
+// Waits for fragments loaded from memory.  (Otherwise each pass of a loop waits for them at
+// their use, and with them for the tiles in flight, which the compiler does not count.)
+template <typename F, int N>
+__device__ __forceinline__ void arrive(F (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i]));
+}
+
 // The numbers of fragments with their signs turned.
 template <typename F, int N>
 __device__ __forceinline__ void negate(F (&f)[N]) {
     constexpr uint32_t sign = sizeof(f[0][0]) == 2 ? 0x80008000u : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = __builtin_bit_cast(F, __builtin_bit_cast(u32x4, f[i]) ^ sign);
+}
+
+// The larger of a lane's number and its partner's (lane ^ 32).
+__device__ __forceinline__ float half_max(float v) {
+    const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
 }
 
 // Accumulators of 32 rows to memory, times m, rounded once.
@@ -401,6 +415,7 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     float top = -kInf, total = 0.0f, ref = -kShift<IO>;
     const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
     if (a.scale < 0.0f) negate(q);
+    arrive(q);
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;  // last key that it sees
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
     // keys that some of the workgroup's rows see; tiles that all of them do
@@ -411,102 +426,156 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
     const RowFrags<C> rows(lds[0]);
     const ColumnFrags<C, O> cols(lds[0] + C::TILE);
-    // Keys j0 .. of the tiles at `by`.  Scores come relative to `ref`, in powers of two.
-    auto tile = [&](auto kind, int j0, int by) __attribute__((always_inline)) {
+    constexpr int S1 = (kStages<C> - 1) * 2 * C::TILE;  // from one stage to the other
+    const int n_tiles = tiles(end), blocks = n_rows > 0 && wave_end > 0 ? (wave_end + 31) / 32 : 0;  // blocks that the wave works on
+    auto load_k = [&](int t) {
+        const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        if (t < n_tiles) lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[t & (kStages<C> - 1)]);
+    };
+    auto load_v = [&](int t) {
+        const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        if (t < n_tiles) lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[t & (kStages<C> - 1)] + C::TILE);
+    };
+    f32x16 x = {};  // scores of the block at hand
+    F p[C::NT];     // probabilities of the one before
+    // Scores of block kb of the tile at `by`.
+    auto scores = [&](f32x16& y, int kb, int by) __attribute__((always_inline)) {
+        y = f32x16{};
+#pragma unroll
+        for (int st = 0; st < C::NS; ++st) O::mma(y, rows.template get<F>(by, kb, st), q[st]);
+    };
+    // Block n's probabilities, packed, from its scores in x; between() before the sums are scaled.
+    auto probabilities = [&](auto kind, int n, auto&& between) __attribute__((always_inline)) {
         constexpr int K = decltype(kind)::value;
-        f32x16 x[2];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            x[kb] = f32x16{};
-#pragma unroll
-            for (int st = 0; st < C::NS; ++st) O::mma(x[kb], rows.template get<F>(by, kb, st), q[st]);
-        }
+        const int j = 32 * n;
         if constexpr (BIAS) {
-            const int from = w0 + shift - j0;  // distance of the wave's first row and the tile's first key
+            const int from = w0 + shift - j;  // distance of the wave's first row and the block's first key
             const float* t = tab + a.reach + kPad;
-            if (from - 63 >= a.reach || from + 31 <= -a.reach) {
-                const float f = t[from > 0 ? a.reach : -a.reach];
+            // (the far ones share a value: no other way, which would part the products from it)
+            const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
+            t += far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, f);
-            } else {
-                t += from + (lane & 31) - 4 * h;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, t[-(32 * kb + row_of(i))]);
-            }
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[-row_of(i)]);
         }
         if constexpr (K != kWhole) {
-            const int lim = last - j0 - 4 * h;
+            const int lim = last - j - 4 * h;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[kb][i] = 32 * kb + row_of(i) <= lim ? x[kb][i] : -kInf;
+            for (int i = 0; i < 16; ++i) x[i] = row_of(i) <= lim ? x[i] : -kInf;
         }
-        float mx = -kInf;
+        float mx = x[0];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[kb][i]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+        mx = half_max(mx);
         if constexpr (!BIAS) mx *= scale;
-        if (__any(mx > top + kSlack<IO>)) {
-            // (a row without scores so far has sums of 0, and none of its terms is counted against -infinity)
-            const float now = mx > top + kSlack<IO> ? mx : top;
-            const float c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
-            top = now;
-            ref = (top == -kInf ? 0.0f : top) - kShift<IO>;
+        const bool grown = mx > top + kSlack<IO>;
+        // (a row without scores so far has sums of 0, and none of its terms is counted against -infinity)
+        const float now = grown ? mx : top, c = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+        top = now;
+        ref = (top == -kInf ? 0.0f : top) - kShift<IO>;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(BIAS ? x[i] - ref : __builtin_fmaf(x[i], scale, -ref));
+        between();
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t) {
+            float w[C::E];
+#pragma unroll
+            for (int e = 0; e < C::E; ++e) w[e] = x[t * C::E + e];
+            p[t] = O::pack(w);
+        }
+        float sum = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) sum += x[i];
+        if (__any(grown)) {
             total *= c;
             asm volatile("");  // (rare: not to be computed beside the other way)
 #pragma unroll
             for (int cb = 0; cb < DB; ++cb) acc[cb] *= c;
         }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[kb][i] = __builtin_amdgcn_exp2f(BIAS ? x[kb][i] - ref : __builtin_fmaf(x[kb][i], scale, -ref));
-                total += x[kb][i];
-            }
+        total += sum;
+    };
+    // The product of block n's probabilities with v: block kb of the tile at `by`.
+    auto product = [&](auto kind, int n, int by, int kb) __attribute__((always_inline)) {
+        constexpr int K = decltype(kind)::value;
         uint32_t odd = 0;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int t = 0; t < C::NT; ++t)
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t) {
-                float w[C::E];
-#pragma unroll
-                for (int e = 0; e < C::E; ++e) w[e] = x[kb][t * C::E + e];
-                const F p = O::pack(w);
-#pragma unroll
-                for (int cb = 0; cb < DB; ++cb) {
-                    F v[1] = {cols.get(by, kb, t, cb)};
-                    if constexpr (K == kUnseen) {
-                        const uint32_t o = O::top(v);
-                        odd = o > odd ? o : odd;
-                        v[0] = O::finite(v[0]);
-                    }
-                    O::mma(acc[cb], v[0], p);
+            for (int cb = 0; cb < DB; ++cb) {
+                F v[1] = {cols.get(by, kb, t, cb)};
+                if constexpr (K == kUnseen) {
+                    const uint32_t o = O::top(v);
+                    odd = o > odd ? o : odd;
+                    v[0] = O::finite(v[0]);
                 }
+                O::mma(acc[cb], v[0], p[t]);
             }
         if (K == kUnseen && __any(odd >= O::kInf))
-            add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by, kTile, last - j0, false, found[wave]);
+            add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), 32, last - 32 * n, false, found[wave]);
     };
-    auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
-        if (n_rows > 0 && t * kTile < wave_end) tile(kind, t * kTile, stage * 2 * C::TILE);
-    };
-    pass_over<C>(
-        whole, tiles(end) - whole,
-        [&](int t, int stage) {
-            const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
-            lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[stage]);
-            lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
-        },
-        [&](int t, int stage) {
-            if (n_rows > 0) tile(Kind<kWhole>{}, t * kTile, stage * 2 * C::TILE);
-        },
-        [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
+    using Edge = Kind<UNSEEN ? kUnseen : kPartial>;
+    if constexpr (kStages<C> == 2) {
+        // While a wave makes block n's probabilities, its matrix core has block n + 1's scores and
+        // block n - 1's product to make: v follows k by a block, and a tile's v is there one visit
+        // later than its k.
+        __syncthreads();
+        load_k(0), load_v(0);
+        wait_loads();
+        __syncthreads();
+        load_k(1);
+        f32x16 y;
+        if (blocks > 0) {
+            scores(x, 0, 0);
+            scores(y, 1, 0);
+            probabilities(Edge{}, 0, [] {});
+            x = y;
+        }
+        auto next = [&](int t) {
+            wait_loads();  // k of tile t + 1, v of tile t
+            __syncthreads();
+            load_k(t + 2), load_v(t + 1);
+        };
+        auto block = [&](auto kind, int n, int by_k, int by_v, int kb) __attribute__((always_inline)) {
+            scores(y, kb, by_k);  // (past the last key: of anything, and not used)
+            probabilities(kind, n, [&]() __attribute__((always_inline)) { product(kind, n - 1, by_v, kb); });
+            x = y;
+        };
+        int t = 0;
+        for (; t + 1 < whole; ++t) {
+            next(t);
+            const int by_v = (t & 1) * S1, by_k = S1 - by_v;
+            if (blocks > 0) {
+                block(Kind<kWhole>{}, 2 * t + 1, by_k, by_v, 0);
+                block(Kind<kWhole>{}, 2 * t + 2, by_k, by_v, 1);
+            }
+        }
+        for (; t < n_tiles; ++t) {
+            next(t);
+            const int by_v = (t & 1) * S1, by_k = S1 - by_v;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int n = 2 * t + 1 + kb;
+                if (n < blocks) block(Edge{}, n, by_k, by_v, kb);
+                else if (n == blocks) product(Edge{}, n - 1, by_v, kb);
+            }
+        }
+    } else {
+        auto tile = [&](auto kind, int t) __attribute__((always_inline)) {
+            __syncthreads();
+            load_k(t), load_v(t);
+            wait_loads();
+            __syncthreads();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (2 * t + kb < blocks) {
+                    scores(x, kb, 0);
+                    probabilities(kind, 2 * t + kb, [] {});
+                    product(kind, 2 * t + kb, 0, kb);
+                }
+        };
+        int t = 0;
+        for (; t < whole; ++t) tile(Kind<kWhole>{}, t);
+        for (; t < n_tiles; ++t) tile(Edge{}, t);
+    }
     if (n_rows <= 0) return;
     total += __shfl_xor(total, 32);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
@@ -563,12 +632,11 @@ __device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, floa
 // difference) shows twofold and the biases' fp32 gradients by 1e-3 of their size.  It also
 // takes lse's own rounding out of P (sum P = 1), and leaves both for dkv_kernel.  The second
 // makes dS.  Of the biases, dS is summed by distance: along the diagonals of a block in
-// registers, then into an array for each half of each wave (the lanes of an instruction hold 32
-// distances apiece, all different, and a wave's instructions come in order: the sums do not
-// depend on timing); distances past the reach share a bucket on either side and are summed
-// in registers.  (One LDS addition for each of a block's 16 accumulators instead of its diagonals
-// took the kernel from 140 to 370 us in packed training on images.)  A workgroup writes the sums
-// of its buckets; reduce_kernel joins those of a head.
+// registers, then into an array for each half of each wave (its own: read, added to, written);
+// distances past the reach share a bucket on either side and are summed in registers.  (In
+// packed training on images the kernel took 370 us with one LDS atomic for each of a block's 16
+// accumulators, 124 with two for its diagonals, 80 without any.)  A workgroup writes the
+// sums of its buckets; reduce_kernel joins those of a head.
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
@@ -622,6 +690,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
     const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
     if (a.scale < 0.0f) negate(q);
+    arrive(q), arrive(d_o);
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
@@ -712,11 +781,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
                 if (from > 0) far_pos += t;
                 else far_neg += t;
             } else if (a.dbias) {
-                float near = 0.0f, wrap = 0.0f;
-                add_diagonals(x[0], near, wrap);
                 lds_float* const t = (lds_float*)tab + table_words(a.reach, a.buckets) + (2 * wave + h) * width + a.reach + kPad + from + (lane & 31) - 4 * h;
-                __hip_atomic_fetch_add(t, near, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                __hip_atomic_fetch_add(t - 32, wrap, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                float near = t[0], wrap = t[-32];
+                add_diagonals(x[0], near, wrap);
+                t[0] = near, t[-32] = wrap;
             }
         }
         const float f = hold<IO>(x, held, acc);
@@ -822,6 +890,8 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     float held = kTopScale;
     const float scale = fabsf(a.scale) * kLog2e;  // the keys take its sign
     if (a.scale < 0.0f) negate(k);
+    arrive(k);
+    if constexpr (DK) arrive(v);
     // Tiles of queries from the first that sees one of the workgroup's keys: t_edge .. t_whole - 1
     // see all of them and are visited first, then those before, then the last, if it is not whole.
     const int t_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile : 0;
