@@ -38,6 +38,14 @@ uint32_t slots_for(const int64_t* offsets, int64_t batch, int64_t T) {
     return (uint32_t)(offsets ? T / kRows + batch : batch * ((T / batch + kRows - 1) / kRows));
 }
 
+// Dealt are sequences of 16 slots and more.
+Deal deal_for(const int64_t* offsets, int64_t batch, int64_t T, int heads) {
+    const uint32_t slots = slots_for(offsets, batch, T);
+    if (slots == 0 || T / batch < 16 * kRows) return Deal{slots, 0, 0};
+    if (offsets) return Deal{slots, (uint32_t)heads, 1};
+    return Deal{slots / (uint32_t)batch, (uint32_t)(heads * batch), (uint32_t)batch};
+}
+
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -51,7 +59,8 @@ size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, boo
 hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipStream_t stream) {
     if (a.T <= 0) return hipSuccess;
     a.slots = slots_for(a.offsets, a.batch, a.T);
-    if ((int64_t)a.slots * a.heads > 0x7fffffff) return hipErrorNotSupported;
+    a.deal = deal_for(a.offsets, a.batch, a.T, a.heads);
+    if (a.deal.workgroups(a.heads) > 0x7fffffff) return hipErrorNotSupported;
     return io == kIoF32 ? att::forward<float>(a, map, stream)
                         : (io == kIoBF16 ? att::forward<__bf16>(a, map, stream) : att::forward<_Float16>(a, map, stream));
 }
@@ -62,8 +71,9 @@ hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& m
     a.row_delta = reinterpret_cast<float*>(static_cast<char*>(ws) + n);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n);
     a.slots = slots_for(a.offsets, a.batch, a.T);
-    a.kv_slots = slots_for(a.kv_offsets, a.batch, a.T_kv);
-    if ((int64_t)a.slots * a.heads > 0x7fffffff || (int64_t)a.kv_slots * a.kv_heads > 0x7fffffff) return hipErrorNotSupported;
+    a.deal = deal_for(a.offsets, a.batch, a.T, a.heads);
+    a.kv_deal = deal_for(a.kv_offsets, a.batch, a.T_kv, a.kv_heads);
+    if (a.deal.workgroups(a.heads) > 0x7fffffff || a.kv_deal.workgroups(a.kv_heads) > 0x7fffffff) return hipErrorNotSupported;
     const hipError_t e = io == kIoF32 ? att::backward<float>(a, map, stream)
                          : io == kIoBF16 ? att::backward<__bf16>(a, map, stream)
                                          : att::backward<_Float16>(a, map, stream);

@@ -179,8 +179,17 @@ constexpr int kMaxBuckets = 256, kMaxReach = 1024;
 struct BucketMap {
     uint16_t start[kMaxBuckets + 1];
 };
+// How workgroups take the slots of a launch (place_of in attention.h).
+struct Deal {
+    uint32_t slots, units, per_head;  // slots and number of units, units of a head; not dealt: slots of all, 0
+    __host__ __device__ constexpr int64_t workgroups(int heads) const {
+        if (units == 0) return (int64_t)slots * heads;
+        return 8 * ((int64_t)(units / 8) * slots + (int64_t)(units % 8) * ((slots + 7) / 8));
+    }
+};
 struct AttentionArgs {
-    uint32_t slots, kv_slots;  // runs of rows of all sequences
+    uint32_t slots;      // runs of rows of all sequences
+    Deal deal, kv_deal;  // how workgroups take them, and those of keys
     int causal;
     float scale;
     int64_t batch, T, T_kv;
