@@ -244,14 +244,14 @@ __device__ __forceinline__ Place place_of(uint32_t base, const Deal& d, bool fal
 // reach.  scratch: LDS for the head's biases.  Ends with its writes not waited for.
 __host__ __device__ constexpr int tab_width(int reach) { return 2 * (reach + kPad) + 1; }
 __host__ __device__ constexpr int table_words(int reach, int buckets) { return tab_width(reach) + buckets + 1; }
-template <typename IO>
+template <typename IO, int THREADS = 256>
 __device__ __forceinline__ void fill_biases(float* tab, float* scratch, const AttentionArgs& a, const BucketMap& map, int head) {
     const int tid = (int)threadIdx.x, off = a.reach + kPad, side = a.causal ? a.buckets : a.buckets / 2;
     int* const starts = reinterpret_cast<int*>(tab + tab_width(a.reach));
     if (tid < a.buckets) scratch[tid] = a.bias ? kLog2e * (float)((const IO*)a.bias)[(int64_t)head * a.buckets + tid] : 0.0f;
-    for (int i = tid; i <= side; i += 256) starts[i] = map.start[i];
+    for (int i = tid; i <= side; i += THREADS) starts[i] = map.start[i];
     __syncthreads();
-    for (int x = tid; x <= 2 * off; x += 256) {
+    for (int x = tid; x <= 2 * off; x += THREADS) {
         const int d = x - off, m = d < 0 ? -d : d, n = m < a.reach ? m : a.reach;
         int lo = 0, hi = side - 1;  // last bucket that starts at n or before
         while (lo < hi) {
@@ -894,20 +894,26 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
 }
 
 // Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the
-// queries of every head that shares it, in a fixed order; DK and DV: which of the two.
+// queries of every head that shares it, in a fixed order; DK and DV: which of the two.  Two groups of four waves own the same keys and take
+// every other tile of queries each; their sums are joined at the end.  (A key of a causal
+// sequence is seen by all queries after it: with one group, 512 workgroups that all run at once took as
+// long as the longest of them, 817 us for dk of 2 x 8192 tokens.)
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN, bool DK, bool DV>
-__global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+__global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
-    __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
-    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
-    __shared__ __attribute__((aligned(16))) float stats[kStages<C>][2][kTile];  // lse, delta
+    __shared__ __attribute__((aligned(16))) char tiles_of[2][kStages<C>][2 * C::TILE];
+    __shared__ __attribute__((aligned(16))) int found[8][2 * C::D];  // (add_odd_numbers)
+    __shared__ __attribute__((aligned(16))) float stats_of[2][kStages<C>][2][kTile];  // lse, delta
     extern __shared__ float tab[];
     const Place place = place_of(base, a.kv_deal, false);
     if (place.head < 0) return;
     const int kv = place.head, r = a.heads / a.kv_heads;
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave8 = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int group = wave8 >> 2, wave = wave8 & 3;
+    auto& lds = tiles_of[group];
+    auto& stats = stats_of[group];
     int64_t b, row0;
     slot_of(a.kv_offsets, a.batch, a.T_kv, place.slot, b, row0);
     Seq s;
@@ -934,7 +940,9 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     const int t_whole = s.n_q / kTile, tail = s.n_q % kTile && t_first <= t_whole ? 1 : 0;
     const int t_edge = t_all < t_whole ? (t_all > t_first ? t_all : t_first) : t_whole;  // edge tiles: t_first .. t_edge - 1
     const int n_whole = t_whole > t_edge ? t_whole - t_edge : 0, n_early = t_edge > t_first ? t_edge - t_first : 0;
-    auto row_at = [&](int t) {
+    const int n_all = n_whole + n_early + tail;
+    auto row_at = [&](int v) {  // of the group's visit v
+        int t = 2 * v + group;
         t -= n_whole;
         return (t < 0 ? t + n_whole + t_edge : (t < n_early ? t_first + t : t_whole)) * kTile;
     };
@@ -1012,27 +1020,28 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
         if constexpr (DK) product(dk, by, ds[0]);
         if (K == kUnseen && __any(odd >= O::kInf)) {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
-            if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave]);
-            if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave]);
+            if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave8]);
+            if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave8]);
         }
     };
     for (int hh = 0; hh < r; ++hh) {
         const int head = kv * r + hh;
         if constexpr (BIAS) {
             __syncthreads();
-            fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
+            fill_biases<IO, 512>(tab, reinterpret_cast<float*>(tiles_of), a, map, head);
         }
         auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
             for (int qb = 0; qb < 2; ++qb) {
                 const int q0 = row_at(t) + 32 * qb;
-                if (n_rows > 0 && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
+                if (n_rows > 0 && 2 * t + group < n_all && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
                     block(kind, q0, qb, stage * 2 * C::TILE, stats[stage]);
             }
         };
         pass_over<C>(
-            n_whole, n_early + tail,
+            n_whole / 2, (n_all + 1) / 2 - n_whole / 2,
             [&](int t, int stage) {
+                if (2 * t + group >= n_all) return;
                 const int i0 = row_at(t), n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
                 lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
                 lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
@@ -1048,11 +1057,40 @@ __global__ __launch_bounds__(256, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
             },
             [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
     }
-    if (n_rows <= 0) return;
+    // The other group's sums, in LDS in the accumulators' order, 4 KB for a wave and 32 columns
+    // (as many tiles as they are wide hold them).
+    static_assert((DK && DV ? 2 : 1) * DB * 4 * 4096 <= (int)sizeof(tiles_of), "the sums fit the tiles");
     const bool half = std::is_same_v<IO, _Float16>;
-    if constexpr (DK)
-        store_rows<C, IO>(dk, a.dk, s.k0 + w0, kv, n_rows, a.D_k, half ? a.scale * inverse_of_power(held) : a.scale, a.dk_vec);
-    if constexpr (DV) store_rows<C, IO>(dv, a.dv, s.k0 + w0, kv, n_rows, a.D_v, half ? 1.0f / 4096.0f : 1.0f, a.dv_vec);
+    const float mk = half ? a.scale * inverse_of_power(held) : a.scale, mv = half ? 1.0f / 4096.0f : 1.0f;
+    float* const other = reinterpret_cast<float*>(tiles_of) + wave * (DB * 1024) + lane;
+    auto pass = [&](f32x16 (&acc)[DB], float m, float* to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int cb = 0; cb < DB; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                acc[cb][i] *= m;
+                if (group) to[(16 * cb + i) * 64] = acc[cb][i];
+            }
+    };
+    __syncthreads();
+    if constexpr (DK) pass(dk, mk, other);
+    if constexpr (DV) pass(dv, mv, other + (DK ? 4 * DB * 1024 : 0));
+    __syncthreads();
+    if (group || n_rows <= 0) return;
+    auto join = [&](f32x16 (&acc)[DB], const float* from) __attribute__((always_inline)) {
+#pragma unroll
+        for (int cb = 0; cb < DB; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[cb][i] += from[(16 * cb + i) * 64];
+    };
+    if constexpr (DK) {
+        join(dk, other);
+        store_rows<C, IO>(dk, a.dk, s.k0 + w0, kv, n_rows, a.D_k, 1.0f, a.dk_vec);
+    }
+    if constexpr (DV) {
+        join(dv, other + (DK ? 4 * DB * 1024 : 0));
+        store_rows<C, IO>(dv, a.dv, s.k0 + w0, kv, n_rows, a.D_v, 1.0f, a.dv_vec);
+    }
 }
 
 // --- host side ------------------------------------------------------------------------
@@ -1071,12 +1109,12 @@ hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_
     in_pieces(a.deal.workgroups(a.heads), 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
     });
-    in_pieces(a.kv_deal.workgroups(a.kv_heads), 256, [&](uint32_t base, uint32_t wgs) {
+    in_pieces(a.kv_deal.workgroups(a.kv_heads), 512, [&](uint32_t base, uint32_t wgs) {
         if constexpr (dkv_apart(sizeof(IO), DB)) {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, false>), dim3(wgs), dim3(256), table, stream, a, map, base);
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, false, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, false>), dim3(wgs), dim3(512), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, false, true>), dim3(wgs), dim3(512), table, stream, a, map, base);
         } else {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, true>), dim3(wgs), dim3(256), table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, true>), dim3(wgs), dim3(512), table, stream, a, map, base);
         }
     });
     return hipGetLastError();
