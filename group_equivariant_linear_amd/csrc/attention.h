@@ -374,15 +374,22 @@ constexpr int kWhole = 0, kPartial = 1, kUnseen = 2;
 template <int K>
 using Kind = std::integral_constant<int, K>;
 
-// Visits n_a + n_b pairs of tiles: load(v, stage) of visit v, then, when its tiles are there,
-// a(v, stage) for the first n_a visits and b(v, stage) for the others.  Every wave calls it, and
-// a() and b() have no barrier.  (Loops of their own: work with and without masks in one, by a
-// branch, costs half as many registers again.)
-template <class C, typename L, typename A, typename B>
-__device__ __forceinline__ void pass_over(int n_a, int n_b, L&& load, A&& a, B&& b) {
-    const int n = n_a + n_b;
-    int stage = 0;
-    auto next = [&](int v) {
+// `rounds` rounds of visits to n_a + n_b pairs of tiles: load(v, stage) of visit v (counted through
+// all rounds), then, when its tiles are there, a(v, stage) for a round's first n_a visits and
+// b(v, stage) for the others; between(r) after round r.  Every wave calls it, and a() and b() have no
+// barrier.  start_pass() before it loads the first tiles: early, as the rest of what a
+// kernel starts with can be on its way at the same time.  (Loops of their own for a and b: work with
+// and without masks in one, by a branch, costs half as many registers again.)
+template <class C, typename L>
+__device__ __forceinline__ void start_pass(int visits, L&& load) {
+    if constexpr (kStages<C> == 2)
+        if (visits > 0) load(0, 0);
+}
+template <class C, typename L, typename A, typename B, typename R>
+__device__ __forceinline__ void pass_over(int rounds, int n_a, int n_b, L&& load, A&& a, B&& b, R&& between) {
+    const int n = rounds * (n_a + n_b);
+    int stage = 0, v = 0;
+    auto next = [&]() __attribute__((always_inline)) {
         if constexpr (kStages<C> == 2) {
             wait_loads();
             __syncthreads();
@@ -394,18 +401,16 @@ __device__ __forceinline__ void pass_over(int n_a, int n_b, L&& load, A&& a, B&&
             __syncthreads();
         }
     };
-    if constexpr (kStages<C> == 2) {
-        __syncthreads();
-        if (n > 0) load(0, 0);
-    }
-    int v = 0;
-    for (; v < n_a; ++v, stage ^= kStages<C> - 1) {
-        next(v);
-        a(v, stage);
-    }
-    for (; v < n; ++v, stage ^= kStages<C> - 1) {
-        next(v);
-        b(v, stage);
+    for (int r = 0; r < rounds; ++r) {
+        for (int i = 0; i < n_a; ++i, ++v, stage ^= kStages<C> - 1) {
+            next();
+            a(v, stage);
+        }
+        for (int i = 0; i < n_b; ++i, ++v, stage ^= kStages<C> - 1) {
+            next();
+            b(v, stage);
+        }
+        between(r);
     }
 }
 __device__ __forceinline__ int tiles(int rows) { return rows > 0 ? (rows + kTile - 1) / kTile : 0; }
@@ -440,15 +445,10 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_q - w0;
     const int my = w0 + (lane & 31);
 
-    F q[C::NS];
-    load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
-    if constexpr (BIAS) fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
     f32x16 acc[DB];
     clear(acc);
     float top = -kInf, total = 0.0f, ref = -kShift<IO>;
     const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
-    if (a.scale < 0.0f) negate(q);
-    arrive(q);
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;  // last key that it sees
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
     // keys that some of the workgroup's rows see; tiles that all of them do
@@ -469,6 +469,13 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
         const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
         if (t < n_tiles) lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[t & (kStages<C> - 1)] + C::TILE);
     };
+    if constexpr (kStages<C> == 2) load_k(0), load_v(0);
+    F q[C::NS];
+    load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
+    if constexpr (BIAS) fill_biases<IO>(tab, reinterpret_cast<float*>(found), a, map, head);
+    if (a.scale < 0.0f) negate(q);
+    arrive(q);
+
     f32x16 x = {};  // scores of the block at hand
     F p[C::NT];     // probabilities of the one before
     // Scores of block kb of the tile at `by`.
@@ -550,8 +557,6 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
         // While a wave makes block n's probabilities, its matrix core has block n + 1's scores and
         // block n - 1's product to make: v follows k by a block, and a tile's v is there one visit
         // later than its k.
-        __syncthreads();
-        load_k(0), load_v(0);
         wait_loads();
         __syncthreads();
         load_k(1);
@@ -696,8 +701,28 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     const int my = w0 + (lane & 31);
     const int width = tab_width(a.reach);
     float* const sums = tab + table_words(a.reach, a.buckets);
+    f32x16 acc[DB];
+    clear(acc);
+    float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
+    const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
+    const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
+    const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
+    const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
+    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
+
+    constexpr int NP = (C::P + 3) / 4;
+    const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
+    const RowFrags<C> krows(lds[0]);  // (v's tile lies C::TILE behind k's)
+    const ColumnFrags<C, O> kcols(lds[0]);
+    auto load = [&](int t, int stage) {
+        const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
+        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[stage]);
+        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
+    };
+    const int visits = tiles(end);
+    start_pass<C>(visits, load);
     if constexpr (BIAS) {
-        fill_biases<IO>(tab, reinterpret_cast<float*>(lds[0]), a, map, head);
+        fill_biases<IO>(tab, reinterpret_cast<float*>(found), a, map, head);
         if (a.dbias)
             for (int x = tid; x < 8 * width; x += 256) sums[x] = 0.0f;
     }
@@ -719,26 +744,8 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             for (int e = 0; e < C::E; ++e) delta = __builtin_fmaf(O::get(o[st], e), O::get(d_o[st], e), delta);
         delta += __shfl_xor(delta, 32);
     }
-    f32x16 acc[DB];
-    clear(acc);
-    float held = kTopScale, far_pos = 0.0f, far_neg = 0.0f;
-    const float scale = fabsf(a.scale) * kLog2e;  // the queries take its sign
     if (a.scale < 0.0f) negate(q);
     arrive(q), arrive(d_o);
-    const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
-    const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
-    const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
-    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
-
-    constexpr int NP = (C::P + 3) / 4;
-    const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
-    const RowFrags<C> krows(lds[0]);  // (v's tile lies C::TILE behind k's)
-    const ColumnFrags<C, O> kcols(lds[0]);
-    auto load = [&](int t, int stage) {
-        const int j0 = t * kTile, n = s.n_k - j0 < kTile ? s.n_k - j0 : kTile;
-        lk.run(a.k, s.k0 + j0, kv, n, a.D_k, 0, wave, 4, lds[stage]);
-        lv.run(a.v, s.k0 + j0, kv, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
-    };
     // Probabilities and dP of 32 keys from j on, at block kb of the tiles at `by`.
     auto scores = [&](f32x16& x, f32x16& dp, int j, int kb, int by) __attribute__((always_inline)) {
         x = f32x16{}, dp = f32x16{};
@@ -786,8 +793,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         }
     };
     pass_over<C>(
-        whole, tiles(end) - whole, load, [&](int t, int stage) { first(false, t, stage); },
-        [&](int t, int stage) { first(true, t, stage); });
+        1, whole, visits - whole, load, [&](int t, int stage) { first(false, t, stage); },
+        [&](int t, int stage) { first(true, t, stage); }, [](int) {});
+    __syncthreads();
+    start_pass<C>(visits, load);
     ones += __shfl_xor(ones, 32);
     left += __shfl_xor(left, 32);
     if (ones != 0.0f) {
@@ -850,8 +859,8 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             if (n_rows > 0 && t * kTile + 32 * kb < wave_end) block(kind, t * kTile + 32 * kb, kb, stage * 2 * C::TILE);
     };
     pass_over<C>(
-        whole, tiles(end) - whole, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
-        [&](int t, int stage) { second(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
+        1, whole, visits - whole, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
+        [&](int t, int stage) { second(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); }, [](int) {});
     if (n_rows > 0) {
         const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
         store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
@@ -894,18 +903,18 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
 }
 
 // Gradients of k and v, after dq_kernel: a wave owns 32 keys of a kv head and passes over the
-// queries of every head that shares it, in a fixed order; DK and DV: which of the two.  Two groups of four waves own the same keys and take
-// every other tile of queries each; their sums are joined at the end.  (A key of a causal
+// queries of every head that shares it, in a fixed order; DK and DV: which of the two.  G groups of four waves own the same keys and take
+// every G-th tile of queries each; their sums are joined at the end.  (A key of a causal
 // sequence is seen by all queries after it: with one group, 512 workgroups that all run at once took as
 // long as the longest of them, 817 us for dk of 2 x 8192 tokens.)
-template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN, bool DK, bool DV>
-__global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN, int G, bool DK, bool DV>
+__global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
-    __shared__ __attribute__((aligned(16))) char tiles_of[2][kStages<C>][2 * C::TILE];
-    __shared__ __attribute__((aligned(16))) int found[8][2 * C::D];  // (add_odd_numbers)
-    __shared__ __attribute__((aligned(16))) float stats_of[2][kStages<C>][2][kTile];  // lse, delta
+    __shared__ __attribute__((aligned(16))) char tiles_of[G][kStages<C>][2 * C::TILE];
+    __shared__ __attribute__((aligned(16))) int found[4 * G][2 * C::D];  // (add_odd_numbers)
+    __shared__ __attribute__((aligned(16))) float stats_of[G][kStages<C>][2][kTile];  // lse, delta
     extern __shared__ float tab[];
     const Place place = place_of(base, a.kv_deal, false);
     if (place.head < 0) return;
@@ -923,16 +932,10 @@ __global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     const int shift = s.n_k - s.n_q, w0 = (int)row0 + 32 * wave, n_rows = s.n_k - w0;
     const int my = w0 + (lane & 31);
 
-    F k[C::NS], v[C::NS];
-    load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
-    if constexpr (DK) load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
     f32x16 dk[DB], dv[DB];
     clear(dk), clear(dv);
     float held = kTopScale;
     const float scale = fabsf(a.scale) * kLog2e;  // the keys take its sign
-    if (a.scale < 0.0f) negate(k);
-    arrive(k);
-    if constexpr (DK) arrive(v);
     // Tiles of queries from the first that sees one of the workgroup's keys: t_edge .. t_whole - 1
     // see all of them and are visited first, then those before, then the last, if it is not whole.
     const int t_first = a.causal && (int)row0 - shift > 0 ? ((int)row0 - shift) / kTile : 0;
@@ -940,9 +943,9 @@ __global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     const int t_whole = s.n_q / kTile, tail = s.n_q % kTile && t_first <= t_whole ? 1 : 0;
     const int t_edge = t_all < t_whole ? (t_all > t_first ? t_all : t_first) : t_whole;  // edge tiles: t_first .. t_edge - 1
     const int n_whole = t_whole > t_edge ? t_whole - t_edge : 0, n_early = t_edge > t_first ? t_edge - t_first : 0;
-    const int n_all = n_whole + n_early + tail;
+    const int n_all = n_whole + n_early + tail, n_visits = (n_all + G - 1) / G;
     auto row_at = [&](int v) {  // of the group's visit v
-        int t = 2 * v + group;
+        int t = G * (v % n_visits) + group;
         t -= n_whole;
         return (t < 0 ? t + n_whole + t_edge : (t < n_early ? t_first + t : t_whole)) * kTile;
     };
@@ -951,6 +954,24 @@ __global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
     const Loader<IO, C::P, NP, true, VEC> lq(a.q, a.D_k, 0, wave, 4), lg(a.d_o, a.D_v, 0, wave, 4);
     const RowFrags<C> qrows(lds[0]);  // (d_o's tile lies C::TILE behind q's)
     const ColumnFrags<C, O> qcols(lds[0]);
+    auto load = [&](int t, int stage) {
+        if (G * (t % n_visits) + group >= n_all) return;
+        const int head = kv * r + t / n_visits, i0 = row_at(t), n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
+        lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
+        lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
+        if (wave < 2) {
+            const float* from = (wave ? a.row_delta : a.row_lse) + (int64_t)head * a.T + s.q0 + i0;
+            load_words_to_lds(resource(from, (uint32_t)n * 4), (uint32_t)lane * 4, stats[stage][wave]);
+        }
+    };
+    start_pass<C>(n_visits, load);
+    F k[C::NS], v[C::NS];
+    load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
+    if constexpr (DK) load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
+    if constexpr (BIAS) fill_biases<IO, 256 * G>(tab, reinterpret_cast<float*>(found), a, map, kv * r);
+    if (a.scale < 0.0f) negate(k);
+    arrive(k);
+    if constexpr (DK) arrive(v);
     // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  Their statistics are what the
     // accumulators start from: the products end in (score - lse) / scale and dP - delta.
     auto block = [&](auto kind, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
@@ -1024,42 +1045,31 @@ __global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
             if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave8]);
         }
     };
-    for (int hh = 0; hh < r; ++hh) {
-        const int head = kv * r + hh;
-        if constexpr (BIAS) {
-            __syncthreads();
-            fill_biases<IO, 512>(tab, reinterpret_cast<float*>(tiles_of), a, map, head);
+    auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int qb = 0; qb < 2; ++qb) {
+            const int q0 = row_at(t) + 32 * qb;
+            if (n_rows > 0 && G * (t % n_visits) + group < n_all && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
+                block(kind, q0, qb, stage * 2 * C::TILE, stats[stage]);
         }
-        auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
+    };
+    pass_over<C>(
+        r, n_whole / G, n_visits - n_whole / G, load,
+        [&](int t, int stage) {
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb) {
-                const int q0 = row_at(t) + 32 * qb;
-                if (n_rows > 0 && 2 * t + group < n_all && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
-                    block(kind, q0, qb, stage * 2 * C::TILE, stats[stage]);
+            for (int qb = 0; qb < 2; ++qb)
+                if (n_rows > 0) block(Kind<kWhole>{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
+        },
+        [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); },
+        [&](int hh) {
+            if (BIAS && hh + 1 < r) {  // the next head's biases, while its first tiles come
+                __syncthreads();
+                fill_biases<IO, 256 * G>(tab, reinterpret_cast<float*>(found), a, map, kv * r + hh + 1);
             }
-        };
-        pass_over<C>(
-            n_whole / 2, (n_all + 1) / 2 - n_whole / 2,
-            [&](int t, int stage) {
-                if (2 * t + group >= n_all) return;
-                const int i0 = row_at(t), n = s.n_q - i0 < kTile ? s.n_q - i0 : kTile;
-                lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
-                lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
-                if (wave < 2) {
-                    const float* from = (wave ? a.row_delta : a.row_lse) + (int64_t)head * a.T + s.q0 + i0;
-                    load_words_to_lds(resource(from, (uint32_t)n * 4), (uint32_t)lane * 4, stats[stage][wave]);
-                }
-            },
-            [&](int t, int stage) {
-#pragma unroll
-                for (int qb = 0; qb < 2; ++qb)
-                    if (n_rows > 0) block(Kind<kWhole>{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
-            },
-            [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); });
-    }
+        });
     // The other group's sums, in LDS in the accumulators' order, 4 KB for a wave and 32 columns
     // (as many tiles as they are wide hold them).
-    static_assert((DK && DV ? 2 : 1) * DB * 4 * 4096 <= (int)sizeof(tiles_of), "the sums fit the tiles");
+    static_assert(G == 1 || (DK && DV ? 2 : 1) * DB * 4 * 4096 <= (int)sizeof(tiles_of), "the sums fit the tiles");
     const bool half = std::is_same_v<IO, _Float16>;
     const float mk = half ? a.scale * inverse_of_power(held) : a.scale, mv = half ? 1.0f / 4096.0f : 1.0f;
     float* const other = reinterpret_cast<float*>(tiles_of) + wave * (DB * 1024) + lane;
@@ -1069,19 +1079,20 @@ __global__ __launch_bounds__(512, dkv_waves(sizeof(IO), DB)) void dkv_kernel(Att
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 acc[cb][i] *= m;
-                if (group) to[(16 * cb + i) * 64] = acc[cb][i];
+                if (G > 1 && group) to[(16 * cb + i) * 64] = acc[cb][i];
             }
     };
-    __syncthreads();
+    if constexpr (G > 1) __syncthreads();
     if constexpr (DK) pass(dk, mk, other);
     if constexpr (DV) pass(dv, mv, other + (DK ? 4 * DB * 1024 : 0));
-    __syncthreads();
+    if constexpr (G > 1) __syncthreads();
     if (group || n_rows <= 0) return;
     auto join = [&](f32x16 (&acc)[DB], const float* from) __attribute__((always_inline)) {
 #pragma unroll
         for (int cb = 0; cb < DB; ++cb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[cb][i] += from[(16 * cb + i) * 64];
+            for (int i = 0; i < 16; ++i)
+                if constexpr (G > 1) acc[cb][i] += from[(16 * cb + i) * 64];
     };
     if constexpr (DK) {
         join(dk, other);
@@ -1103,20 +1114,29 @@ hipError_t forward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t
     return hipGetLastError();
 }
 
+template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN, int G>
+void dkv_launch(const AttentionArgs& a, const BucketMap& map, size_t table, hipStream_t stream) {
+    in_pieces(a.kv_deal.workgroups(a.kv_heads), 256 * G, [&](uint32_t base, uint32_t wgs) {
+        const dim3 grid(wgs), threads(256 * G);
+        if constexpr (dkv_apart(sizeof(IO), DB)) {
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, G, true, false>), grid, threads, table, stream, a, map, base);
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, G, false, true>), grid, threads, table, stream, a, map, base);
+        } else {
+            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, G, true, true>), grid, threads, table, stream, a, map, base);
+        }
+    });
+}
+
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_t stream) {
     const size_t table = BIAS ? table_words(a.reach, a.buckets) * 4 : 0, sums = a.dbias ? 8 * tab_width(a.reach) * 4 : 0;
     in_pieces(a.deal.workgroups(a.heads), 256, [&](uint32_t base, uint32_t wgs) {
         hipLaunchKernelGGL((dq_kernel<IO, DB, VEC, BIAS, UNSEEN>), dim3(wgs), dim3(256), table + sums, stream, a, map, base);
     });
-    in_pieces(a.kv_deal.workgroups(a.kv_heads), 512, [&](uint32_t base, uint32_t wgs) {
-        if constexpr (dkv_apart(sizeof(IO), DB)) {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, false>), dim3(wgs), dim3(512), table, stream, a, map, base);
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, false, true>), dim3(wgs), dim3(512), table, stream, a, map, base);
-        } else {
-            hipLaunchKernelGGL((dkv_kernel<IO, DB, VEC, BIAS, UNSEEN, true, true>), dim3(wgs), dim3(512), table, stream, a, map, base);
-        }
-    });
+    // two groups where a causal key may have thousands of queries; short sequences (64 images of mean 197
+    // tokens: 82 us with two groups, 74 with one) have no use for them
+    if (a.kv_deal.units) dkv_launch<IO, DB, VEC, BIAS, UNSEEN, 2>(a, map, table, stream);
+    else dkv_launch<IO, DB, VEC, BIAS, UNSEEN, 1>(a, map, table, stream);
     return hipGetLastError();
 }
 
