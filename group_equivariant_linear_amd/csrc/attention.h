@@ -664,6 +664,40 @@ __device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, floa
     });
 }
 
+// acc += w's 32 rows (of block b) times the columns of the tile at `at`; FINITE: odd numbers as
+// 0, odd the largest that was met.  fp32 sums a block on its own first: one long chain of roundings
+// left dq of 5590 tokens off by a relative 1.5e-6, 0.7e-6 so (and costs 3 % of packed training in fp32).
+template <typename C, typename O, bool FINITE, typename Columns, int DB>
+__device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& columns, int at, int b, const f32x16& w, uint32_t& odd) {
+    using F = typename O::F;
+    auto one = [&](f32x16& to, int t, int cb) __attribute__((always_inline)) {
+        float u[C::E];
+#pragma unroll
+        for (int e = 0; e < C::E; ++e) u[e] = w[t * C::E + e];
+        F g[1] = {columns.get(at, b, t, cb)};
+        if constexpr (FINITE) {
+            const uint32_t o = O::top(g);
+            odd = o > odd ? o : odd;
+            g[0] = O::finite(g[0]);
+        }
+        O::mma(to, g[0], O::pack(u));
+    };
+    if constexpr (C::E == 8) {
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+            for (int cb = 0; cb < DB; ++cb) one(acc[cb], t, cb);
+    } else {
+#pragma unroll
+        for (int cb = 0; cb < DB; ++cb) {
+            f32x16 sum{};
+#pragma unroll
+            for (int t = 0; t < C::NT; ++t) one(sum, t, cb);
+            acc[cb] += sum;
+        }
+    }
+}
+
 // Gradients of q and, if wanted, of the biases: a wave owns 32 queries and passes over the
 // keys twice.  The first pass makes delta = sum P dP, as what d_o . o leaves of it: o is
 // rounded to the plan's type, and delta from it alone is off by that rounding, which dS (a
@@ -781,6 +815,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             scores(x, dp, j, kb, stage * 2 * C::TILE);
             if (edge) {
                 const int lim = last - j - 4 * h;
+                if (j == 0) {  // a row that sees one key: its dP to the bit, its dS is 0
+                    const float one = __shfl(dp[0], lane & 31);
+                    delta = last == 0 ? one : delta;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     ones += row_of(i) <= lim ? x[i] : 0.0f;
@@ -833,24 +871,8 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         const float f = hold<IO>(x, held, acc);
         if constexpr (std::is_same_v<IO, _Float16>) x[0] *= f;
         uint32_t odd = 0;
-#pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
-            float w[C::E];
-#pragma unroll
-            for (int e = 0; e < C::E; ++e) w[e] = x[0][t * C::E + e];
-            const F p = O::pack(w);
-#pragma unroll
-            for (int cb = 0; cb < DB; ++cb) {
-                F k[1] = {kcols.get(by, kb, t, cb)};
-                if constexpr (K == kUnseen) {
-                    const uint32_t o = O::top(k);
-                    odd = o > odd ? o : odd;
-                    k[0] = O::finite(k[0]);
-                }
-                O::mma(acc[cb], k[0], p);
-            }
-        }
-        if (K == kUnseen && __any(odd >= O::kInf)) 
+        add_columns<C, O, K == kUnseen>(acc, kcols, by, kb, x[0], odd);
+        if (K == kUnseen && __any(odd >= O::kInf))
             add_odd_numbers<C, IO, false>(acc, lds[0] + by + kb * (32 * C::P * 16), 32, last - j, true, found[wave]);
     };
     auto second = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
@@ -972,24 +994,34 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
     if (a.scale < 0.0f) negate(k);
     arrive(k);
     if constexpr (DK) arrive(v);
-    // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  Their statistics are what the
-    // accumulators start from: the products end in (score - lse) / scale and dP - delta.
+    // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  In 16 bits their statistics are what the
+    // accumulators start from: the products end in (score - lse) / scale and dP - delta.  fp32 adds them
+    // behind the products, which would round at lse's size 16 D times (relative 1.2e-6 in dk at D = 48, 4e-7 so),
+    // and so do blocks at an edge: dP is then dq_kernel's bit for bit, and a lone key's dS is 0.
     auto block = [&](auto kind, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
         constexpr int K = decltype(kind)::value;
         const int low = a.causal ? my - shift - q0 : 0, high = s.n_q - 1 - q0;  // rows of the block that see the lane's key
-        f32x16 x, dp, p[1], ds[1];
+        constexpr bool LATE = sizeof(IO) == 4 || K != kWhole;
+        f32x16 x{}, dp{}, p[1], ds[1];
+        auto add_stats = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[0][32 * qb + 8 * g + 4 * h]);
-            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[0][32 * qb + 8 * g + 4 * h]);
+                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * g + e] = lse[e], dp[4 * g + e] = DK ? delta[e] : 0.0f;
-        }
+                for (int e = 0; e < 4; ++e) {
+                    x[4 * g + e] += lse[e];
+                    if constexpr (DK) dp[4 * g + e] += delta[e];
+                }
+            }
+        };
+        if constexpr (!LATE) add_stats();
 #pragma unroll
         for (int st = 0; st < C::NS; ++st) O::mma(x, qrows.template get<F>(by, qb, st), k[st]);
 #pragma unroll
         for (int st = 0; st < C::NS; ++st)
             if constexpr (DK) O::mma(dp, qrows.template get<F>(by + C::TILE, qb, st), v[st]);
+        if constexpr (LATE) add_stats();
         if constexpr (BIAS) {
             const int from = q0 + shift - w0;  // distance of the block's first row and the wave's first key
             const float* t = tab + a.reach + kPad;
@@ -1017,28 +1049,8 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         if constexpr (DK && std::is_same_v<IO, _Float16>) ds[0] *= hold<IO>(ds, held, dk);
         if constexpr (DV && std::is_same_v<IO, _Float16>) p[0] *= 4096.0f;
         uint32_t odd = 0;
-        // column frags of the tile at `at` (finite, where it matters) times numbers w
-        auto product = [&](f32x16 (&acc)[DB], int at, const f32x16& w) __attribute__((always_inline)) {
-#pragma unroll
-            for (int st = 0; st < C::NT; ++st) {
-                float u[C::E];
-#pragma unroll
-                for (int e = 0; e < C::E; ++e) u[e] = w[st * C::E + e];
-                const F f = O::pack(u);
-#pragma unroll
-                for (int cb = 0; cb < DB; ++cb) {
-                    F g[1] = {qcols.get(at, qb, st, cb)};
-                    if constexpr (K == kUnseen) {
-                        const uint32_t o = O::top(g);
-                        odd = o > odd ? o : odd;
-                        g[0] = O::finite(g[0]);
-                    }
-                    O::mma(acc[cb], g[0], f);
-                }
-            }
-        };
-        if constexpr (DV) product(dv, by + C::TILE, p[0]);
-        if constexpr (DK) product(dk, by, ds[0]);
+        if constexpr (DV) add_columns<C, O, K == kUnseen>(dv, qcols, by + C::TILE, qb, p[0], odd);
+        if constexpr (DK) add_columns<C, O, K == kUnseen>(dk, qcols, by, qb, ds[0], odd);
         if (K == kUnseen && __any(odd >= O::kInf)) {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
             if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave8]);
