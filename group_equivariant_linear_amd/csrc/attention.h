@@ -29,6 +29,7 @@ constexpr int kRows = 128;  // rows that a workgroup's four waves own
 constexpr int kTile = 64;   // rows of the tiles that they pass over
 constexpr int kPad = 96;    // a wave's rows and a tile span fewer distances than this
 constexpr float kInf = __builtin_inff();
+constexpr float kLeastLse = -0x1p20f;
 
 template <typename IO>
 struct Op32 : Op<IO> {  // __bf16, _Float16
@@ -792,9 +793,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     load_rows<C, IO, F, VEC>(d_o, a.d_o, s.q0 + w0, head, n_rows, a.D_v);
     const bool real = (lane & 31) < n_rows;
     const int64_t row = (int64_t)head * a.T + s.q0 + my;
-    // in powers of two; a row that sees nothing has probabilities of 0
-    float lse = real ? a.lse[row] * kLog2e : kInf, delta = 0.0f, left = 0.0f, ones = 0.0f;
-    lse = lse == -kInf ? kInf : lse;
+    // In powers of two.  A row that sees nothing has probabilities of 0, and so has one whose every bias is a
+    // large negative number: fp32 holds that lse to no fraction, and exp(s - lse) may be anything.
+    float lse = real ? a.lse[row] : kInf, delta = 0.0f, left = 0.0f, ones = 0.0f;
+    lse = lse < kLeastLse ? kInf : lse * kLog2e;
     {
         F o[C::NS];
         load_rows<C, IO, F, VEC>(o, a.o, s.q0 + w0, head, n_rows, a.D_v);

@@ -33,8 +33,9 @@ __global__ __launch_bounds__(256) void reduce_kernel(const float* parts, float* 
     if (tid == 0) dbias[blockIdx.x] = sum[0];
 }
 
+// (no tokens: no slots, of packed sequences either; nothing launches, and no sums of slots exist)
 uint32_t slots_for(const int64_t* offsets, int64_t batch, int64_t T) {
-    if (batch <= 0) return 0;
+    if (batch <= 0 || T <= 0) return 0;
     return (uint32_t)(offsets ? T / kRows + batch : batch * ((T / batch + kRows - 1) / kRows));
 }
 

@@ -627,8 +627,9 @@ size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_k
  *   that query i sees of exp(s_ij),  o_i = sum P_ij v_j,  lse_i = log sum exp(s_ij)
  *   q [T][heads][d_k][N], k [T_kv][kv_heads][d_k][N], v [T_kv][kv_heads][d_v][N],
  *   o [T][heads][d_v][N]
- *   scale     finite, not 0
- *   bias      [heads][buckets], plan dtype, element-aligned, or NULL
+ *   scale     finite, of size 2^-100 at least
+ *   bias      [heads][buckets], plan dtype, element-aligned, or NULL; -infinity (and what
+ *             log2(e) times overflows to it, such as the lowest fp32) takes keys out
  *   offsets, kv_offsets  batch + 1 each, of the queries and of the keys (they may be the
  *             same array); NULL: equal lengths T / batch, T_kv / batch
  *   lse       fp32 [heads][T], for the backward or to join attention over several sets of
@@ -653,8 +654,10 @@ eqlinear_status eqlinear_attention(eqlinear_plan_t plan, const eqlinear_heads* q
  *   d_bias  fp32 [heads][buckets], or NULL; overwritten
  * 16-bit plans round P and dS to the plan dtype before their products (fp16: times powers of
  * two that keep them within its range, so that gradients may be smaller or larger than fp16's
- * numbers as long as dq, dk and dv are not); d_bias sums dS in fp32.  Rows of k and v that no
- * query sees get zeros.  Asynchronous on stream, no allocation; deterministic. */
+ * numbers as long as dq, dk and dv are not); d_bias sums dS in fp32, and o's rounding is taken
+ * out of delta.  Rows of k and v that no query sees get zeros.  lse is fp32, so P is off by a
+ * relative 2^-22 |lse|; rows whose lse is below -2^20 (every key under a large negative bias)
+ * count as rows that see no key: their gradients are 0.  Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_attention_backward(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
                                             const eqlinear_heads* v, const eqlinear_heads* o, const eqlinear_heads* d_o,
                                             const float* lse, float scale, const void* bias, const int64_t* offsets,

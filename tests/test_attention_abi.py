@@ -214,3 +214,9 @@ def test_calls_that_the_binding_refuses(eq, plan):
         eq.eqlinear_attention_step(plan, h, K, V, TB, LN, h, 0.1, batch=3)  # blocks of an address
     with pytest.raises(eq.EqlError):
         eq.eqlinear_attention(eq.eqlinear_mixer_plan(8, 4, 2, 8, 8, eq.EQL_BF16), h, h, h, h, 0.1, T=4, T_kv=4)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -101, -2.0 ** -101, 1e-45])
+def test_scales_that_lse_cannot_be_divided_by(eq, plan, scale):
+    for call in (call_forward, call_backward, call_step):
+        assert call(eq, plan, scale=scale) == eq.EQL_ERR_INVALID

@@ -84,3 +84,48 @@ def test_a_step_of_thousands(eq, dt, batch):  # noqa: F811
     s = Step(eq, dt, 4, 2, 1, 2, 2, [(7 * b) % 150 for b in range(batch)], 16, 8, 20, seed=batch)
     s.run()
     s.check(f"{dt} {batch}")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("low", [-1e8, -1e30])
+def test_rows_under_large_negative_biases(eq, dt, low):  # noqa: F811
+    """Every key of head 0 under one large number: o is a mean of v's rows, gradients are 0; head 1 is as ever."""
+    import torch
+    p, plain = (Problem(eq, dt, 8, 2, 2, 4, 4, [90, 200], causal=True, buckets=8, reach=40, seed=7) for _ in range(2))
+    p.bias[0] = low
+    for x in (p, plain):
+        x.forward()
+        x.backward()
+    o = p.o.float()
+    # a weighted mean, rounded: P and o by u each, and 16 e for the sums of up to 200 terms that are at most 1
+    top = p.v[:, 0].float().abs().max() * (1 + 2.0 ** -6)
+    assert torch.isfinite(o).all() and (o[:, 0].abs() <= top).all() and torch.isfinite(p.lse).all()
+    for t in (p.dq[:, 0], p.dk_[:, 0], p.dv_[:, 0], p.dbias[0]):
+        assert (t == 0).all()
+    for a, b in ((p.o, plain.o), (p.dq, plain.dq), (p.dk_, plain.dk_), (p.dv_, plain.dv_)):
+        assert torch.equal(a[:, 1], b[:, 1])
+    assert torch.equal(p.dbias[1], plain.dbias[1])
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("scale", [2.0 ** -100, -2.0 ** -40])
+def test_the_smallest_scales(eq, dt, scale):  # noqa: F811
+    """Scores of nothing: the biases alone decide."""
+    both(Problem(eq, dt, 8, 2, 1, 4, 4, [100], causal=True, buckets=8, reach=40, scale=scale, seed=8), f"{dt} {scale}")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("what", ["no sequences", "no queries", "no keys"])
+def test_nothing(eq, dt, what):  # noqa: F811
+    """Gradients are written all the same, as zeros (offsets belong to one sequence at least: without any, batch = 0)."""
+    lens, kv_lens = {"no sequences": ([], []), "no queries": ([0, 0], [70, 3]), "no keys": ([5, 40], [0, 0])}[what]
+    p = Problem(eq, dt, 8, 2, 1, 4, 4, lens, kv_lens, buckets=8, reach=40, packed=bool(lens), seed=9)
+    if not lens:
+        with pytest.raises(eq.EqlError):
+            Problem(eq, dt, 8, 2, 1, 4, 4, lens, kv_lens, buckets=8, reach=40, seed=9).forward()
+    p.forward()
+    p.backward()
+    for t in (p.o, p.dq, p.dk_, p.dv_, p.dbias):
+        assert (t == 0).all()
+    if p.T:
+        assert (p.lse == -float("inf")).all()
