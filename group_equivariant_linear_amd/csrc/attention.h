@@ -695,29 +695,34 @@ __device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, floa
 template <typename C, typename O, bool FINITE, typename Columns, int DB>
 __device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& columns, int at, int b, const f32x16& w, uint32_t& odd) {
     using F = typename O::F;
-    auto one = [&](f32x16& to, int t, int cb) __attribute__((always_inline)) {
+    auto packed = [&](int t) __attribute__((always_inline)) {
         float u[C::E];
 #pragma unroll
         for (int e = 0; e < C::E; ++e) u[e] = w[t * C::E + e];
+        return O::pack(u);
+    };
+    auto one = [&](f32x16& to, int t, int cb, const F& f) __attribute__((always_inline)) {
         F g[1] = {columns.get(at, b, t, cb)};
         if constexpr (FINITE) {
             const uint32_t o = O::top(g);
             odd = o > odd ? o : odd;
             g[0] = O::finite(g[0]);
         }
-        O::mma(to, g[0], O::pack(u));
+        O::mma(to, g[0], f);
     };
     if constexpr (C::E == 8) {
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t)
+        for (int t = 0; t < C::NT; ++t) {
+            const F f = packed(t);
 #pragma unroll
-            for (int cb = 0; cb < DB; ++cb) one(acc[cb], t, cb);
+            for (int cb = 0; cb < DB; ++cb) one(acc[cb], t, cb, f);
+        }
     } else {
 #pragma unroll
         for (int cb = 0; cb < DB; ++cb) {
             f32x16 sum{};
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t) one(sum, t, cb);
+            for (int t = 0; t < C::NT; ++t) one(sum, t, cb, packed(t));
             acc[cb] += sum;
         }
     }

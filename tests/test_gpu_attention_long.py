@@ -129,3 +129,18 @@ def test_nothing(eq, dt, what):  # noqa: F811
         assert (t == 0).all()
     if p.T:
         assert (p.lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("d", [7, 12, 16])
+@pytest.mark.parametrize("lens", [[300], [2050]])
+def test_the_longest_reach_of_wide_heads(eq, dt, d, lens):  # noqa: F811
+    """The most LDS that tiles and biases take together."""
+    both(Problem(eq, dt, 8, 1, 1, d, d, lens, causal=True, buckets=256, reach=1024, packed=False, seed=d), f"{dt} {d}")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_a_step_of_thousands_with_wide_heads(eq, dt):  # noqa: F811
+    s = Step(eq, dt, 8, 1, 1, 16, 16, [(11 * b) % 40 for b in range(2048)], 16, 256, 1024, seed=1)
+    s.run()
+    s.check(f"{dt}")
