@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void tokens_kernel(TablesArgs a, const Request
     if (t < a.T) place_token(a, requests, a.offsets, t);
 }
 
-// W numbers a thread: 16 bytes, or one.
+// W numbers a thread: 16 bytes, or one.  A copy: 104 MB in 24.4 us, 4.3 TB/s.
 template <typename R>
 __global__ __launch_bounds__(256) void store_kernel(StoreArgs a, int W, int pk, int pv, uint32_t base) {
     const int per = a.kv_heads * (pk + pv);  // pieces of a token
