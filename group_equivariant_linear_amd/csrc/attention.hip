@@ -19,10 +19,11 @@ namespace {
 using namespace att;
 
 // Gradient of one bias: the sums of every slot of its head, in a fixed order.
-__global__ __launch_bounds__(256) void reduce_kernel(const float* parts, float* dbias, int64_t n) {
+__global__ __launch_bounds__(256) void reduce_kernel(const float* parts, float* dbias, int64_t n, uint32_t base) {
     __shared__ float sum[256];
     const int tid = (int)threadIdx.x;
-    const float* p = parts + (int64_t)blockIdx.x * n;
+    const uint32_t cell = blockIdx.x + base;
+    const float* p = parts + (int64_t)cell * n;
     float t = 0.0f;
     for (int64_t i = tid; i < n; i += 256) t += p[i];
     sum[tid] = t;
@@ -30,7 +31,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(const float* parts, float* 
         __syncthreads();
         if (tid < w) sum[tid] += sum[tid + w];
     }
-    if (tid == 0) dbias[blockIdx.x] = sum[0];
+    if (tid == 0) dbias[cell] = sum[0];
 }
 
 // (no tokens: no slots, of packed sequences either; nothing launches, and no sums of slots exist)
@@ -80,8 +81,9 @@ hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& m
                                          : att::backward<_Float16>(a, map, stream);
     if (e != hipSuccess) return e;
     if (a.dbias)
-        hipLaunchKernelGGL(reduce_kernel, dim3((uint32_t)(a.heads * a.buckets)), dim3(256), 0, stream, a.parts, a.dbias,
-                           (int64_t)a.slots);
+        in_pieces((int64_t)a.heads * a.buckets, 256, [&](uint32_t base, uint32_t wgs) {
+            hipLaunchKernelGGL(reduce_kernel, dim3(wgs), dim3(256), 0, stream, a.parts, a.dbias, (int64_t)a.slots, base);
+        });
     return hipGetLastError();
 }
 

@@ -385,11 +385,12 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
 // threads, 71 with a wave that takes one part after the other; 3072 rows of two parts or so
 // took 13.7 us on 512 threads, whose waves come in three rounds.
 template <typename IO, int kJoin>
-__global__ __launch_bounds__(kJoin) void join_kernel(StepArgs a, Grid g, const float* ws) {
+__global__ __launch_bounds__(kJoin) void join_kernel(StepArgs a, Grid g, const float* ws, uint32_t base) {
     constexpr int G = kJoin / 32;
     __shared__ float tops[kWorkgroups + 1], sums[G][att::Shape<float, 4>::D], red[kJoin / 64];
-    const int tid = (int)threadIdx.x, id = (int)blockIdx.x;
-    const int b = id / a.heads, head = id - b * a.heads, r = a.heads / a.kv_heads, kv = head / r;
+    const int tid = (int)threadIdx.x;
+    const uint32_t id = blockIdx.x + base;
+    const int b = (int)(id / (uint32_t)a.heads), head = (int)(id - (uint32_t)b * (uint32_t)a.heads), r = a.heads / a.kv_heads, kv = head / r;
     const int group = (head - kv * r) / kQueries, h = head - kv * r - group * kQueries, nr = r < kQueries ? r : kQueries;
     const int* const before = reinterpret_cast<const int*>(ws);
     const Cut cut((int64_t)before[a.batch] * g.items, g.wgs);
@@ -457,9 +458,11 @@ hipError_t run_cfg(const StepArgs& a, const BucketMap& map, float* ws, hipStream
     });
     if (g.shared) {
         // many rows: few parts each (on average); few: many
-        const dim3 rows((uint32_t)(a.batch * a.heads));
-        if (a.batch * g.items >= g.wgs / 8) hipLaunchKernelGGL((join_kernel<IO, 128>), rows, dim3(128), 0, stream, a, g, ws);
-        else hipLaunchKernelGGL((join_kernel<IO, 512>), rows, dim3(512), 0, stream, a, g, ws);
+        const bool many = a.batch * g.items >= g.wgs / 8;
+        in_pieces(a.batch * a.heads, many ? 128 : 512, [&](uint32_t base, uint32_t rows) {
+            if (many) hipLaunchKernelGGL((join_kernel<IO, 128>), dim3(rows), dim3(128), 0, stream, a, g, ws, base);
+            else hipLaunchKernelGGL((join_kernel<IO, 512>), dim3(rows), dim3(512), 0, stream, a, g, ws, base);
+        });
     }
     return hipGetLastError();
 }
