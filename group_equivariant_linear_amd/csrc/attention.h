@@ -894,6 +894,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             if constexpr (K != kWhole) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
         }
         if constexpr (BIAS) {
+            // (rows past the last query have probabilities of 0 and distances of their own: 0 times a NaN is no term)
+            if (a.dbias && n_rows < 32)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[0][i] = real ? x[0][i] : 0.0f;
             const int from = w0 + shift - j;
             if (a.dbias && (from - 31 >= a.reach || from + 31 <= -a.reach)) {
                 float t = 0.0f;
