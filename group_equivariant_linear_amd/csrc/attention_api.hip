@@ -84,8 +84,8 @@ bool caches_apart(const eqlinear_pages& a, const eqlinear_pages& b, int64_t bloc
 
 Pages pages_of(const eqlinear_pages& c) { return Pages{c.ptr, c.block_stride, c.token_stride, c.head_stride}; }
 
-// (the backward divides lse by it)
-bool scale_ok(float scale) { return std::isfinite(scale) && std::fabs(scale) >= 0x1p-100f; }
+// (the backward divides lse by it, and all kernels multiply it by log2 e: NaN is refused too)
+bool scale_ok(float scale) { return std::fabs(scale) >= 0x1p-100f && std::fabs(scale) <= 0x1p100f; }
 
 bool bias_ok(const eqlinear_plan_s* p, const void* bias) { return !bias || (p->buckets > 0 && aligned(bias, elem_size(p))); }
 

@@ -627,7 +627,7 @@ size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_k
  *   that query i sees of exp(s_ij),  o_i = sum P_ij v_j,  lse_i = log sum exp(s_ij)
  *   q [T][heads][d_k][N], k [T_kv][kv_heads][d_k][N], v [T_kv][kv_heads][d_v][N],
  *   o [T][heads][d_v][N]
- *   scale     finite, of size 2^-100 at least
+ *   scale     of size 2^-100 to 2^100
  *   bias      [heads][buckets], plan dtype, element-aligned, or NULL; -infinity (and what
  *             log2(e) times overflows to it, such as the lowest fp32) takes keys out
  *   offsets, kv_offsets  batch + 1 each, of the queries and of the keys (they may be the
