@@ -496,6 +496,9 @@ size_t attention_step_workspace(int io, int heads, int kv_heads, int D_k, int D_
 
 hipError_t launch_attention_step(int io, const StepArgs& a, const BucketMap& map, void* ws, hipStream_t stream) {
     if (a.batch * a.kv_heads * ((a.heads / a.kv_heads + kQueries - 1) / kQueries) > 0x7fffffff) return hipErrorNotSupported;
+    // (units before each sequence are counted in 32 bits)
+    const int64_t most = ((int64_t)a.max_blocks * a.block_size + kUnit - 1) / kUnit;
+    if (a.batch <= kMaxShared && a.batch * (most > 0 ? most : 1) > 0x7fffffff) return hipErrorNotSupported;
     float* w = static_cast<float*>(ws);
     return io == kIoF32 ? run<float>(a, map, w, stream)
                         : (io == kIoBF16 ? run<__bf16>(a, map, w, stream) : run<_Float16>(a, map, w, stream));

@@ -687,7 +687,8 @@ size_t eqlinear_attention_step_workspace(eqlinear_plan_t plan, int64_t batch);
  * there; a sequence without keys has o = 0, lse = -infinity.  Entries past a sequence's
  * last block are not read.  Roundings as in eqlinear_attention.  A long sequence is split
  * over workgroups whose parts are joined in a fixed order.  max_blocks block_size at most
- * 2^30 (EQL_ERR_UNSUPPORTED).  Asynchronous on stream, no allocation; deterministic. */
+ * 2^30, and with up to 2048 sequences batch times it below 2^38 (EQL_ERR_UNSUPPORTED).
+ * Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_attention_step(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_pages* k_cache,
                                         const eqlinear_pages* v_cache, int64_t blocks, int block_size, const int32_t* table,
                                         int64_t max_blocks, const int32_t* lengths, float scale, const void* bias,
