@@ -116,28 +116,26 @@ struct ColumnFrags {
     }
 };
 
-// What the products with finite operands left out of acc: the infinities and NaN of a tile's
-// `rows` rows.  (A product would spread those in unseen rows as well: 0 times infinity.)  A
-// lane's row sees rows 0 .. lim, or (SUFFIX) lim and later, so a column's first (last) such
-// number decides: +infinity or NaN in `found`, -infinity or NaN behind it.  nan: any is a NaN at
-// once (it multiplies factors that may be 0).  Rare, and held to few registers.
-template <class C, typename IO, bool SUFFIX>
-__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, int rows, int lim, bool nan, int* found) {
+// What the products with finite operands left out of acc: the infinities and NaN of a block of 32 rows
+// of a tile.  (A product would spread those in unseen rows as well: 0 times infinity.)  `sees`: the rows
+// that the lane's row sees, a bit each; `found` takes for each column the rows of +infinity or NaN, and
+// behind them those of -infinity or NaN.  nan: any is a NaN at once (it multiplies factors that may be 0).
+// Rare, and held to few registers.
+template <class C, typename IO>
+__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, uint32_t sees, bool nan, int* found) {
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
-    constexpr int none = SUFFIX ? -0x7fffffff : 0x7fffffff;
     typedef int i32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll 1
     for (int d = lane; d < C::D; d += 64) {
-        int pos = none, neg = none;
+        uint32_t pos = 0, neg = 0;
 #pragma unroll 1
-        for (int k = 0; k < rows; ++k) {
-            const int row = SUFFIX ? k : rows - 1 - k;
+        for (int row = 0; row < 32; ++row) {
             const float x = (float)*reinterpret_cast<const IO*>(tile + place<C::ES, C::P>(row, d / C::E) + d % C::E * C::ES);
             if (fabsf(x) < kInf) continue;
-            if (nan || !(x < 0.0f)) pos = row;
-            if (nan || !(x > 0.0f)) neg = row;
+            if (nan || !(x < 0.0f)) pos |= 1u << row;
+            if (nan || !(x > 0.0f)) neg |= 1u << row;
         }
-        found[d] = pos, found[C::D + d] = neg;
+        found[d] = (int)pos, found[C::D + d] = (int)neg;
     }
     // (the wave's own numbers: its LDS instructions come in order)
 #pragma unroll
@@ -149,11 +147,23 @@ __device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char
             const i32x4 n = *reinterpret_cast<const i32x4*>(found + C::D + 32 * cb + 8 * g + 4 * h);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                acc[cb][4 * g + e] += (SUFFIX ? p[e] >= lim : p[e] <= lim) ? kInf : 0.0f;
-                acc[cb][4 * g + e] += (SUFFIX ? n[e] >= lim : n[e] <= lim) ? -kInf : 0.0f;
+                acc[cb][4 * g + e] += p[e] & (int)sees ? kInf : 0.0f;
+                acc[cb][4 * g + e] += n[e] & (int)sees ? -kInf : 0.0f;
             }
         }
     asm volatile("" ::: "memory");
+}
+// Bits 0 .. last (none below 0, all from 31 on).
+__device__ __forceinline__ uint32_t bits_to(int last) { return last >= 31 ? ~0u : (last < 0 ? 0u : (2u << last) - 1u); }
+// Bits of the 32 distances from d on, step apart, whose biases in tab are -infinity.
+__device__ __forceinline__ uint32_t taken_out_of(const float* tab, int reach, int d, int step) {
+    uint32_t out = 0;
+#pragma unroll 1
+    for (int r = 0; r < 32; ++r, d += step) {
+        const int at = d > reach ? reach : (d < -reach ? -reach : d);
+        out |= tab[reach + kPad + at] == -kInf ? 1u << r : 0u;
+    }
+    return out;
 }
 
 template <int N>
@@ -245,6 +255,7 @@ __device__ __forceinline__ Place place_of(uint32_t base, const Deal& d, bool fal
 // reach.  A wave's lanes hold 64 buckets' starts and biases, loaded before all else, and the wave
 // writes every 4th (of all: 256 / 64) bucket's distances: no wait between load and store.  (A
 // search of each distance's bucket in LDS took 29.2 us for 64 images, this 27.7.)  Ends with its writes not waited for.
+// Returns whether one of them is -infinity, alike in all waves: a key at such a distance is not seen, whatever stands there.
 __host__ __device__ constexpr int tab_width(int reach) { return 2 * (reach + kPad) + 1; }
 __host__ __device__ constexpr int table_words(int reach, int buckets) { return tab_width(reach) + buckets + 1; }
 struct BiasLanes {  // of buckets b0 + lane
@@ -263,13 +274,15 @@ __device__ __forceinline__ BiasLanes load_biases(const AttentionArgs& a, const B
     return x;
 }
 template <typename IO, int THREADS = 256>
-__device__ __forceinline__ void fill_biases(float* tab, BiasLanes x, const AttentionArgs& a, const BucketMap& map, int head) {
+__device__ __forceinline__ bool fill_biases(float* tab, BiasLanes x, const AttentionArgs& a, const BucketMap& map, int head) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int off = a.reach + kPad, side = a.causal ? a.buckets : a.buckets / 2;
     int* const starts = reinterpret_cast<int*>(tab + tab_width(a.reach));
+    bool out = false;
     for (int b0 = 0; b0 < side; b0 += 64) {
         if (b0) x = load_biases<IO>(a, map, head, b0);
         if (wave == 0 && b0 + lane < side) starts[b0 + lane] = x.start, starts[b0 + lane + 1] = x.next;
+        out |= __any(x.before == -kInf || x.after == -kInf);
         const int n = side - b0 < 64 ? side - b0 : 64;
         for (int b = wave; b < n; b += THREADS / 64) {
             const int from = __builtin_amdgcn_readlane(x.start, b), next = __builtin_amdgcn_readlane(x.next, b);
@@ -284,6 +297,23 @@ __device__ __forceinline__ void fill_biases(float* tab, BiasLanes x, const Atten
     }
     if (side == 0)
         for (int m = tid; m <= 2 * off; m += THREADS) tab[m] = 0.0f;
+    return out;
+}
+
+// Scores x of a block in powers of two, with the biases at t[STEP row_of(i)]; a key whose bias takes
+// it out has -infinity, whatever its number (and 0 in y).  Returns these, bit i of accumulator i.
+template <int STEP>
+__device__ __forceinline__ uint32_t biased_or_out(f32x16& x, f32x16& y, float scale, const float* t) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float bias = t[STEP * row_of(i)];
+        const bool gone = bias == -kInf;
+        x[i] = gone ? -kInf : __builtin_fmaf(x[i], scale, bias);
+        y[i] = gone ? 0.0f : y[i];
+        out |= gone ? 1u << i : 0u;
+    }
+    return out;
 }
 
 // Fragments of 32 rows from memory, the operand of the products over the head's numbers.
@@ -391,14 +421,14 @@ constexpr int kStages = 4 * C::TILE <= 80 * 1024 ? 2 : 1;
 
 // What work on a tile has to look at: every row sees all of it; some of its rows are not
 // there (zeros); some are there and not seen, so that no infinity of theirs may be multiplied.
-// (UNSEEN kernels look for those: causal ones, and those for rows off 16 bytes, which are one
-// for all calls.)
+// (UNSEEN kernels look for those: causal ones, those with biases, which may take keys out, and
+// those for rows off 16 bytes, which are one for all calls.)
 constexpr int kWhole = 0, kPartial = 1, kUnseen = 2;
 template <int K>
 using Kind = std::integral_constant<int, K>;
 
-// `rounds` rounds of visits to n_a + n_b pairs of tiles: load(v, stage) of visit v (counted through
-// all rounds), then, when its tiles are there, a(v, stage) for a round's first n_a visits and
+// `rounds` rounds of n visits to pairs of tiles: load(v, stage) of visit v (counted through
+// all rounds), then, when its tiles are there, a(v, stage) for a round's first n_a() visits and
 // b(v, stage) for the others; between(r) after round r.  Every wave calls it, and a() and b() have no
 // barrier.  start_pass() before it loads the first tiles: early, as the rest of what a
 // kernel starts with can be on its way at the same time.  (Loops of their own for a and b: work with
@@ -408,9 +438,9 @@ __device__ __forceinline__ void start_pass(int visits, L&& load) {
     if constexpr (kStages<C> == 2)
         if (visits > 0) load(0, 0);
 }
-template <class C, typename L, typename A, typename B, typename R>
-__device__ __forceinline__ void pass_over(int rounds, int n_a, int n_b, L&& load, A&& a, B&& b, R&& between) {
-    const int n = rounds * (n_a + n_b);
+template <class C, typename N, typename L, typename A, typename B, typename R>
+__device__ __forceinline__ void pass_over(int rounds, N&& n_a, int visits, L&& load, A&& a, B&& b, R&& between) {
+    const int n = rounds * visits;
     int stage = 0, v = 0;
     auto next = [&]() __attribute__((always_inline)) {
         if constexpr (kStages<C> == 2) {
@@ -425,11 +455,12 @@ __device__ __forceinline__ void pass_over(int rounds, int n_a, int n_b, L&& load
         }
     };
     for (int r = 0; r < rounds; ++r) {
-        for (int i = 0; i < n_a; ++i, ++v, stage ^= kStages<C> - 1) {
+        const int whole = n_a();
+        for (int i = 0; i < whole; ++i, ++v, stage ^= kStages<C> - 1) {
             next();
             a(v, stage);
         }
-        for (int i = 0; i < n_b; ++i, ++v, stage ^= kStages<C> - 1) {
+        for (int i = whole; i < visits; ++i, ++v, stage ^= kStages<C> - 1) {
             next();
             b(v, stage);
         }
@@ -485,7 +516,8 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;    // keys that the wave sees
     // keys that some of the workgroup's rows see; tiles that all of them do
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
-    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
+    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k;
+    int whole = all > 0 ? all / kTile : 0;
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
@@ -504,7 +536,9 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     if constexpr (kStages<C> == 2) load_k(0), load_v(0);
     F q[C::NS];
     load_rows<C, IO, F, VEC>(q, a.q, s.q0 + w0, head, n_rows, a.D_k);
-    if constexpr (BIAS) fill_biases<IO>(tab, biases, a, map, head);
+    bool taken_out = false;  // keys by their biases: then no tile is whole
+    if constexpr (BIAS) taken_out = fill_biases<IO>(tab, biases, a, map, head);
+    if (taken_out) whole = 0;
     if (a.scale < 0.0f) negate(q);
     arrive(q);
 
@@ -526,8 +560,13 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
             // (the far ones share a value: no other way, which would part the products from it)
             const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
             t += far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h;
+            if (K != kWhole && taken_out) {
+                f32x16 none{};
+                biased_or_out<-1>(x, none, scale, t);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[-row_of(i)]);
+                for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[-row_of(i)]);
+            }
         }
         if constexpr (K != kWhole) {
             const int lim = last - j - 4 * h;
@@ -581,8 +620,11 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
                 }
                 O::mma(acc[cb], v[0], p[t]);
             }
-        if (K == kUnseen && __any(odd >= O::kInf))
-            add_odd_numbers<C, IO, false>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), 32, last - 32 * n, false, found[wave]);
+        if (K == kUnseen && __any(odd >= O::kInf)) {
+            uint32_t sees = bits_to(last - 32 * n);
+            if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - 32 * n, -1);
+            add_odd_numbers<C, IO>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), sees, false, found[wave]);
+        }
     };
     using Edge = Kind<UNSEEN ? kUnseen : kPartial>;
     if constexpr (kStages<C> == 2) {
@@ -781,7 +823,8 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     const int last = a.causal ? (my + shift < s.n_k - 1 ? my + shift : s.n_k - 1) : s.n_k - 1;
     const int wave_end = a.causal && w0 + 31 + shift < s.n_k - 1 ? w0 + 32 + shift : s.n_k;
     const int end = a.causal && (int)row0 + kRows - 1 + shift < s.n_k - 1 ? (int)row0 + kRows + shift : s.n_k;
-    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k, whole = all > 0 ? all / kTile : 0;
+    const int all = a.causal && (int)row0 + shift < s.n_k - 1 ? (int)row0 + shift + 1 : s.n_k;
+    int whole = all > 0 ? all / kTile : 0;
 
     constexpr int NP = (C::P + 3) / 4;
     const Loader<IO, C::P, NP, true, VEC> lk(a.k, a.D_k, 0, wave, 4), lv(a.v, a.D_v, 0, wave, 4);
@@ -794,8 +837,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     };
     const int visits = tiles(end);
     start_pass<C>(visits, load);
+    bool taken_out = false;  // keys by their biases: then no tile is whole
     if constexpr (BIAS) {
-        fill_biases<IO>(tab, biases, a, map, head);
+        taken_out = fill_biases<IO>(tab, biases, a, map, head);
+        if (taken_out) whole = 0;
         if (a.dbias)
             for (int x = tid; x < 8 * width; x += 256) sums[x] = 0.0f;
     }
@@ -820,8 +865,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     }
     if (a.scale < 0.0f) negate(q);
     arrive(q), arrive(d_o);
-    // Probabilities and dP of 32 keys from j on, at block kb of the tiles at `by`.
-    auto scores = [&](f32x16& x, f32x16& dp, int j, int kb, int by) __attribute__((always_inline)) {
+    // Probabilities and dP of 32 keys from j on, at block kb of the tiles at `by`; returns the keys taken
+    // out (of a block at an edge), bit i of accumulator i.
+    auto scores = [&](bool edge, f32x16& x, f32x16& dp, int j, int kb, int by) __attribute__((always_inline)) {
+        uint32_t out = 0;
         x = f32x16{}, dp = f32x16{};
 #pragma unroll
         for (int st = 0; st < C::NS; ++st) O::mma(x, krows.template get<F>(by, kb, st), q[st]);
@@ -830,7 +877,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         if constexpr (BIAS) {
             const int from = w0 + shift - j;  // distance of the wave's first row and the block's first key
             const float* t = tab + a.reach + kPad;
-            if (from - 31 >= a.reach || from + 31 <= -a.reach) {
+            const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
+            if (edge && taken_out) {
+                out = biased_or_out<-1>(x, dp, scale, t + (far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h));
+            } else if (far) {
                 const float f = t[from > 0 ? a.reach : -a.reach];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, f);
@@ -845,6 +895,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -lse));
         }
+        return out;
     };
     auto first = [&](bool edge, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
@@ -852,7 +903,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             const int j = t * kTile + 32 * kb;
             if (n_rows <= 0 || j >= wave_end) return;
             f32x16 x, dp;
-            scores(x, dp, j, kb, stage * 2 * C::TILE);
+            scores(edge, x, dp, j, kb, stage * 2 * C::TILE);
             if (edge) {
                 const int lim = last - j - 4 * h;
                 if (j == 0) {  // a row that sees one key: its dP to the bit, its dS is 0
@@ -871,7 +922,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         }
     };
     pass_over<C>(
-        1, whole, visits - whole, load, [&](int t, int stage) { first(false, t, stage); },
+        1, [&]() { return whole; }, visits, load, [&](int t, int stage) { first(false, t, stage); },
         [&](int t, int stage) { first(true, t, stage); }, [](int) {});
     __syncthreads();
     start_pass<C>(visits, load);
@@ -886,13 +937,16 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     auto block = [&](auto kind, int j, int kb, int by) __attribute__((always_inline)) {
         constexpr int K = decltype(kind)::value;
         f32x16 x[1], dp;
-        scores(x[0], dp, j, kb, by);
+        const uint32_t out = scores(K != kWhole, x[0], dp, j, kb, by);
         const int lim = last - j - 4 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             x[0][i] *= dp[i] - delta;
             if constexpr (K != kWhole) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
         }
+        if (BIAS && K != kWhole && taken_out)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[0][i] = out >> i & 1 ? 0.0f : x[0][i];
         if constexpr (BIAS) {
             // (rows past the last query have probabilities of 0 and distances of their own: 0 times a NaN is no term)
             if (a.dbias && n_rows < 32)
@@ -916,8 +970,11 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         if constexpr (std::is_same_v<IO, _Float16>) x[0] *= f;
         uint32_t odd = 0;
         add_columns<C, O, K == kUnseen>(acc, kcols, by, kb, x[0], odd);
-        if (K == kUnseen && __any(odd >= O::kInf))
-            add_odd_numbers<C, IO, false>(acc, lds[0] + by + kb * (32 * C::P * 16), 32, last - j, true, found[wave]);
+        if (K == kUnseen && __any(odd >= O::kInf)) {
+            uint32_t sees = bits_to(last - j);
+            if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - j, -1);
+            add_odd_numbers<C, IO>(acc, lds[0] + by + kb * (32 * C::P * 16), sees, true, found[wave]);
+        }
     };
     auto second = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
@@ -925,7 +982,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             if (n_rows > 0 && t * kTile + 32 * kb < wave_end) block(kind, t * kTile + 32 * kb, kb, stage * 2 * C::TILE);
     };
     pass_over<C>(
-        1, whole, visits - whole, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
+        1, [&]() { return whole; }, visits, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
         [&](int t, int stage) { second(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); }, [](int) {});
     if (n_rows > 0) {
         const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
@@ -1036,7 +1093,8 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
     F k[C::NS], v[C::NS];
     load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
     if constexpr (DK) load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
-    if constexpr (BIAS) fill_biases<IO, 256 * G>(tab, biases, a, map, kv * r);
+    bool taken_out = false;  // keys by this head's biases: then no tile is whole
+    if constexpr (BIAS) taken_out = fill_biases<IO, 256 * G>(tab, biases, a, map, kv * r);
     if (a.scale < 0.0f) negate(k);
     arrive(k);
     if constexpr (DK) arrive(v);
@@ -1049,6 +1107,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         const int low = a.causal ? my - shift - q0 : 0, high = s.n_q - 1 - q0;  // rows of the block that see the lane's key
         constexpr bool LATE = sizeof(IO) == 4 || K != kWhole;
         f32x16 x{}, dp{}, p[1], ds[1];
+        uint32_t out = 0;
         auto add_stats = [&]() __attribute__((always_inline)) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -1071,7 +1130,10 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         if constexpr (BIAS) {
             const int from = q0 + shift - w0;  // distance of the block's first row and the wave's first key
             const float* t = tab + a.reach + kPad;
-            if (from - 31 >= a.reach || from + 31 <= -a.reach) {
+            const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
+            if (K != kWhole && taken_out) {
+                out = biased_or_out<1>(x, dp, scale, t + (far ? (from > 0 ? a.reach : -a.reach - 31) : from - (lane & 31) + 4 * h));
+            } else if (far) {
                 const float f = t[from > 0 ? a.reach : -a.reach];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, f);
@@ -1087,7 +1149,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
             if constexpr (DK) ds[0][i] = p[0][i] * dp[i];
             if constexpr (K != kWhole) {
                 const int at = row_of(i) + 4 * h;
-                const bool seen = at >= low && at <= high;
+                const bool seen = at >= low && at <= high && !(BIAS && (out >> i & 1));
                 p[0][i] = seen ? p[0][i] : 0.0f;
                 if constexpr (DK) ds[0][i] = seen ? ds[0][i] : 0.0f;
             }
@@ -1099,8 +1161,10 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         if constexpr (DK) add_columns<C, O, K == kUnseen>(dk, qcols, by, qb, ds[0], odd);
         if (K == kUnseen && __any(odd >= O::kInf)) {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
-            if constexpr (DV) add_odd_numbers<C, IO, true>(dv, t + C::TILE, 32, low, false, found[wave8]);
-            if constexpr (DK) add_odd_numbers<C, IO, true>(dk, t, 32, low, true, found[wave8]);
+            uint32_t sees = bits_to(high) & ~bits_to(low - 1);
+            if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, q0 + shift - my, 1);
+            if constexpr (DV) add_odd_numbers<C, IO>(dv, t + C::TILE, sees, false, found[wave8]);
+            if constexpr (DK) add_odd_numbers<C, IO>(dk, t, sees, true, found[wave8]);
         }
     };
     auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
@@ -1112,7 +1176,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         }
     };
     pass_over<C>(
-        r, n_whole / G, n_visits - n_whole / G, load,
+        r, [&]() { return taken_out ? 0 : n_whole / G; }, n_visits, load,
         [&](int t, int stage) {
 #pragma unroll
             for (int qb = 0; qb < 2; ++qb)
@@ -1123,7 +1187,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
             if (BIAS && hh + 1 < r) {  // the next head's biases, while its first tiles come
                 const BiasLanes next = load_biases<IO>(a, map, kv * r + hh + 1);
                 __syncthreads();
-                fill_biases<IO, 256 * G>(tab, next, a, map, kv * r + hh + 1);
+                taken_out = fill_biases<IO, 256 * G>(tab, next, a, map, kv * r + hh + 1);
             }
         });
     // The other group's sums, in LDS in the accumulators' order, 4 KB for a wave and 32 columns
@@ -1209,8 +1273,9 @@ hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_
     return EQL_ATTENTION_DB(WHAT, 4);
 #define EQL_ATTENTION_DB(WHAT, DB)                                                                                            \
     !vec       ? WHAT<IO, DB, false, true, true>(a, map, stream)                                                              \
-    : a.causal ? (bias ? WHAT<IO, DB, true, true, true>(a, map, stream) : WHAT<IO, DB, true, false, true>(a, map, stream))    \
-               : (bias ? WHAT<IO, DB, true, true, false>(a, map, stream) : WHAT<IO, DB, true, false, false>(a, map, stream))
+    : bias     ? WHAT<IO, DB, true, true, true>(a, map, stream)                                                               \
+    : a.causal ? WHAT<IO, DB, true, false, true>(a, map, stream)                                                              \
+               : WHAT<IO, DB, true, false, false>(a, map, stream)
 
 template <typename IO>
 hipError_t forward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {
