@@ -81,7 +81,8 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
     constexpr int NL = kKeys * P / 64;  // loads of a tile of v
     __shared__ __attribute__((aligned(16))) char lds[4][kKeys * P * 16];
     __shared__ float ms[4][kQueries], ls[4][kQueries], all_top[kQueries], all_sum[kQueries];
-    __shared__ int wave_units[4];
+    __shared__ int wave_units[4], wave_out[4];
+    __shared__ __attribute__((aligned(16))) int found[4][2][D];  // columns' keys of +infinity or NaN, of -infinity or NaN
     extern __shared__ int shared[];  // units before each sequence, lengths; an item's biases; the buckets of distances
     const uint32_t wg = blockIdx.x + base;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4, ln = lane & 15;
@@ -226,10 +227,17 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
         there = (uint32_t)__ballot(id >= 0 && id < a.blocks);
         id = block_of(j_first + kUnit);
 
+        bool out = false;
         if (a.bias)
-            for (int i = tid; i < nq * a.buckets; i += 256)
+            for (int i = tid; i < nq * a.buckets; i += 256) {
                 biases[i] = kLog2e * (float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i];
+                out |= biases[i] == -kInf;
+            }
+        out = __any(out);
+        if (lane == 0) wave_out[wave] = out;
         __syncthreads();
+        // Some biases are -infinity: their heads do not see the keys at these distances, whatever stands there.
+        const bool taken_out = __builtin_amdgcn_readfirstlane(wave_out[0] | wave_out[1] | wave_out[2] | wave_out[3]);
 
         f32x4 acc[NB];
 #pragma unroll
@@ -251,12 +259,18 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                 }
             }
             load_k(at(a.k, j0 + kUnit, id));
+            uint32_t odd = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int s = 64 * i + lane, row = s / P, piece = s % P;
                 u32x4 v = vreg[i];
                 if (VEC && D != a.D_v && piece * E >= a.D_v) v = u32x4{0u, 0u, 0u, 0u};
                 if (there != 0xffffffffu && !(there >> row & 1)) v = u32x4{0u, 0u, 0u, 0u};
+                if (taken_out) {
+                    const F f[1] = {__builtin_bit_cast(F, v)};
+                    const uint32_t o = O::top(f);
+                    odd = o > odd ? o : odd;
+                }
                 *reinterpret_cast<u32x4*>(tv + place<ES, P>(row, piece)) = v;
             }
             load_v(at(a.v, j0 + kUnit, id));
@@ -276,6 +290,38 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, far);
+            }
+            uint32_t sees = ~0u;  // keys of the tile, a bit each
+            if (taken_out) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        int far_by = n - 1 - (j0 + 16 * kb + 4 * kg + i);
+                        far_by = far_by < 0 ? 0 : (far_by < a.reach ? far_by : a.reach);
+                        if (biases[(ln < nq ? ln : 0) * a.buckets + buckets[far_by]] == -kInf)
+                            x[kb][i] = -kInf, sees &= ~(1u << (16 * kb + 4 * kg + i));
+                    }
+                sees &= __shfl_xor(sees, 16);
+                sees &= __shfl_xor(sees, 32);
+                odd = __any(odd >= O::kInf);
+                // (rare) infinities and NaN leave the tile: a product would take them to the heads that do not see
+                // them as well, 0 times infinity
+                asm volatile("" ::: "memory");
+#pragma unroll 1
+                for (int d = lane; odd && d < D; d += 64) {
+                    uint32_t pos = 0, neg = 0;
+#pragma unroll 1
+                    for (int row = 0; row < kKeys; ++row) {
+                        IO* const y = reinterpret_cast<IO*>(tv + place<ES, P>(row, d / E) + d % E * ES);
+                        const float f = (float)*y;
+                        if (fabsf(f) < kInf) continue;
+                        if (!(f < 0.0f)) pos |= 1u << row;
+                        if (!(f > 0.0f)) neg |= 1u << row;
+                        *y = (IO)0.0f;
+                    }
+                    found[wave][0][d] = (int)pos, found[wave][1][d] = (int)neg;
+                }
             }
             float mx = -kInf;
 #pragma unroll
@@ -328,6 +374,16 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                         O::mma(acc[cb], v, x[kb]);
                     }
             }
+            if (taken_out && odd)  // and join those that do
+#pragma unroll
+                for (int cb = 0; cb < NB; ++cb) {
+                    asm volatile("" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[cb][i] += found[wave][0][16 * cb + 4 * kg + i] & (int)sees ? kInf : 0.0f;
+                        acc[cb][i] += found[wave][1][16 * cb + 4 * kg + i] & (int)sees ? -kInf : 0.0f;
+                    }
+                }
             asm volatile("" ::: "memory");
             there = next;
         }
