@@ -118,41 +118,49 @@ struct ColumnFrags {
 
 // What the products with finite operands left out of acc: the infinities and NaN of a block of 32 rows
 // of a tile.  (A product would spread those in unseen rows as well: 0 times infinity.)  `sees`: the rows
-// that the lane's row sees, a bit each; `found` takes for each column the rows of +infinity or NaN, and
-// behind them those of -infinity or NaN.  nan: any is a NaN at once (it multiplies factors that may be 0).
-// Rare, and held to few registers.
+// that the lane's row sees, a bit each.  Of 32 columns, a lane finds the rows of +infinity or NaN in one, or
+// (upper half) of -infinity or NaN.  nan: any is a NaN at once (it multiplies factors that may be 0).  Rare,
+// and held to few registers; no LDS of its own (4 KB more left one workgroup a CU of two in dq_kernel at 128
+// numbers a head, reach 128: 152 us for 111).
 template <class C, typename IO>
-__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, uint32_t sees, bool nan, int* found) {
-    const int lane = (int)threadIdx.x & 63, h = lane >> 5;
-    typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void add_odd_numbers(f32x16 (&acc)[C::DB], const char* tile, uint32_t sees, bool nan) {
+    int lane = (int)threadIdx.x & 63;
+    asm volatile("" : "+v"(lane)::"memory");  // (addresses are made here, not kept from the kernel's start on)
+    const float sign = lane >> 5 ? -1.0f : 1.0f;
+    uint32_t met[C::DB] = {};
 #pragma unroll 1
-    for (int d = lane; d < C::D; d += 64) {
-        uint32_t pos = 0, neg = 0;
-#pragma unroll 1
-        for (int row = 0; row < 32; ++row) {
+    for (int row = 0; row < 32; ++row)
+#pragma unroll
+        for (int cb = 0; cb < C::DB; ++cb) {
+            const int d = 32 * cb + (lane & 31);
             const float x = (float)*reinterpret_cast<const IO*>(tile + place<C::ES, C::P>(row, d / C::E) + d % C::E * C::ES);
-            if (fabsf(x) < kInf) continue;
-            if (nan || !(x < 0.0f)) pos |= 1u << row;
-            if (nan || !(x > 0.0f)) neg |= 1u << row;
+            if (!(fabsf(x) < kInf) && (nan || !(x * sign < 0.0f))) met[cb] |= 1u << row;
         }
-        found[d] = (int)pos, found[C::D + d] = (int)neg;
-    }
-    // (the wave's own numbers: its LDS instructions come in order)
+    const int from = (lane >> 5) * 16;
 #pragma unroll
     for (int cb = 0; cb < C::DB; ++cb)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            asm volatile("" ::: "memory");
-            const i32x4 p = *reinterpret_cast<const i32x4*>(found + 32 * cb + 8 * g + 4 * h);
-            const i32x4 n = *reinterpret_cast<const i32x4*>(found + C::D + 32 * cb + 8 * g + 4 * h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc[cb][4 * g + e] += p[e] & (int)sees ? kInf : 0.0f;
-                acc[cb][4 * g + e] += n[e] & (int)sees ? -kInf : 0.0f;
-            }
+        for (int i = 0; i < 16; ++i) {
+            if (i % 4 == 0) asm volatile("" ::: "memory");
+            // column row_of(i) + 4 h's lanes
+            const int pos = __builtin_amdgcn_ds_bpermute(from + 4 * row_of(i), (int)met[cb]);
+            const int neg = __builtin_amdgcn_ds_bpermute(from + 4 * row_of(i) + 128, (int)met[cb]);
+            acc[cb][i] += pos & (int)sees ? kInf : 0.0f;
+            acc[cb][i] += neg & (int)sees ? -kInf : 0.0f;
         }
     asm volatile("" ::: "memory");
 }
+// N fragments with these as 0; odd: the largest number met, as O::top has it.
+template <typename O, typename F, int N>
+__device__ __forceinline__ void take_finite(F (&f)[N], uint32_t& odd) {
+    const uint32_t o = O::top(f);
+    odd = o > odd ? o : odd;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = O::finite(f[i]);
+}
+// Fragments read before such a look that is taken or not: their loads wait together, not one by one.
+template <bool ALWAYS>
+constexpr int kAtOnce = ALWAYS ? 1 : 2;
 // Bits 0 .. last (none below 0, all from 31 on).
 __device__ __forceinline__ uint32_t bits_to(int last) { return last >= 31 ? ~0u : (last < 0 ? 0u : (2u << last) - 1u); }
 // Bits of the 32 distances from d on, step apart, whose biases in tab are -infinity.
@@ -421,8 +429,9 @@ constexpr int kStages = 4 * C::TILE <= 80 * 1024 ? 2 : 1;
 
 // What work on a tile has to look at: every row sees all of it; some of its rows are not
 // there (zeros); some are there and not seen, so that no infinity of theirs may be multiplied.
-// (UNSEEN kernels look for those: causal ones, those with biases, which may take keys out, and
-// those for rows off 16 bytes, which are one for all calls.)
+// (UNSEEN kernels look for those: causal ones, and those for rows off 16 bytes, which are one
+// for all calls; others with biases do for a head whose biases take keys out: looking at all edges
+// took 31.7 us for 64 images, this 28.1.)
 constexpr int kWhole = 0, kPartial = 1, kUnseen = 2;
 template <int K>
 using Kind = std::integral_constant<int, K>;
@@ -491,7 +500,6 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
     using O = Op32<IO>;
     using F = typename O::F;
     __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
-    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
     extern __shared__ float tab[];  // with biases: fill_biases'
     const Place at = place_of(base, a.deal, true);
     if (at.head < 0) return;
@@ -610,23 +618,22 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
         uint32_t odd = 0;
 #pragma unroll
         for (int t = 0; t < C::NT; ++t)
+            static_for<0, (DB + kAtOnce<UNSEEN> - 1) / kAtOnce<UNSEEN>>([&](auto ic) {
+                constexpr int c0 = decltype(ic)::value * kAtOnce<UNSEEN>, n = DB - c0 < kAtOnce<UNSEEN> ? DB - c0 : kAtOnce<UNSEEN>;
+                F v[n];
 #pragma unroll
-            for (int cb = 0; cb < DB; ++cb) {
-                F v[1] = {cols.get(by, kb, t, cb)};
-                if constexpr (K == kUnseen) {
-                    const uint32_t o = O::top(v);
-                    odd = o > odd ? o : odd;
-                    v[0] = O::finite(v[0]);
-                }
-                O::mma(acc[cb], v[0], p[t]);
-            }
+                for (int c = 0; c < n; ++c) v[c] = cols.get(by, kb, t, c0 + c);
+                if (K == kUnseen && (UNSEEN || taken_out)) take_finite<O>(v, odd);
+#pragma unroll
+                for (int c = 0; c < n; ++c) O::mma(acc[c0 + c], v[c], p[t]);
+            });
         if (K == kUnseen && __any(odd >= O::kInf)) {
             uint32_t sees = bits_to(last - 32 * n);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - 32 * n, -1);
-            add_odd_numbers<C, IO>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), sees, false, found[wave]);
+            add_odd_numbers<C, IO>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), sees, false);
         }
     };
-    using Edge = Kind<UNSEEN ? kUnseen : kPartial>;
+    using Edge = Kind<UNSEEN || BIAS ? kUnseen : kPartial>;
     if constexpr (kStages<C> == 2) {
         // While a wave makes block n's probabilities, its matrix core has block n + 1's scores and
         // block n - 1's product to make: v follows k by a block, and a tile's v is there one visit
@@ -738,11 +745,11 @@ __device__ __forceinline__ void add_diagonals(const f32x16& x, float& near, floa
     });
 }
 
-// acc += w's 32 rows (of block b) times the columns of the tile at `at`; FINITE: odd numbers as
-// 0, odd the largest that was met.  fp32 sums a block on its own first: one long chain of roundings
+// acc += w's 32 rows (of block b) times the columns of the tile at `at`; FINITE and (ALWAYS or) look: odd
+// numbers as 0, odd the largest that was met.  fp32 sums a block on its own first: one long chain of roundings
 // left dq of 5590 tokens off by a relative 1.5e-6, 0.7e-6 so (and costs 3 % of packed training in fp32).
-template <typename C, typename O, bool FINITE, typename Columns, int DB>
-__device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& columns, int at, int b, const f32x16& w, uint32_t& odd) {
+template <typename C, typename O, bool FINITE, bool ALWAYS, typename Columns, int DB>
+__device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& columns, int at, int b, const f32x16& w, bool look, uint32_t& odd) {
     using F = typename O::F;
     auto packed = [&](int t) __attribute__((always_inline)) {
         float u[C::E];
@@ -750,28 +757,30 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& co
         for (int e = 0; e < C::E; ++e) u[e] = w[t * C::E + e];
         return O::pack(u);
     };
-    auto one = [&](f32x16& to, int t, int cb, const F& f) __attribute__((always_inline)) {
-        F g[1] = {columns.get(at, b, t, cb)};
-        if constexpr (FINITE) {
-            const uint32_t o = O::top(g);
-            odd = o > odd ? o : odd;
-            g[0] = O::finite(g[0]);
-        }
-        O::mma(to, g[0], f);
-    };
     if constexpr (C::E == 8) {
 #pragma unroll
         for (int t = 0; t < C::NT; ++t) {
             const F f = packed(t);
+            static_for<0, (DB + kAtOnce<ALWAYS> - 1) / kAtOnce<ALWAYS>>([&](auto ic) {
+                constexpr int c0 = decltype(ic)::value * kAtOnce<ALWAYS>, n = DB - c0 < kAtOnce<ALWAYS> ? DB - c0 : kAtOnce<ALWAYS>;
+                F g[n];
 #pragma unroll
-            for (int cb = 0; cb < DB; ++cb) one(acc[cb], t, cb, f);
+                for (int c = 0; c < n; ++c) g[c] = columns.get(at, b, t, c0 + c);
+                if (FINITE && (ALWAYS || look)) take_finite<O>(g, odd);
+#pragma unroll
+                for (int c = 0; c < n; ++c) O::mma(acc[c0 + c], g[c], f);
+            });
         }
     } else {
 #pragma unroll
         for (int cb = 0; cb < DB; ++cb) {
+            F g[C::NT];
+#pragma unroll
+            for (int t = 0; t < C::NT; ++t) g[t] = columns.get(at, b, t, cb);
+            if (FINITE && (ALWAYS || look)) take_finite<O>(g, odd);
             f32x16 sum{};
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t) one(sum, t, cb, packed(t));
+            for (int t = 0; t < C::NT; ++t) O::mma(sum, g[t], packed(t));
             acc[cb] += sum;
         }
     }
@@ -794,7 +803,6 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     using O = Op32<IO>;
     using F = typename O::F;
     __shared__ __attribute__((aligned(16))) char lds[kStages<C>][2 * C::TILE];
-    __shared__ __attribute__((aligned(16))) int found[4][2 * C::D];  // (add_odd_numbers)
     __shared__ float far_sums[BIAS ? 8 : 1];
     extern __shared__ float tab[];  // with biases: fill_biases', then [8][width] with their gradients
     const Place at = place_of(base, a.deal, true);
@@ -969,11 +977,11 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         const float f = hold<IO>(x, held, acc);
         if constexpr (std::is_same_v<IO, _Float16>) x[0] *= f;
         uint32_t odd = 0;
-        add_columns<C, O, K == kUnseen>(acc, kcols, by, kb, x[0], odd);
+        add_columns<C, O, K == kUnseen, UNSEEN>(acc, kcols, by, kb, x[0], taken_out, odd);
         if (K == kUnseen && __any(odd >= O::kInf)) {
             uint32_t sees = bits_to(last - j);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - j, -1);
-            add_odd_numbers<C, IO>(acc, lds[0] + by + kb * (32 * C::P * 16), sees, true, found[wave]);
+            add_odd_numbers<C, IO>(acc, lds[0] + by + kb * (32 * C::P * 16), sees, true);
         }
     };
     auto second = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
@@ -983,7 +991,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     };
     pass_over<C>(
         1, [&]() { return whole; }, visits, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
-        [&](int t, int stage) { second(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); }, [](int) {});
+        [&](int t, int stage) { second(Kind<UNSEEN || BIAS ? kUnseen : kPartial>{}, t, stage); }, [](int) {});
     if (n_rows > 0) {
         const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
         store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
@@ -1036,7 +1044,6 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
     using O = Op32<IO>;
     using F = typename O::F;
     __shared__ __attribute__((aligned(16))) char tiles_of[G][kStages<C>][2 * C::TILE];
-    __shared__ __attribute__((aligned(16))) int found[4 * G][2 * C::D];  // (add_odd_numbers)
     __shared__ __attribute__((aligned(16))) float stats_of[G][kStages<C>][2][kTile];  // lse, delta
     extern __shared__ float tab[];
     const Place place = place_of(base, a.kv_deal, false);
@@ -1157,14 +1164,14 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         if constexpr (DK && std::is_same_v<IO, _Float16>) ds[0] *= hold<IO>(ds, held, dk);
         if constexpr (DV && std::is_same_v<IO, _Float16>) p[0] *= 4096.0f;
         uint32_t odd = 0;
-        if constexpr (DV) add_columns<C, O, K == kUnseen>(dv, qcols, by + C::TILE, qb, p[0], odd);
-        if constexpr (DK) add_columns<C, O, K == kUnseen>(dk, qcols, by, qb, ds[0], odd);
+        if constexpr (DV) add_columns<C, O, K == kUnseen, UNSEEN>(dv, qcols, by + C::TILE, qb, p[0], taken_out, odd);
+        if constexpr (DK) add_columns<C, O, K == kUnseen, UNSEEN>(dk, qcols, by, qb, ds[0], taken_out, odd);
         if (K == kUnseen && __any(odd >= O::kInf)) {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
             uint32_t sees = bits_to(high) & ~bits_to(low - 1);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, q0 + shift - my, 1);
-            if constexpr (DV) add_odd_numbers<C, IO>(dv, t + C::TILE, sees, false, found[wave8]);
-            if constexpr (DK) add_odd_numbers<C, IO>(dk, t, sees, true, found[wave8]);
+            if constexpr (DV) add_odd_numbers<C, IO>(dv, t + C::TILE, sees, false);
+            if constexpr (DK) add_odd_numbers<C, IO>(dk, t, sees, true);
         }
     };
     auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
@@ -1182,7 +1189,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
             for (int qb = 0; qb < 2; ++qb)
                 if (n_rows > 0) block(Kind<kWhole>{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
         },
-        [&](int t, int stage) { edge(Kind<UNSEEN ? kUnseen : kPartial>{}, t, stage); },
+        [&](int t, int stage) { edge(Kind<UNSEEN || BIAS ? kUnseen : kPartial>{}, t, stage); },
         [&](int hh) {
             if (BIAS && hh + 1 < r) {  // the next head's biases, while its first tiles come
                 const BiasLanes next = load_biases<IO>(a, map, kv * r + hh + 1);
@@ -1273,9 +1280,8 @@ hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_
     return EQL_ATTENTION_DB(WHAT, 4);
 #define EQL_ATTENTION_DB(WHAT, DB)                                                                                            \
     !vec       ? WHAT<IO, DB, false, true, true>(a, map, stream)                                                              \
-    : bias     ? WHAT<IO, DB, true, true, true>(a, map, stream)                                                               \
-    : a.causal ? WHAT<IO, DB, true, false, true>(a, map, stream)                                                              \
-               : WHAT<IO, DB, true, false, false>(a, map, stream)
+    : a.causal ? (bias ? WHAT<IO, DB, true, true, true>(a, map, stream) : WHAT<IO, DB, true, false, true>(a, map, stream))    \
+               : (bias ? WHAT<IO, DB, true, true, false>(a, map, stream) : WHAT<IO, DB, true, false, false>(a, map, stream))
 
 template <typename IO>
 hipError_t forward(AttentionArgs a, const BucketMap& map, hipStream_t stream) {

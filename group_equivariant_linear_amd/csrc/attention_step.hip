@@ -73,7 +73,7 @@ __device__ __forceinline__ int units_of(int n) { return n > 0 ? (n + kUnit - 1) 
 // those with them.  Its four waves' sums are joined at the end of an item.  256 sequences of mean
 // 2048 tokens: 211 us, the keys and values at 5.0 TB/s (994 with an item to a workgroup); 8 sequences 13.3 us
 // and one of 131072 tokens 32.6, of which a workgroup's start and the chain table, keys, values is the most.
-template <typename IO, int DB, bool VEC>
+template <typename IO, int DB, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(StepArgs a, BucketMap map, Grid g, float* ws, uint32_t base) {
     using O = Op<IO>;
     using F = typename O::F;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
     __shared__ __attribute__((aligned(16))) char lds[4][kKeys * P * 16];
     __shared__ float ms[4][kQueries], ls[4][kQueries], all_top[kQueries], all_sum[kQueries];
     __shared__ int wave_units[4], wave_out[4];
-    __shared__ __attribute__((aligned(16))) int found[4][2][D];  // columns' keys of +infinity or NaN, of -infinity or NaN
+    __shared__ __attribute__((aligned(16))) int found[4][2][BIAS ? D : 1];  // columns' keys of +infinity or NaN, of -infinity or NaN
     extern __shared__ int shared[];  // units before each sequence, lengths; an item's biases; the buckets of distances
     const uint32_t wg = blockIdx.x + base;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4, ln = lane & 15;
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
     float* const biases = reinterpret_cast<float*>(shared + (g.shared ? 2 * a.batch + 1 : 0));
     uint8_t* const buckets = reinterpret_cast<uint8_t*>(biases + kQueries * a.buckets);
 
-    if (a.bias)  // each bucket marks its distances (the step is causal: all past ones are on the first side)
+    if (BIAS && a.bias)  // each bucket marks its distances (the step is causal: all past ones are on the first side)
         for (int i = tid; i < a.side; i += 256)
             for (int x = map.start[i]; x < map.start[i + 1]; ++x) buckets[x] = (uint8_t)i;
     int64_t u0, u1;
@@ -228,23 +228,24 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
         id = block_of(j_first + kUnit);
 
         bool out = false;
-        if (a.bias)
-            for (int i = tid; i < nq * a.buckets; i += 256) {
+        if constexpr (BIAS) {
+            for (int i = tid; a.bias && i < nq * a.buckets; i += 256) {
                 biases[i] = kLog2e * (float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i];
                 out |= biases[i] == -kInf;
             }
-        out = __any(out);
-        if (lane == 0) wave_out[wave] = out;
+            out = __any(out);
+            if (lane == 0) wave_out[wave] = out;
+        }
         __syncthreads();
         // Some biases are -infinity: their heads do not see the keys at these distances, whatever stands there.
-        const bool taken_out = __builtin_amdgcn_readfirstlane(wave_out[0] | wave_out[1] | wave_out[2] | wave_out[3]);
+        const bool taken_out = BIAS && __builtin_amdgcn_readfirstlane(wave_out[0] | wave_out[1] | wave_out[2] | wave_out[3]);
 
         f32x4 acc[NB];
 #pragma unroll
         for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         float top = -kInf, total = 0.0f;
         char* const tv = lds[wave];
-        const float far = a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.side - 1] : 0.0f;
+        const float far = BIAS && a.bias ? biases[(ln < nq ? ln : 0) * a.buckets + a.side - 1] : 0.0f;
         for (int j0 = j_first; j0 < k1; j0 += kUnit) {
             f32x4 x[2];
 #pragma unroll
@@ -259,24 +260,18 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                 }
             }
             load_k(at(a.k, j0 + kUnit, id));
-            uint32_t odd = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int s = 64 * i + lane, row = s / P, piece = s % P;
                 u32x4 v = vreg[i];
                 if (VEC && D != a.D_v && piece * E >= a.D_v) v = u32x4{0u, 0u, 0u, 0u};
                 if (there != 0xffffffffu && !(there >> row & 1)) v = u32x4{0u, 0u, 0u, 0u};
-                if (taken_out) {
-                    const F f[1] = {__builtin_bit_cast(F, v)};
-                    const uint32_t o = O::top(f);
-                    odd = o > odd ? o : odd;
-                }
                 *reinterpret_cast<u32x4*>(tv + place<ES, P>(row, piece)) = v;
             }
             load_v(at(a.v, j0 + kUnit, id));
             const uint32_t next = (uint32_t)__ballot(id >= 0 && id < a.blocks);
             id = block_of(j0 + 2 * kUnit);
-            if (a.bias && n - 1 - (j0 + kKeys - 1) < a.reach) {  // the tile's last key
+            if (BIAS && a.bias && n - 1 - (j0 + kKeys - 1) < a.reach) {  // the tile's last key
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -292,6 +287,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                     for (int i = 0; i < 4; ++i) x[kb][i] = __builtin_fmaf(x[kb][i], scale, far);
             }
             uint32_t sees = ~0u;  // keys of the tile, a bit each
+            bool odd = false;
             if (taken_out) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -304,10 +300,17 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                     }
                 sees &= __shfl_xor(sees, 16);
                 sees &= __shfl_xor(sees, 32);
-                odd = __any(odd >= O::kInf);
                 // (rare) infinities and NaN leave the tile: a product would take them to the heads that do not see
                 // them as well, 0 times infinity
                 asm volatile("" ::: "memory");
+                uint32_t largest = 0;
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const F f[1] = {*reinterpret_cast<const F*>(tv + (64 * i + lane) * 16)};
+                    const uint32_t o = O::top(f);
+                    largest = o > largest ? o : largest;
+                }
+                odd = __any(largest >= O::kInf);
 #pragma unroll 1
                 for (int d = lane; odd && d < D; d += 64) {
                     uint32_t pos = 0, neg = 0;
@@ -505,12 +508,12 @@ __global__ __launch_bounds__(kJoin) void join_kernel(StepArgs a, Grid g, const f
             sum == 0.0f ? -kInf : ((all == -kInf ? 0.0f : all) - att::kShift<IO> + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <typename IO, int DB, bool VEC>
+template <typename IO, int DB, bool VEC, bool BIAS>
 hipError_t run_cfg(const StepArgs& a, const BucketMap& map, float* ws, hipStream_t stream) {
     const Grid g = grid_for(sizeof(IO), a.heads, a.kv_heads, a.D_k, a.D_v, a.batch);
     const size_t lds = (g.shared ? (size_t)(2 * a.batch + 1) * 4 : 0) + (a.bias ? (size_t)kQueries * a.buckets * 4 + a.reach + 1 : 0);
     in_pieces(g.wgs, 256, [&](uint32_t base, uint32_t wgs) {
-        hipLaunchKernelGGL((step_kernel<IO, DB, VEC>), dim3(wgs), dim3(256), lds, stream, a, map, g, ws, base);
+        hipLaunchKernelGGL((step_kernel<IO, DB, VEC, BIAS>), dim3(wgs), dim3(256), lds, stream, a, map, g, ws, base);
     });
     if (g.shared) {
         // many rows: few parts each (on average); few: many
@@ -532,7 +535,9 @@ hipError_t run(StepArgs a, const BucketMap& map, float* ws, hipStream_t stream) 
     };
     const bool v = vec(a.k, a.D_k) && vec(a.v, a.D_v);
     const int db = ((a.D_k > a.D_v ? a.D_k : a.D_v) + 31) / 32;
-#define EQL_STEP(DB) v ? run_cfg<IO, DB, true>(a, map, ws, stream) : run_cfg<IO, DB, false>(a, map, ws, stream)
+#define EQL_STEP(DB)                                                                                               \
+    !v       ? run_cfg<IO, DB, false, true>(a, map, ws, stream)                                                    \
+    : a.bias ? run_cfg<IO, DB, true, true>(a, map, ws, stream) : run_cfg<IO, DB, true, false>(a, map, ws, stream)
     if (db == 1) return EQL_STEP(1);
     if (db == 2) return EQL_STEP(2);
     if (db == 3) return EQL_STEP(3);
