@@ -270,6 +270,12 @@ struct BiasLanes {  // of buckets b0 + lane
     int start, next;
     float before, after;
 };
+// A bias in powers of two; a finite one stays finite (from 2.36e38 on its product is past fp32's largest number).
+__device__ __forceinline__ float in_powers(float bias) {
+    constexpr float most = 0x1.fffffep127f;
+    const float y = kLog2e * bias;
+    return fabsf(bias) < kInf ? fminf(fmaxf(y, -most), most) : y;
+}
 template <typename IO>
 __device__ __forceinline__ BiasLanes load_biases(const AttentionArgs& a, const BucketMap& map, int head, int b0 = 0) {
     const int side = a.causal ? a.buckets : a.buckets / 2, b = b0 + ((int)threadIdx.x & 63);
@@ -277,7 +283,7 @@ __device__ __forceinline__ BiasLanes load_biases(const AttentionArgs& a, const B
     if (b < side) {
         x.start = map.start[b], x.next = map.start[b + 1];
         const IO* const row = (const IO*)a.bias + (int64_t)head * a.buckets;
-        if (a.bias) x.before = kLog2e * (float)row[b], x.after = a.causal ? x.before : kLog2e * (float)row[side + b];
+        if (a.bias) x.before = in_powers((float)row[b]), x.after = a.causal ? x.before : in_powers((float)row[side + b]);
     }
     return x;
 }

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
         bool out = false;
         if constexpr (BIAS) {
             for (int i = tid; a.bias && i < nq * a.buckets; i += 256) {
-                biases[i] = kLog2e * (float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i];
+                biases[i] = att::in_powers((float)((const IO*)a.bias)[(int64_t)head0 * a.buckets + i]);
                 out |= biases[i] == -kInf;
             }
             out = __any(out);

@@ -628,8 +628,9 @@ size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_k
  *   q [T][heads][d_k][N], k [T_kv][kv_heads][d_k][N], v [T_kv][kv_heads][d_v][N],
  *   o [T][heads][d_v][N]
  *   scale     of size 2^-100 to 2^100
- *   bias      [heads][buckets], plan dtype, element-aligned, or NULL; -infinity (and what
- *             log2(e) times overflows to it, such as the lowest fp32) takes keys out
+ *   bias      [heads][buckets], plan dtype, element-aligned, or NULL; -infinity takes keys
+ *             out: the query does not see them.  Finite ones past 2.35e38 in size (fp32's
+ *             and bf16's lowest among them) count as that number
  *   offsets, kv_offsets  batch + 1 each, of the queries and of the keys (they may be the
  *             same array); NULL: equal lengths T / batch, T_kv / batch
  *   lse       fp32 [heads][T], for the backward or to join attention over several sets of
