@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
             }
             uint32_t sees = ~0u;  // keys of the tile, a bit each
             bool odd = false;
-            if (taken_out) {
+            if (taken_out) [[unlikely]] {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                         O::mma(acc[cb], v, x[kb]);
                     }
             }
-            if (taken_out && odd)  // and join those that do
+            if (taken_out && odd) [[unlikely]] {  // and join those that do
 #pragma unroll
                 for (int cb = 0; cb < NB; ++cb) {
                     asm volatile("" ::: "memory");
@@ -387,6 +387,7 @@ __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(S
                         acc[cb][i] += found[wave][1][16 * cb + 4 * kg + i] & (int)sees ? -kInf : 0.0f;
                     }
                 }
+            }
             asm volatile("" ::: "memory");
             there = next;
         }
