@@ -29,7 +29,11 @@ constexpr int kRows = 128;  // rows that a workgroup's four waves own
 constexpr int kTile = 64;   // rows of the tiles that they pass over
 constexpr int kPad = 96;    // a wave's rows and a tile span fewer distances than this
 constexpr float kInf = __builtin_inff();
-constexpr float kLeastLse = -0x1p20f;
+// Rows whose |lse| passes this are steep: fp32 holds lse, and scores less lse, to 2^-14 and worse, and to no fraction
+// from 2^24 on.  dq_kernel finds their largest score again, bit for bit, and probabilities are made from the
+// difference to it.  (16 bit: dkv_kernel's accumulators start at lse and are rounded at its size up to 8 times: 2^-11
+// of a probability at this one, a quarter of the operand's own rounding.)
+constexpr float kSteepLse = 1024.0f;
 
 template <typename IO>
 struct Op32 : Op<IO> {  // __bf16, _Float16
@@ -486,7 +490,9 @@ __device__ __forceinline__ int tiles(int rows) { return rows > 0 ? (rows + kTile
 
 // Waves per SIMD that the registers are held to.
 constexpr int forward_waves(int es, int db) { return es == 4 ? (db <= 2 ? 2 : 1) : (db == 1 ? 4 : (db == 2 ? 3 : 2)); }
-constexpr int dq_waves(int es, int db) { return es == 4 ? (db <= 2 ? 2 : 1) : (db == 1 ? 4 : (db == 2 ? 3 : 2)); }
+constexpr int dq_waves(int es, int db, bool alone) {  // alone: no biases, every key seen
+    return es == 4 ? (db <= 2 ? 2 : 1) : (db == 1 || (db == 2 && alone) ? 4 : (db == 2 ? 3 : 2));
+}
 constexpr int dkv_waves(int es, int db) { return es == 4 ? 2 : (db == 1 ? 3 : 2); }
 // Whether dk and dv are two launches, each with its own accumulators and the scores made twice:
 // both at once hold more numbers than 256 registers (at 128 numbers a head 2 x 128 in accumulators
@@ -574,7 +580,7 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
             // (the far ones share a value: no other way, which would part the products from it)
             const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
             t += far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h;
-            if (K != kWhole && taken_out) {
+            if (K != kWhole && taken_out) [[unlikely]] {
                 f32x16 none{};
                 biased_or_out<-1>(x, none, scale, t);
             } else {
@@ -629,11 +635,11 @@ __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_ke
                 F v[n];
 #pragma unroll
                 for (int c = 0; c < n; ++c) v[c] = cols.get(by, kb, t, c0 + c);
-                if (K == kUnseen && (UNSEEN || taken_out)) take_finite<O>(v, odd);
+                if (K == kUnseen && (UNSEEN || taken_out)) [[unlikely]] take_finite<O>(v, odd);
 #pragma unroll
                 for (int c = 0; c < n; ++c) O::mma(acc[c0 + c], v[c], p[t]);
             });
-        if (K == kUnseen && __any(odd >= O::kInf)) {
+        if (K == kUnseen && __any(odd >= O::kInf)) [[unlikely]] {
             uint32_t sees = bits_to(last - 32 * n);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - 32 * n, -1);
             add_odd_numbers<C, IO>(acc, lds[0] + C::TILE + by + kb * (32 * C::P * 16), sees, false);
@@ -772,7 +778,7 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& co
                 F g[n];
 #pragma unroll
                 for (int c = 0; c < n; ++c) g[c] = columns.get(at, b, t, c0 + c);
-                if (FINITE && (ALWAYS || look)) take_finite<O>(g, odd);
+                if (FINITE && (ALWAYS || look)) [[unlikely]] take_finite<O>(g, odd);
 #pragma unroll
                 for (int c = 0; c < n; ++c) O::mma(acc[c0 + c], g[c], f);
             });
@@ -783,7 +789,7 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& co
             F g[C::NT];
 #pragma unroll
             for (int t = 0; t < C::NT; ++t) g[t] = columns.get(at, b, t, cb);
-            if (FINITE && (ALWAYS || look)) take_finite<O>(g, odd);
+            if (FINITE && (ALWAYS || look)) [[unlikely]] take_finite<O>(g, odd);
             f32x16 sum{};
 #pragma unroll
             for (int t = 0; t < C::NT; ++t) O::mma(sum, g[t], packed(t));
@@ -796,15 +802,16 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[DB], const Columns& co
 // keys twice.  The first pass makes delta = sum P dP, as what d_o . o leaves of it: o is
 // rounded to the plan's type, and delta from it alone is off by that rounding, which dS (a
 // difference) shows twofold and the biases' fp32 gradients by 1e-3 of their size.  It also
-// takes lse's own rounding out of P (sum P = 1), and leaves both for dkv_kernel.  The second
-// makes dS.  Of the biases, dS is summed by distance: along the diagonals of a block in
+// takes lse's own rounding out of P (sum P = 1), and leaves both for dkv_kernel.  Steep rows (rare)
+// look for their largest score before it, with keys straight from memory, and leave that and 1 / sum P.
+// The second makes dS.  Of the biases, dS is summed by distance: along the diagonals of a block in
 // registers, then into an array for each half of each wave (its own: read, added to, written);
 // distances past the reach share a bucket on either side and are summed in registers.  (In
 // packed training on images the kernel took 370 us with one LDS atomic for each of a block's 16
 // accumulators, 124 with two for its diagonals, 107 so.)  A workgroup writes the
 // sums of its buckets; reduce_kernel joins those of a head.
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
-__global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
+__global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB, !BIAS && !UNSEEN)) void dq_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;
     using O = Op32<IO>;
     using F = typename O::F;
@@ -864,10 +871,10 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     load_rows<C, IO, F, VEC>(d_o, a.d_o, s.q0 + w0, head, n_rows, a.D_v);
     const bool real = (lane & 31) < n_rows;
     const int64_t row = (int64_t)head * a.T + s.q0 + my;
-    // In powers of two.  A row that sees nothing has probabilities of 0, and so has one whose every bias is a
-    // large negative number: fp32 holds that lse to no fraction, and exp(s - lse) may be anything.
-    float lse = real ? a.lse[row] : kInf, delta = 0.0f, left = 0.0f, ones = 0.0f;
-    lse = lse < kLeastLse ? kInf : lse * kLog2e;
+    // In powers of two.  A row that sees nothing has probabilities of 0.
+    float lse = real ? a.lse[row] : kInf, delta = 0.0f, left = 0.0f, ones = 0.0f, inv = 1.0f;
+    const bool steep = fabsf(lse) > kSteepLse && fabsf(lse) < kInf, some_steep = __any(steep);
+    lse = lse == -kInf ? kInf : lse * kLog2e;
     {
         F o[C::NS];
         load_rows<C, IO, F, VEC>(o, a.o, s.q0 + w0, head, n_rows, a.D_v);
@@ -879,6 +886,29 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     }
     if (a.scale < 0.0f) negate(q);
     arrive(q), arrive(d_o);
+    if constexpr (BIAS) lds_barrier();  // the biases are there
+    if (some_steep) [[unlikely]] {
+        float top = -kInf;
+#pragma unroll 1
+        for (int j = 0; j < wave_end; j += 32) {
+            F k[C::NS];
+            load_rows<C, IO, F, VEC>(k, a.k, s.k0 + j, kv, s.n_k - j, a.D_k);
+            f32x16 x{}, none{};
+#pragma unroll
+            for (int st = 0; st < C::NS; ++st) O::mma(x, k[st], q[st]);
+            if constexpr (BIAS) {
+                const int from = w0 + shift - j;
+                const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
+                biased_or_out<-1>(x, none, scale,
+                                  tab + a.reach + kPad + (far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = row_of(i) <= last - j - 4 * h ? fmaxf(top, x[i]) : top;
+        }
+        top = half_max(top);
+        if constexpr (!BIAS) top *= scale;
+        if (steep && top > -kInf) lse = top;
+    }
     // Probabilities and dP of 32 keys from j on, at block kb of the tiles at `by`; returns the keys taken
     // out (of a block at an edge), bit i of accumulator i.
     auto scores = [&](bool edge, f32x16& x, f32x16& dp, int j, int kb, int by) __attribute__((always_inline)) {
@@ -892,7 +922,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
             const int from = w0 + shift - j;  // distance of the wave's first row and the block's first key
             const float* t = tab + a.reach + kPad;
             const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
-            if (edge && taken_out) {
+            if (edge && taken_out) [[unlikely]] {
                 out = biased_or_out<-1>(x, dp, scale, t + (far ? (from > 0 ? a.reach + 31 : -a.reach) : from + (lane & 31) - 4 * h));
             } else if (far) {
                 const float f = t[from > 0 ? a.reach : -a.reach];
@@ -944,10 +974,15 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
     left += __shfl_xor(left, 32);
     if (ones != 0.0f) {
         delta += left / ones;
-        lse += __builtin_amdgcn_logf(ones);
+        if (some_steep) inv = 1.0f / ones;
+        else lse += __builtin_amdgcn_logf(ones);
     }
-    if (real && h == 0) a.row_lse[row] = -lse / scale, a.row_delta[row] = -delta;  // (as dkv_kernel takes them)
+    if (real && h == 0)  // (as dkv_kernel takes them; +infinity: see the others)
+        a.row_stats(kRowLse)[row] = some_steep && lse < kInf ? kInf : -lse / scale, a.row_stats(kRowDelta)[row] = -delta;
+    if (real && some_steep) a.row_stats(kRowTop)[row] = lse, a.row_stats(kRowInv)[row] = inv;
+    if (lane == 0) a.steep()[((int64_t)head * a.slots + slot) * 4 + wave] = some_steep;
 
+    const float delta_inv = delta * inv;
     auto block = [&](auto kind, int j, int kb, int by) __attribute__((always_inline)) {
         constexpr int K = decltype(kind)::value;
         f32x16 x[1], dp;
@@ -955,12 +990,14 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         const int lim = last - j - 4 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[0][i] *= dp[i] - delta;
+            // (1 / sum P of steep rows here, as d_bias adds rows up, or, without biases, at the end; else it is 1)
+            x[0][i] *= BIAS ? __builtin_fmaf(dp[i], inv, -delta_inv) : dp[i] - delta;
             if constexpr (K != kWhole) x[0][i] = row_of(i) <= lim ? x[0][i] : 0.0f;
         }
-        if (BIAS && K != kWhole && taken_out)
+        if (BIAS && K != kWhole && taken_out) [[unlikely]] {
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[0][i] = out >> i & 1 ? 0.0f : x[0][i];
+        }
         if constexpr (BIAS) {
             // (rows past the last query have probabilities of 0 and distances of their own: 0 times a NaN is no term)
             if (a.dbias && n_rows < 32)
@@ -984,7 +1021,7 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         if constexpr (std::is_same_v<IO, _Float16>) x[0] *= f;
         uint32_t odd = 0;
         add_columns<C, O, K == kUnseen, UNSEEN>(acc, kcols, by, kb, x[0], taken_out, odd);
-        if (K == kUnseen && __any(odd >= O::kInf)) {
+        if (K == kUnseen && __any(odd >= O::kInf)) [[unlikely]] {
             uint32_t sees = bits_to(last - j);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, my + shift - j, -1);
             add_odd_numbers<C, IO>(acc, lds[0] + by + kb * (32 * C::P * 16), sees, true);
@@ -999,7 +1036,13 @@ __global__ __launch_bounds__(256, dq_waves(sizeof(IO), DB)) void dq_kernel(Atten
         1, [&]() { return whole; }, visits, load, [&](int t, int stage) { second(Kind<kWhole>{}, t, stage); },
         [&](int t, int stage) { second(Kind<UNSEEN || BIAS ? kUnseen : kPartial>{}, t, stage); }, [](int) {});
     if (n_rows > 0) {
-        const float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
+        float m = std::is_same_v<IO, _Float16> ? a.scale * inverse_of_power(held) : a.scale;
+        if (!BIAS && some_steep) [[unlikely]] {
+            // (the lane's own store, found again: held in registers all along, it left a SIMD 3 waves of 4)
+            int own = lane & 31;
+            asm volatile("" : "+v"(own));
+            if (own < n_rows) m *= *(const volatile float*)(a.row_stats(kRowInv) + (int64_t)head * a.T + s.q0 + w0 + own);
+        }
         store_rows<C, IO>(acc, a.dq, s.q0 + w0, head, n_rows, a.D_k, m, a.dq_vec);
     }
     if constexpr (BIAS) {
@@ -1098,11 +1141,19 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         lq.run(a.q, s.q0 + i0, head, n, a.D_k, 0, wave, 4, lds[stage]);
         lg.run(a.d_o, s.q0 + i0, head, n, a.D_v, 0, wave, 4, lds[stage] + C::TILE);
         if (wave < 2) {
-            const float* from = (wave ? a.row_delta : a.row_lse) + (int64_t)head * a.T + s.q0 + i0;
+            const float* from = a.row_stats(wave ? kRowDelta : kRowLse) + (int64_t)head * a.T + s.q0 + i0;
             load_words_to_lds(resource(from, (uint32_t)n * 4), (uint32_t)lane * 4, stats[stage][wave]);
         }
     };
     start_pass<C>(n_visits, load);
+    // Whether some query of the sequence, of any of the heads, is steep: then no tile is whole.  (The marks of four
+    // heads' first 64 runs of rows are on their way beside the rest.)
+    const int runs = (s.n_q + 31) / 32;
+    const int* const marks =
+        a.steep() + ((int64_t)kv * r * a.slots + (a.offsets ? s.q0 / kRows + b : b * ((s.n_q + kRows - 1) / kRows))) * 4;
+    int mark[4];
+#pragma unroll
+    for (int hh = 0; hh < 4; ++hh) mark[hh] = hh < r && lane < runs ? marks[(int64_t)hh * a.slots * 4 + lane] : 0;
     F k[C::NS], v[C::NS];
     load_rows<C, IO, F, VEC>(k, a.k, s.k0 + w0, kv, n_rows, a.D_k);
     if constexpr (DK) load_rows<C, IO, F, VEC>(v, a.v, s.k0 + w0, kv, n_rows, a.D_v);
@@ -1111,12 +1162,17 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
     if (a.scale < 0.0f) negate(k);
     arrive(k);
     if constexpr (DK) arrive(v);
+    int some = mark[0] | mark[1] | mark[2] | mark[3];
+    for (int hh = 0; hh < r; ++hh)
+        for (int i = hh < 4 ? 64 + lane : lane; i < runs; i += 64) some |= marks[(int64_t)hh * a.slots * 4 + i];
+    const bool steep = __any(some);
     // Queries q0 .. q0 + 31, at block qb of the tiles at `by`.  In 16 bits their statistics are what the
     // accumulators start from: the products end in (score - lse) / scale and dP - delta.  fp32 adds them
     // behind the products, which would round at lse's size 16 D times (relative 1.2e-6 in dk at D = 48, 4e-7 so),
     // and so do blocks at an edge: dP is then dq_kernel's bit for bit, and a lone key's dS is 0.
-    auto block = [&](auto kind, int q0, int qb, int by, const float (&stat)[2][kTile]) __attribute__((always_inline)) {
+    auto block = [&](auto kind, auto of_steep, int q0, int qb, int by, const float (&stat)[2][kTile], int head) __attribute__((always_inline)) {
         constexpr int K = decltype(kind)::value;
+        constexpr bool STEEP = decltype(of_steep)::value;  // (from the scores alone, which are dq_kernel's bit for bit)
         const int low = a.causal ? my - shift - q0 : 0, high = s.n_q - 1 - q0;  // rows of the block that see the lane's key
         constexpr bool LATE = sizeof(IO) == 4 || K != kWhole;
         f32x16 x{}, dp{}, p[1], ds[1];
@@ -1128,7 +1184,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
                 const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[1][32 * qb + 8 * g + 4 * h]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[4 * g + e] += lse[e];
+                    if constexpr (!STEEP) x[4 * g + e] += lse[e];
                     if constexpr (DK) dp[4 * g + e] += delta[e];
                 }
             }
@@ -1144,7 +1200,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
             const int from = q0 + shift - w0;  // distance of the block's first row and the wave's first key
             const float* t = tab + a.reach + kPad;
             const bool far = from - 31 >= a.reach || from + 31 <= -a.reach;
-            if (K != kWhole && taken_out) {
+            if (K != kWhole && taken_out) [[unlikely]] {
                 out = biased_or_out<1>(x, dp, scale, t + (far ? (from > 0 ? a.reach : -a.reach - 31) : from - (lane & 31) + 4 * h));
             } else if (far) {
                 const float f = t[from > 0 ? a.reach : -a.reach];
@@ -1156,9 +1212,24 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
                 for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(x[i], scale, t[row_of(i)]);
             }
         }
+        if constexpr (STEEP) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                asm volatile("" ::: "memory");  // (rare: one row's numbers at a time)
+                const float l = stat[0][32 * qb + row_of(i) + 4 * h];
+                float top = -l * scale, inv = 1.0f;
+                if (l == kInf) {
+                    const int64_t row = (int64_t)head * a.T + s.q0 + q0 + row_of(i) + 4 * h;
+                    top = a.row_stats(kRowTop)[row], inv = a.row_stats(kRowInv)[row];
+                }
+                p[0][i] = inv * __builtin_amdgcn_exp2f(BIAS ? x[i] - top : __builtin_fmaf(x[i], scale, -top));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[0][i] = __builtin_amdgcn_exp2f(BIAS ? x[i] : x[i] * scale);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            p[0][i] = __builtin_amdgcn_exp2f(BIAS ? x[i] : x[i] * scale);
             if constexpr (DK) ds[0][i] = p[0][i] * dp[i];
             if constexpr (K != kWhole) {
                 const int at = row_of(i) + 4 * h;
@@ -1172,7 +1243,7 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
         uint32_t odd = 0;
         if constexpr (DV) add_columns<C, O, K == kUnseen, UNSEEN>(dv, qcols, by + C::TILE, qb, p[0], taken_out, odd);
         if constexpr (DK) add_columns<C, O, K == kUnseen, UNSEEN>(dk, qcols, by, qb, ds[0], taken_out, odd);
-        if (K == kUnseen && __any(odd >= O::kInf)) {
+        if (K == kUnseen && __any(odd >= O::kInf)) [[unlikely]] {
             const char* t = lds[0] + by + qb * (32 * C::P * 16);
             uint32_t sees = bits_to(high) & ~bits_to(low - 1);
             if (BIAS && taken_out) sees &= ~taken_out_of(tab, a.reach, q0 + shift - my, 1);
@@ -1180,29 +1251,36 @@ __global__ __launch_bounds__(256 * G, dkv_waves(sizeof(IO), DB)) void dkv_kernel
             if constexpr (DK) add_odd_numbers<C, IO>(dk, t, sees, true);
         }
     };
-    auto edge = [&](auto kind, int t, int stage) __attribute__((always_inline)) {
+    auto edge = [&](auto kind, auto of_steep, int t, int stage) __attribute__((always_inline)) {
 #pragma unroll
         for (int qb = 0; qb < 2; ++qb) {
             const int q0 = row_at(t) + 32 * qb;
             if (n_rows > 0 && G * (t % n_visits) + group < n_all && q0 < s.n_q && !(a.causal && q0 + 31 + shift < w0))
-                block(kind, q0, qb, stage * 2 * C::TILE, stats[stage]);
+                block(kind, of_steep, q0, qb, stage * 2 * C::TILE, stats[stage], kv * r + t / n_visits);
         }
     };
-    pass_over<C>(
-        r, [&]() { return taken_out ? 0 : n_whole / G; }, n_visits, load,
-        [&](int t, int stage) {
+    auto between = [&](int hh) {
+        if (BIAS && hh + 1 < r) {  // the next head's biases, while its first tiles come
+            const BiasLanes next = load_biases<IO>(a, map, kv * r + hh + 1);
+            __syncthreads();
+            taken_out = fill_biases<IO, 256 * G>(tab, next, a, map, kv * r + hh + 1);
+        }
+    };
+    using Edge = Kind<UNSEEN || BIAS ? kUnseen : kPartial>;
+    if (!steep) [[likely]]
+        pass_over<C>(
+            r, [&]() { return taken_out ? 0 : n_whole / G; }, n_visits, load,
+            [&](int t, int stage) {
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb)
-                if (n_rows > 0) block(Kind<kWhole>{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage]);
-        },
-        [&](int t, int stage) { edge(Kind<UNSEEN || BIAS ? kUnseen : kPartial>{}, t, stage); },
-        [&](int hh) {
-            if (BIAS && hh + 1 < r) {  // the next head's biases, while its first tiles come
-                const BiasLanes next = load_biases<IO>(a, map, kv * r + hh + 1);
-                __syncthreads();
-                taken_out = fill_biases<IO, 256 * G>(tab, next, a, map, kv * r + hh + 1);
-            }
-        });
+                for (int qb = 0; qb < 2; ++qb)
+                    if (n_rows > 0)
+                        block(Kind<kWhole>{}, std::false_type{}, row_at(t) + 32 * qb, qb, stage * 2 * C::TILE, stats[stage], 0);
+            },
+            [&](int t, int stage) { edge(Edge{}, std::false_type{}, t, stage); }, between);
+    else
+        pass_over<C>(
+            r, []() { return 0; }, n_visits, load, [](int, int) {},
+            [&](int t, int stage) { edge(Edge{}, std::true_type{}, t, stage); }, between);
     // The other group's sums, in LDS in the accumulators' order, 4 KB for a wave and 32 columns
     // (as many tiles as they are wide hold them).
     static_assert(G == 1 || (DK && DV ? 2 : 1) * DB * 4 * 4096 <= (int)sizeof(tiles_of), "the sums fit the tiles");

@@ -52,10 +52,11 @@ size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Rows' statistics, and the sums of each slot's buckets (packed sequences have the most slots).
+// Rows' statistics, marks of steep ones, and the sums of each slot's buckets (packed sequences have the most slots).
 size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, bool backward) {
     if (!backward || T <= 0) return 0;
-    return 2 * round_up((size_t)T * heads * 4) + (size_t)(T / kRows + batch) * heads * buckets * 4;
+    const size_t slots = (size_t)(T / kRows + batch) * heads;
+    return 4 * round_up((size_t)T * heads * 4) + round_up(slots * 16) + slots * buckets * 4;
 }
 
 hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipStream_t stream) {
@@ -68,11 +69,9 @@ hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipSt
 }
 
 hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& map, void* ws, hipStream_t stream) {
-    const size_t n = round_up((size_t)a.T * a.heads * 4);
-    a.row_lse = static_cast<float*>(ws);
-    a.row_delta = reinterpret_cast<float*>(static_cast<char*>(ws) + n);
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * n);
     a.slots = slots_for(a.offsets, a.batch, a.T);
+    a.rows = static_cast<float*>(ws);
+    a.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(a.steep()) + round_up((size_t)a.slots * a.heads * 16));
     a.deal = deal_for(a.offsets, a.batch, a.T, a.heads);
     a.kv_deal = deal_for(a.kv_offsets, a.batch, a.T_kv, a.kv_heads);
     if (a.deal.workgroups(a.heads) > 0x7fffffff || a.kv_deal.workgroups(a.kv_heads) > 0x7fffffff) return hipErrorNotSupported;

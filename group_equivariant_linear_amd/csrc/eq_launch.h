@@ -201,9 +201,16 @@ struct AttentionArgs {
     float* lse;
     Heads d_o, dq, dk, dv;  // backward
     float* dbias;
-    float *row_lse, *row_delta, *parts;  // workspace: -lse / |scale| and -delta of each row, sums of the biases' gradients
+    float *rows, *parts;  // workspace: row_stats and steep, sums of the biases' gradients
     int out_vec, dq_vec, dk_vec, dv_vec;  // rows of an output in whole pieces of four
+    // Numbers of every row of every head: -lse / |scale| and -delta; of steep rows (attention.h) the largest score in
+    // powers of two and 1 / sum P.  (Addresses from one: as arguments of their own they cost dq_kernel registers.)
+    __host__ __device__ int64_t all_rows() const { return ((int64_t)T * heads + 63) / 64 * 64; }
+    __host__ __device__ float* row_stats(int which) const { return rows + which * all_rows(); }
+    // Whether a run of 32 rows holds steep ones: [heads][slots][4].
+    __host__ __device__ int* steep() const { return reinterpret_cast<int*>(row_stats(4)); }
 };
+constexpr int kRowLse = 0, kRowDelta = 1, kRowTop = 2, kRowInv = 3;
 size_t attention_workspace(int heads, int buckets, int64_t T, int64_t batch, bool backward);
 hipError_t launch_attention(int io, AttentionArgs a, const BucketMap& map, hipStream_t stream);
 hipError_t launch_attention_backward(int io, AttentionArgs a, const BucketMap& map, void* ws, hipStream_t stream);

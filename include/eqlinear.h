@@ -657,8 +657,9 @@ eqlinear_status eqlinear_attention(eqlinear_plan_t plan, const eqlinear_heads* q
  * two that keep them within its range, so that gradients may be smaller or larger than fp16's
  * numbers as long as dq, dk and dv are not); d_bias sums dS in fp32, and o's rounding is taken
  * out of delta.  Rows of k and v that no query sees get zeros.  lse is fp32, so P is off by a
- * relative 2^-22 |lse|; rows whose lse is below -2^20 (every key under a large negative bias)
- * count as rows that see no key: their gradients are 0.  Asynchronous on stream, no allocation; deterministic. */
+ * relative 2^-22 |lse|; where |lse| passes 2^10 P is made from the row's largest score, found
+ * again, and is off by the rounding of the scores alone.  Asynchronous on stream, no
+ * allocation; deterministic. */
 eqlinear_status eqlinear_attention_backward(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_heads* k,
                                             const eqlinear_heads* v, const eqlinear_heads* o, const eqlinear_heads* d_o,
                                             const float* lse, float scale, const void* bias, const int64_t* offsets,
