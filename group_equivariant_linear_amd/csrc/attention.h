@@ -1354,7 +1354,8 @@ hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_
     return hipGetLastError();
 }
 
-// Rows off 16 bytes go number by number into the kernels with everything.
+// Rows off 16 bytes go number by number, causal or not into the same kernels.  (With biases or without as others do:
+// a score that a bias of 0 is added to is rounded at its size, one without only less its maximum.)
 #define EQL_ATTENTION(WHAT)                                       \
     const int db = ((a.D_k > a.D_v ? a.D_k : a.D_v) + 31) / 32;   \
     const bool bias = a.bias != nullptr;                          \
@@ -1363,7 +1364,7 @@ hipError_t backward_cfg(const AttentionArgs& a, const BucketMap& map, hipStream_
     if (db == 3) return EQL_ATTENTION_DB(WHAT, 3);                \
     return EQL_ATTENTION_DB(WHAT, 4);
 #define EQL_ATTENTION_DB(WHAT, DB)                                                                                            \
-    !vec       ? WHAT<IO, DB, false, true, true>(a, map, stream)                                                              \
+    !vec       ? (bias ? WHAT<IO, DB, false, true, true>(a, map, stream) : WHAT<IO, DB, false, false, true>(a, map, stream))  \
     : a.causal ? (bias ? WHAT<IO, DB, true, true, true>(a, map, stream) : WHAT<IO, DB, true, false, true>(a, map, stream))    \
                : (bias ? WHAT<IO, DB, true, true, false>(a, map, stream) : WHAT<IO, DB, true, false, false>(a, map, stream))
 

@@ -627,7 +627,8 @@ size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_k
  *   that query i sees of exp(s_ij),  o_i = sum P_ij v_j,  lse_i = log sum exp(s_ij)
  *   q [T][heads][d_k][N], k [T_kv][kv_heads][d_k][N], v [T_kv][kv_heads][d_v][N],
  *   o [T][heads][d_v][N]
- *   scale     of size 2^-100 to 2^100
+ *   scale     of size 2^-100 to 2^100.  scale q_i . k_j is for numbers below 2^23 in size:
+ *             from there on fp32 holds scores to no unit, and fp16 plans may give NaN
  *   bias      [heads][buckets], plan dtype, element-aligned, or NULL; -infinity takes keys
  *             out: the query does not see them.  Finite ones past 2.35e38 in size (fp32's
  *             and bf16's lowest among them) count as that number

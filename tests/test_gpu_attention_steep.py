@@ -49,7 +49,8 @@ def test_one_bias_for_all(eq, dt, number, zero, causal, lens, d):  # noqa: F811
 @pytest.mark.parametrize("power", [12, 16, 20])
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("causal,lens,d,layout", [(True, [90, 200], 8, "apart"), (False, [130], 4, "apart"), (True, [2200], 8, "apart"),
-                                                  (True, [150], 16, "apart"), (False, [2100], 16, "apart"), (True, [140], 8, "fused")])
+                                                  (True, [150], 16, "apart"), (False, [2100], 16, "apart"), (True, [140], 8, "fused"),
+                                                  (True, [140], 5, "odd"), (False, [90], 3, "odd")])
 def test_scores_that_share_a_large_number(eq, dt, power, sign, causal, lens, d, layout):  # noqa: F811
     """Scores of +-2^power and small multiples of 1/4: products of whole numbers below 2^24, exact in fp32."""
     import torch
