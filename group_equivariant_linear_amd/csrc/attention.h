@@ -503,9 +503,9 @@ constexpr bool dkv_apart(int es, int db) { return es == 4 ? db >= 2 : db >= 4; }
 // A wave's 32 queries pass over the keys once, with the running maximum and sum of each row; a block's
 // exponentials lie between the next block's scores and the last one's product, so that the matrix cores have
 // work beside them.  10 heads of 32768 causal tokens, 112 numbers each: 3.0 ms, 790 TFLOP/s of the seen pairs,
-// bound by the vector instructions of the exponentials and their packing (matrix cores 40 % busy).  64 images of
-// 197 tokens, 12 heads of 64: 27.6 us where 16.3 would move their bytes, bound by a workgroup's start and four
-// tiles of 1.5 us in turn.
+// bound by the vector instructions of the exponentials and their packing (7 for each matrix instruction; matrix
+// cores 47 % busy, vector ALUs 47 %).  64 images of 197 tokens, 12 heads of 64: 28.3 us where 16.3 would move their
+// bytes, bound by a workgroup's start and four tiles of 1.5 us in turn.
 template <typename IO, int DB, bool VEC, bool BIAS, bool UNSEEN>
 __global__ __launch_bounds__(256, forward_waves(sizeof(IO), DB)) void forward_kernel(AttentionArgs a, BucketMap map, uint32_t base) {
     using C = Shape<IO, DB>;

@@ -24,7 +24,9 @@ constexpr int kWorkgroups = 1024;  // at most
 // on the host).  An item inside one
 // workgroup is finished there; of one that spans several, each writes its part, at 2 w + 1 if
 // the item starts in w, else at 2 w, and join_kernel takes them in order.  With more sequences
-// each item is one workgroup's.
+// each item is one workgroup's: their lengths no longer fit beside the tiles, and there are enough
+// items to fill the card.  (12 heads on 4 of 128 numbers, bf16: 2048 sequences of 400 keys take 258 us
+// cut evenly, 2049 take 224, which need no join; with one of 32768 keys among sequences of 100, 163 and 447.)
 struct Grid {
     int groups, items;  // runs of the query heads of a kv head; items of a sequence
     int shared;
@@ -71,8 +73,8 @@ __device__ __forceinline__ int units_of(int n) { return n > 0 ? (n + kUnit - 1) 
 // memory, the values through an LDS tile of its own (read back transposed).  The next keys'
 // loads go out as soon as these have left their registers, and the blocks of the keys after
 // those with them.  Its four waves' sums are joined at the end of an item.  256 sequences of mean
-// 2048 tokens: 211 us, the keys and values at 5.0 TB/s (994 with an item to a workgroup); 8 sequences 13.3 us
-// and one of 131072 tokens 32.6, of which a workgroup's start and the chain table, keys, values is the most.
+// 2048 tokens: 210 us, the keys and values at 5.0 TB/s (994 with an item to a workgroup); 8 sequences 13.0 us
+// and one of 131072 tokens 30.8, of which a workgroup's start and the chain table, keys, values is the most.
 template <typename IO, int DB, bool VEC, bool BIAS>
 __global__ __launch_bounds__(256, step_waves(sizeof(IO), DB)) void step_kernel(StepArgs a, BucketMap map, Grid g, float* ws, uint32_t base) {
     using O = Op<IO>;

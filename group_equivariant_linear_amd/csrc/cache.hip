@@ -74,8 +74,11 @@ __device__ __forceinline__ void place_token(const TablesArgs& a, const Request* 
 }
 
 // One workgroup walks the requests: offsets of their new tokens, lengths, and where in the
-// free list their new blocks start.  Few requests and tokens (ALONE) are all its own: one launch
-// of 5 us instead of two of 4.5 and 2.5.
+// free list their new blocks start.  Few requests and tokens (ALONE) are all its own, in one launch
+// instead of two: 8.2 us a call for 10.8 with 64 requests of one token, 10.9 for 12.9 with 2048.  Its
+// waves place tokens slower than a launch of their own from about 3000 on (64 requests, in a graph:
+// 6.9 us for 8.5 with 2048 tokens, 8.0 for 8.3 with 48 each, 9.2 for 8.5 with 64, 13.5 for 8.6 with
+// 128), and 2048 requests' offsets and starts take 48 KB of LDS.
 constexpr int kAloneRequests = 2048, kAloneTokens = 2 * kScan;
 template <bool ALONE>
 __global__ __launch_bounds__(kScan) void requests_kernel(TablesArgs a, Request* ws) {

@@ -635,7 +635,8 @@ size_t eqlinear_attention_workspace(eqlinear_plan_t plan, int64_t T, int64_t T_k
  *   offsets, kv_offsets  batch + 1 each, of the queries and of the keys (they may be the
  *             same array); NULL: equal lengths T / batch, T_kv / batch
  *   lse       fp32 [heads][T], for the backward or to join attention over several sets of
- *             keys, or NULL
+ *             keys, or NULL.  The backward is of one call: it takes the lse and o of that
+ *             call, not joined ones
  * A query that sees no key (or whose every score is -infinity) has o = 0 and lse =
  * -infinity.  What a query does not see does not change its bits, NaN and infinities
  * included.  Tokens that belong to no sequence are neither read for others nor written.
@@ -688,9 +689,10 @@ size_t eqlinear_attention_step_workspace(eqlinear_plan_t plan, int64_t batch);
  *   lse       fp32 [heads][batch], or NULL
  * Keys of a block that the cache does not have (negative, or blocks and above) count as not
  * there; a sequence without keys has o = 0, lse = -infinity.  Entries past a sequence's
- * last block are not read.  Roundings as in eqlinear_attention.  A long sequence is split
- * over workgroups whose parts are joined in a fixed order.  max_blocks block_size at most
- * 2^30, and with up to 2048 sequences batch times it below 2^38 (EQL_ERR_UNSUPPORTED).
+ * last block are not read.  Roundings and biases as in eqlinear_attention.  Of up to 2048
+ * sequences a long one is split over workgroups whose parts are joined in a fixed order; of
+ * more, each (sequence, kv head) is one workgroup's.  max_blocks block_size at most 2^30, and
+ * with up to 2048 sequences batch times it below 2^38 (EQL_ERR_UNSUPPORTED).
  * Asynchronous on stream, no allocation; deterministic. */
 eqlinear_status eqlinear_attention_step(eqlinear_plan_t plan, const eqlinear_heads* q, const eqlinear_pages* k_cache,
                                         const eqlinear_pages* v_cache, int64_t blocks, int block_size, const int32_t* table,
