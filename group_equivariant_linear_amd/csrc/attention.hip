@@ -40,7 +40,7 @@ uint32_t slots_for(const int64_t* offsets, int64_t batch, int64_t T) {
     return (uint32_t)(offsets ? T / kRows + batch : batch * ((T / batch + kRows - 1) / kRows));
 }
 
-// Dealt are sequences of 16 slots and more.
+// Dealt are sequences of 16 slots and more, packed ones by their mean (their lengths are on the device).
 Deal deal_for(const int64_t* offsets, int64_t batch, int64_t T, int heads) {
     const uint32_t slots = slots_for(offsets, batch, T);
     if (slots == 0 || T / batch < 16 * kRows) return Deal{slots, 0, 0};

@@ -140,3 +140,35 @@ def test_a_large_number_beside_keys_taken_out(eq, dt, number, causal, lens, d): 
     p.bias.zero_()
     p.bias[:, gone] = -200.0
     p.check(f"{dt} {number}")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("with_dbias", [True, False])
+def test_captured_before_rows_are_steep(eq, dt, with_dbias):  # noqa: F811
+    """A graph of both directions, replayed as its rows turn steep and back, against eager calls on another stream."""
+    import torch
+    p, q = (Problem(eq, dt, 8, 3, 1, 8, 8, [100, 229], causal=True, buckets=8, reach=40, seed=13) for _ in range(2))
+    for x in (p, q):
+        x.dbias = x.dbias if with_dbias else None
+        x.ws = x.workspace(True)
+        x.forward()
+        x.backward(workspace=x.ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.forward()
+        p.backward(workspace=p.ws)
+    side = torch.cuda.Stream()
+    for number in (0.0, -5000.0, 3000.0, -60000.0, 0.0):
+        for x in (p, q):
+            x.bias[:2] = number
+            for t in x.outputs().values():
+                t.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        g.replay()
+        with torch.cuda.stream(side):
+            q.forward()
+            q.backward(workspace=q.ws)
+        torch.cuda.synchronize()
+        for n, t in p.outputs().items():
+            assert torch.equal(t, q.outputs()[n]), (n, number)
+            assert torch.isfinite(t.float()).all()
